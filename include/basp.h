@@ -430,6 +430,187 @@ basp_status basp_time_next_call(void *start_event, void *stop_event);
  */
 basp_status basp_stream_copy(void *dst, const void *src, uint64_t bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Index-driven re-layouts: experts and vocabulary
+ * ---------------------------------------------------------------------------
+ * Two more places of a transformer step move whole token rows between
+ * layouts, by an index that is data: the exchange with the experts of a
+ * mixture-of-experts layer (seq -> expert and back) and the lookup of token
+ * embeddings.  They are not part of the paper's method; they take the
+ * sequence-sharded activations of this library's boundary as they lie, all N
+ * virtual ranks in one allocation, rows of D channels.
+ *
+ * Experts.  T tokens choose K experts each out of E; slot s = t*K + k is token
+ * t's k-th choice, ids[s] its expert.  A slot whose id lies outside [0, E) is
+ * dropped.  A token may choose one expert twice.
+ *   counts[e]   kept slots with id e
+ *   offsets[e]  first row of expert e: offsets[0] = 0, offsets[e+1] =
+ *               offsets[e] + counts[e] rounded up to a multiple of align;
+ *               offsets[E] is the end of the last expert
+ *   pos[s]      row of slot s: offsets[ids[s]] + the number of earlier kept
+ *               slots with the same id (slot order is kept); -1 if dropped
+ *   order[r]    slot of row r, or -1: padding up to a multiple of align, and
+ *               every row from offsets[E] to max_rows
+ * The expert-sharded buffer is [max_rows][D], max_rows = T*K + min(E, T*K) *
+ * (align - 1) rounded down to a multiple of align, which holds whatever the
+ * ids are.  With the experts split evenly over N ranks, rank r's shard is the
+ * rows [offsets[r*E/N], offsets[(r+1)*E/N]).
+ *
+ * Vocabulary.  T tokens with an id each, a table [V][D].  An id outside [0, V)
+ * gives a row of zeros and takes no part in the gradient.
+ *
+ * Conventions in addition to those at the top of this file:
+ * - All buffers are dense.  ids are 4- or 8-byte signed integers (id_bytes);
+ *   pos, order, offsets and counts are int32.  Rows are bf16, fp16 or fp32.
+ * - Every pointer needs its element's alignment; ws 16 bytes (BASP_ERR_ALIGN).
+ * - Sums, products and weights are computed in fp32 whatever the type, in an
+ *   order that depends on the plan and the ids alone, and rounded once to the
+ *   output's type: the same inputs give the same bits.
+ * - What a dropped slot, a padding row or an ignored id points at is not read:
+ *   infinities and NaN there reach no output.
+ * - Every output is written whole, except that basp_embed_to_seq_grad with
+ *   accumulate leaves the rows without a token as they were.
+ * - pos and order are read back from the caller.  Entries outside [0,
+ *   max_rows) and [0, T*K) count as -1, so a damaged index cannot reach
+ *   memory outside the buffers; which values such a call writes inside them
+ *   is then unspecified.
+ * - ws is device memory of workspace_bytes bytes (0: may be NULL), owned by
+ *   the caller; nothing in it needs to be set and nothing is kept in it
+ *   between calls.  Calls that may run at the same time (other streams,
+ *   captured graphs replayed together) need a workspace each.
+ * - Calls can be captured into a HIP graph: they launch kernels only.
+ * - T = 0 touches no activations: the index is still written (counts and
+ *   offsets 0), and so is the gradient of the table (zeros, unless accumulate).
+ */
+typedef struct basp_expert_plan basp_expert_plan;
+
+typedef struct basp_expert_info {
+    int64_t T, D;
+    int32_t K, E, align, id_bytes, dtype, weight_dtype;
+    int64_t slots;           /* T*K                                            */
+    int64_t max_rows;        /* rows of the expert-sharded buffer              */
+    int64_t workspace_bytes; /* of basp_expert_sort and basp_route_to_expert   */
+} basp_expert_info;
+
+/*
+ * Create an expert plan.  Host only: no device call, no device memory.
+ *   T  tokens (>= 0)    K  choices of a token (>= 1)   E  experts (1 to 1024)
+ *   D  channels of a row (>= 1)      align  rows an expert starts at a multiple
+ *   of (1 to 65536)     id_bytes  4 or 8
+ *   dtype, weight_dtype  BASP_BF16, BASP_FP16 or BASP_FP32, each on its own
+ * Errors (NULL returned, code in basp_last_error()):
+ *   BASP_ERR_INVALID      an argument out of range or an unknown enum
+ *   BASP_ERR_UNSUPPORTED  E above 1024, align above 65536, a row of 2^30 bytes
+ *                         or more, or T*K or max_rows of 2^31 - 1 or more
+ */
+basp_expert_plan *basp_expert_plan_create(int64_t T, int K, int E, int64_t D, int align, int id_bytes,
+                                          basp_dtype dtype, basp_dtype weight_dtype);
+void basp_expert_plan_destroy(basp_expert_plan *plan); /* NULL is allowed */
+basp_status basp_expert_plan_query(const basp_expert_plan *plan, basp_expert_info *info);
+
+/*
+ * The index of a routing: pos [T][K], order [max_rows], offsets [E + 1] and
+ * counts [E] from ids [T][K].
+ */
+basp_status basp_expert_sort(const basp_expert_plan *plan, const void *ids, int32_t *pos, int32_t *order,
+                             int32_t *offsets, int32_t *counts, void *ws, void *stream);
+
+/*
+ * seq -> expert: out[r] = x[order[r] / K], zeros where order[r] is -1.
+ *   x [T][D], pos [T][K], order [max_rows], out [max_rows][D].
+ * pos and order are those of one basp_expert_sort.  The rows are copied bit
+ * for bit.  Also moves any other rows of the same tokens (recomputation).
+ */
+basp_status basp_seq_to_expert(const basp_expert_plan *plan, const void *x, const int32_t *pos,
+                               const int32_t *order, void *out, void *stream);
+
+/*
+ * basp_expert_sort and basp_seq_to_expert in one call and as few launches as
+ * the sizes allow (one for small calls).  Same outputs.
+ */
+basp_status basp_route_to_expert(const basp_expert_plan *plan, const void *x, const void *ids, int32_t *pos,
+                                 int32_t *order, int32_t *offsets, int32_t *counts, void *out, void *ws,
+                                 void *stream);
+
+/*
+ * Gradient of seq -> expert: dx[t] = sum over k of dout[pos[t][k]], k
+ * ascending; zeros for a token without a kept slot.
+ *   dout [max_rows][D], dx [T][D].
+ */
+basp_status basp_seq_to_expert_grad(const basp_expert_plan *plan, const void *dout, const int32_t *pos,
+                                    void *dx, void *stream);
+
+/*
+ * expert -> seq: out[t] = sum over k of weights[t][k] * rows[pos[t][k]], k
+ * ascending; zeros for a token without a kept slot.
+ *   rows [max_rows][D], weights [T][K], out [T][D].
+ */
+basp_status basp_expert_to_seq(const basp_expert_plan *plan, const void *rows, const int32_t *pos,
+                               const void *weights, void *out, void *stream);
+
+/*
+ * Gradient of expert -> seq:
+ *   drows[pos[t][k]] = weights[t][k] * dout[t], zeros in rows without a slot;
+ *   dweights[t][k] = sum over channels of dout[t] * rows[pos[t][k]], 0 if dropped.
+ *   dout [T][D], rows [max_rows][D], drows [max_rows][D], dweights [T][K] (of
+ *   weight_dtype).
+ */
+basp_status basp_expert_to_seq_grad(const basp_expert_plan *plan, const void *dout, const void *rows,
+                                    const int32_t *pos, const int32_t *order, const void *weights,
+                                    void *drows, void *dweights, void *stream);
+
+typedef struct basp_embed_plan basp_embed_plan;
+
+typedef struct basp_embed_info {
+    int64_t T, V, D, padding;
+    int32_t id_bytes, dtype, grad_dtype;
+    int64_t workspace_bytes; /* of basp_embed_to_seq_grad */
+} basp_embed_info;
+
+/*
+ * Create an embedding plan.  Host only: no device call, no device memory.
+ *   layout   the basp_plan whose sequence-sharded layout the rows take: ids
+ *            are in the order [B][S], rank r's shard of the activations is
+ *            [Bl][St][D].  Only its B, S and groups count; T must be B*S, and
+ *            the plan is not kept.  NULL: rows in the order of the ids.
+ *   T        tokens (>= 0)    V  rows of the table (>= 1)   D  channels (>= 1)
+ *   padding  a row that takes no part in the gradient, or -1
+ *   id_bytes 4 or 8
+ *   dtype    of the table and the activations, grad_dtype of the table's
+ *            gradient: BASP_BF16, BASP_FP16 or BASP_FP32, each on its own
+ * Errors (NULL returned, code in basp_last_error()):
+ *   BASP_ERR_INVALID      an argument out of range, an unknown enum, or T
+ *                         other than B*S
+ *   BASP_ERR_UNSUPPORTED  V above 2^30, D of 2^28 or more, T of 2^31 - 1 or
+ *                         more, or more than 2^25 pieces of 32 tokens and 64
+ *                         16-byte vectors of channels (1 TiB of activations)
+ */
+basp_embed_plan *basp_embed_plan_create(const basp_plan *layout, int64_t T, int64_t V, int64_t D,
+                                        int64_t padding, int id_bytes, basp_dtype dtype, basp_dtype grad_dtype);
+void basp_embed_plan_destroy(basp_embed_plan *plan); /* NULL is allowed */
+basp_status basp_embed_plan_query(const basp_embed_plan *plan, basp_embed_info *info);
+
+/*
+ * Lookup with scaling into the sequence-sharded layout: out[row(t)] = scale *
+ * table[ids[t]], zeros for an id outside [0, V).
+ *   ids [T], table [V][D], out [T][D].
+ */
+basp_status basp_embed_to_seq(const basp_embed_plan *plan, const void *ids, const void *table, float scale,
+                              void *out, void *stream);
+
+/*
+ * Gradient of the lookup: dtable[v] = scale * sum over the tokens with id v of
+ * dout[row(t)].  The tokens are sorted by id and summed in token order within
+ * fixed groups (fp32, the same bits on every run).
+ *   dout [T][D] (dtype), dtable [V][D] (grad_dtype).
+ *   accumulate  0: dtable is overwritten, zeros in rows without a token;
+ *               otherwise the sums are added to dtable (one rounding) and
+ *               rows without a token stay as they were.
+ */
+basp_status basp_embed_to_seq_grad(const basp_embed_plan *plan, const void *ids, const void *dout,
+                                   float scale, int accumulate, void *dtable, void *ws, void *stream);
+
 /* Status of the last call made by this thread, and a static description.
  * (Error reporting: not a step of the method.) */
 basp_status basp_last_error(void);

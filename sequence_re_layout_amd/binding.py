@@ -55,6 +55,23 @@ class basp_plan_info(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class basp_expert_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "D")] + [
+        (n, ctypes.c_int32) for n in ("K", "E", "align", "id_bytes", "dtype", "weight_dtype")] + [
+        (n, ctypes.c_int64) for n in ("slots", "max_rows", "workspace_bytes")]
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class basp_embed_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "V", "D", "padding")] + [
+        (n, ctypes.c_int32) for n in ("id_bytes", "dtype", "grad_dtype")] + [("workspace_bytes", ctypes.c_int64)]
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
 class basp_tuning(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "vectors_per_thread", "tile_tokens", "tile_heads", "cache_policy", "max_grid",
@@ -117,6 +134,34 @@ _lib.basp_time_next_call.argtypes = [_vp, _vp]
 _lib.basp_time_next_call.restype = _i32
 _lib.basp_stream_copy.argtypes = [_vp, _vp, ctypes.c_uint64, _vp]
 _lib.basp_stream_copy.restype = _i32
+_lib.basp_expert_plan_create.argtypes = [_i64, _i32, _i32, _i64, _i32, _i32, _i32, _i32]
+_lib.basp_expert_plan_create.restype = _plan_p
+_lib.basp_expert_plan_destroy.argtypes = [_plan_p]
+_lib.basp_expert_plan_destroy.restype = None
+_lib.basp_expert_plan_query.argtypes = [_plan_p, ctypes.POINTER(basp_expert_info)]
+_lib.basp_expert_plan_query.restype = _i32
+_lib.basp_expert_sort.argtypes = [_plan_p] + [_vp] * 7
+_lib.basp_expert_sort.restype = _i32
+_lib.basp_seq_to_expert.argtypes = [_plan_p] + [_vp] * 5
+_lib.basp_seq_to_expert.restype = _i32
+_lib.basp_route_to_expert.argtypes = [_plan_p] + [_vp] * 9
+_lib.basp_route_to_expert.restype = _i32
+_lib.basp_seq_to_expert_grad.argtypes = [_plan_p] + [_vp] * 4
+_lib.basp_seq_to_expert_grad.restype = _i32
+_lib.basp_expert_to_seq.argtypes = [_plan_p] + [_vp] * 5
+_lib.basp_expert_to_seq.restype = _i32
+_lib.basp_expert_to_seq_grad.argtypes = [_plan_p] + [_vp] * 8
+_lib.basp_expert_to_seq_grad.restype = _i32
+_lib.basp_embed_plan_create.argtypes = [_plan_p, _i64, _i64, _i64, _i64, _i32, _i32, _i32]
+_lib.basp_embed_plan_create.restype = _plan_p
+_lib.basp_embed_plan_destroy.argtypes = [_plan_p]
+_lib.basp_embed_plan_destroy.restype = None
+_lib.basp_embed_plan_query.argtypes = [_plan_p, ctypes.POINTER(basp_embed_info)]
+_lib.basp_embed_plan_query.restype = _i32
+_lib.basp_embed_to_seq.argtypes = [_plan_p, _vp, _vp, ctypes.c_float, _vp, _vp]
+_lib.basp_embed_to_seq.restype = _i32
+_lib.basp_embed_to_seq_grad.argtypes = [_plan_p, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp]
+_lib.basp_embed_to_seq_grad.restype = _i32
 _lib.basp_last_error.argtypes = []
 _lib.basp_last_error.restype = _i32
 _lib.basp_status_str.argtypes = [_i32]
@@ -372,3 +417,179 @@ def basp_stream_copy(dst, src, nbytes=None, stream=None) -> None:
             raise ValueError("%s holds fewer than %d bytes" % (name, nbytes))
     _check(_lib.basp_stream_copy(addr(dst, "dst"), addr(src, "src"), nbytes, _stream(stream)),
            "basp_stream_copy")
+
+
+# ------------------------------------------------ index-driven re-layouts --
+
+class ExpertPlan:
+    """Owner of a ``basp_expert_plan*``; destroyed with the object.  ``info``
+    holds the ``basp_expert_plan_query`` result as a dict."""
+
+    def __init__(self, handle: int):
+        self.handle = handle
+        self.info = i = basp_expert_plan_query(self)
+        dt, wt = _torch_dtype(i["dtype"]), _torch_dtype(i["weight_dtype"])
+        tokens, rows = i["T"] * i["D"], i["max_rows"] * i["D"]
+        i32 = torch.int32
+        # dtype and element count of every buffer, by its name in the calls
+        self.ids = (torch.int64 if i["id_bytes"] == 8 else i32, i["slots"])
+        self.pos, self.order = (i32, i["slots"]), (i32, i["max_rows"])
+        self.offsets, self.counts = (i32, i["E"] + 1), (i32, i["E"])
+        self.tokens, self.rows, self.weights = (dt, tokens), (dt, rows), (wt, i["slots"])
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _lib is not None:   # _lib is None during interpreter shutdown
+            _lib.basp_expert_plan_destroy(h)
+
+
+class EmbedPlan:
+    """Owner of a ``basp_embed_plan*``; destroyed with the object.  ``info``
+    holds the ``basp_embed_plan_query`` result as a dict."""
+
+    def __init__(self, handle: int):
+        self.handle = handle
+        self.info = i = basp_embed_plan_query(self)
+        dt = _torch_dtype(i["dtype"])
+        self.ids = (torch.int64 if i["id_bytes"] == 8 else torch.int32, i["T"])
+        self.tokens, self.table = (dt, i["T"] * i["D"]), (dt, i["V"] * i["D"])
+        self.grad = (_torch_dtype(i["grad_dtype"]), i["V"] * i["D"])
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _lib is not None:   # _lib is None during interpreter shutdown
+            _lib.basp_embed_plan_destroy(h)
+
+
+def _addr(x, of, name: str, device: int):
+    """Device address of a tensor of the dtype and element count ``of``, or an
+    int or None as is."""
+    if x is None or isinstance(x, int):
+        return x
+    dtype, numel = of
+    if x.dtype != dtype:
+        raise TypeError("%s: dtype %s, the plan needs %s" % (name, x.dtype, dtype))
+    if not x.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if x.get_device() != device:
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, x.device, device))
+    if not x.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if x.numel() != numel:
+        raise ValueError("%s holds %d elements, the plan needs %d" % (name, x.numel(), numel))
+    return x.data_ptr()
+
+
+def _ws_addr(ws, plan, device: int):
+    need = plan.info["workspace_bytes"]
+    if ws is None or isinstance(ws, int):
+        return ws
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous device tensor")
+    if ws.get_device() != device:
+        raise ValueError("ws is on %s, the current device is cuda:%d" % (ws.device, device))
+    if ws.numel() * ws.element_size() < need:
+        raise ValueError("ws holds %d bytes, the plan needs %d" % (ws.numel() * ws.element_size(), need))
+    return ws.data_ptr()
+
+
+def basp_expert_plan_create(T, K, E, D, align=1, id_bytes=8, dtype=BASP_BF16, weight_dtype=BASP_FP32) -> ExpertPlan:
+    h = _lib.basp_expert_plan_create(T, K, E, D, align, id_bytes, dtype, weight_dtype)
+    if not h:
+        raise BaspError(_lib.basp_last_error(), "basp_expert_plan_create")
+    return ExpertPlan(h)
+
+
+def basp_expert_plan_destroy(plan: ExpertPlan) -> None:
+    h, plan.handle = plan.handle, None
+    _lib.basp_expert_plan_destroy(h)
+
+
+def basp_expert_plan_query(plan: ExpertPlan) -> dict:
+    info = basp_expert_info()
+    _check(_lib.basp_expert_plan_query(plan.handle, ctypes.byref(info)), "basp_expert_plan_query")
+    return info.as_dict()
+
+
+def basp_expert_sort(plan: ExpertPlan, ids, pos, order, offsets, counts, ws, stream=None) -> None:
+    d = torch.cuda.current_device()
+    _check(_lib.basp_expert_sort(
+        plan.handle, _addr(ids, plan.ids, "ids", d), _addr(pos, plan.pos, "pos", d),
+        _addr(order, plan.order, "order", d), _addr(offsets, plan.offsets, "offsets", d),
+        _addr(counts, plan.counts, "counts", d), _ws_addr(ws, plan, d), _stream(stream)), "basp_expert_sort")
+
+
+def basp_seq_to_expert(plan: ExpertPlan, x, pos, order, out, stream=None) -> None:
+    d = torch.cuda.current_device()
+    _check(_lib.basp_seq_to_expert(
+        plan.handle, _addr(x, plan.tokens, "x", d), _addr(pos, plan.pos, "pos", d),
+        _addr(order, plan.order, "order", d), _addr(out, plan.rows, "out", d), _stream(stream)),
+        "basp_seq_to_expert")
+
+
+def basp_route_to_expert(plan: ExpertPlan, x, ids, pos, order, offsets, counts, out, ws, stream=None) -> None:
+    d = torch.cuda.current_device()
+    _check(_lib.basp_route_to_expert(
+        plan.handle, _addr(x, plan.tokens, "x", d), _addr(ids, plan.ids, "ids", d), _addr(pos, plan.pos, "pos", d),
+        _addr(order, plan.order, "order", d), _addr(offsets, plan.offsets, "offsets", d),
+        _addr(counts, plan.counts, "counts", d), _addr(out, plan.rows, "out", d), _ws_addr(ws, plan, d),
+        _stream(stream)), "basp_route_to_expert")
+
+
+def basp_seq_to_expert_grad(plan: ExpertPlan, dout, pos, dx, stream=None) -> None:
+    d = torch.cuda.current_device()
+    _check(_lib.basp_seq_to_expert_grad(
+        plan.handle, _addr(dout, plan.rows, "dout", d), _addr(pos, plan.pos, "pos", d),
+        _addr(dx, plan.tokens, "dx", d), _stream(stream)), "basp_seq_to_expert_grad")
+
+
+def basp_expert_to_seq(plan: ExpertPlan, rows, pos, weights, out, stream=None) -> None:
+    d = torch.cuda.current_device()
+    _check(_lib.basp_expert_to_seq(
+        plan.handle, _addr(rows, plan.rows, "rows", d), _addr(pos, plan.pos, "pos", d),
+        _addr(weights, plan.weights, "weights", d), _addr(out, plan.tokens, "out", d), _stream(stream)),
+        "basp_expert_to_seq")
+
+
+def basp_expert_to_seq_grad(plan: ExpertPlan, dout, rows, pos, order, weights, drows, dweights, stream=None) -> None:
+    d = torch.cuda.current_device()
+    _check(_lib.basp_expert_to_seq_grad(
+        plan.handle, _addr(dout, plan.tokens, "dout", d), _addr(rows, plan.rows, "rows", d),
+        _addr(pos, plan.pos, "pos", d), _addr(order, plan.order, "order", d),
+        _addr(weights, plan.weights, "weights", d), _addr(drows, plan.rows, "drows", d),
+        _addr(dweights, plan.weights, "dweights", d), _stream(stream)), "basp_expert_to_seq_grad")
+
+
+def basp_embed_plan_create(layout, T, V, D, padding=-1, id_bytes=8, dtype=BASP_BF16,
+                           grad_dtype=BASP_BF16) -> EmbedPlan:
+    """``layout``: the Plan whose sequence-sharded order the rows take, or None."""
+    h = _lib.basp_embed_plan_create(None if layout is None else layout.handle, T, V, D, padding, id_bytes, dtype,
+                                    grad_dtype)
+    if not h:
+        raise BaspError(_lib.basp_last_error(), "basp_embed_plan_create")
+    return EmbedPlan(h)
+
+
+def basp_embed_plan_destroy(plan: EmbedPlan) -> None:
+    h, plan.handle = plan.handle, None
+    _lib.basp_embed_plan_destroy(h)
+
+
+def basp_embed_plan_query(plan: EmbedPlan) -> dict:
+    info = basp_embed_info()
+    _check(_lib.basp_embed_plan_query(plan.handle, ctypes.byref(info)), "basp_embed_plan_query")
+    return info.as_dict()
+
+
+def basp_embed_to_seq(plan: EmbedPlan, ids, table, scale, out, stream=None) -> None:
+    d = torch.cuda.current_device()
+    _check(_lib.basp_embed_to_seq(
+        plan.handle, _addr(ids, plan.ids, "ids", d), _addr(table, plan.table, "table", d), scale,
+        _addr(out, plan.tokens, "out", d), _stream(stream)), "basp_embed_to_seq")
+
+
+def basp_embed_to_seq_grad(plan: EmbedPlan, ids, dout, scale, accumulate, dtable, ws, stream=None) -> None:
+    d = torch.cuda.current_device()
+    _check(_lib.basp_embed_to_seq_grad(
+        plan.handle, _addr(ids, plan.ids, "ids", d), _addr(dout, plan.tokens, "dout", d), scale, bool(accumulate),
+        _addr(dtable, plan.grad, "dtable", d), _ws_addr(ws, plan, d), _stream(stream)), "basp_embed_to_seq_grad")

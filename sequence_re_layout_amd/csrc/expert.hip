@@ -1,0 +1,566 @@
+// expert.hip -- tokens sorted by expert and back: the kernels and entry points
+// of the expert plans (basp.h, "Index-driven re-layouts").
+//
+// Every kernel but the sort moves rows of D channels and is bound by HBM: a
+// lane holds one 16-byte vector of a row, so that each row is read once and
+// written once, and the sums and products ride along in fp32 registers.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#define BASP_HD __host__ __device__
+#include "index_plan.hpp"
+#include "plan_internal.hpp"
+#include "rowvec.hpp"
+#include "runtime.hpp"
+#include "sort.hpp"
+
+namespace basp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kLaunchVectors = int64_t{1} << 30;   // vectors of one launch: 31-bit division, 32-bit grid
+
+struct SortDesc {
+    const void *ids;
+    int32_t *pos, *order, *offsets, *counts;
+    int32_t *hist;
+    int64_t slots, items;           // items: slots of one work-group
+    int32_t E, align, max_rows, wide_ids;
+};
+
+__device__ inline int expert_of(const void *ids, int64_t i, int E, int wide)
+{
+    const int64_t id = wide ? static_cast<const int64_t *>(ids)[i] : static_cast<const int32_t *>(ids)[i];
+    return id >= 0 && id < E ? int(id) : -1;
+}
+
+__global__ __launch_bounds__(kSortBlock) void expert_count_kernel(const SortDesc D)
+{
+    extern __shared__ int lds[];
+    const int64_t begin = blockIdx.x * D.items, end = begin + D.items < D.slots ? begin + D.items : D.slots;
+    sort_count<kSortWaves>(lds, begin, end, D.E, D.hist + int64_t{blockIdx.x} * D.E,
+                           [&](int64_t i) { return expert_of(D.ids, i, D.E, D.wide_ids); });
+}
+
+__global__ __launch_bounds__(kSortBlock) void expert_place_kernel(const SortDesc D)
+{
+    extern __shared__ int lds[];
+    const SortLds l = sort_lds(lds, kSortWaves, D.E);
+    const int group = blockIdx.x, groups = gridDim.x, tid = threadIdx.x;
+    const int64_t begin = group * D.items, end = begin + D.items < D.slots ? begin + D.items : D.slots;
+    const auto bin = [&](int64_t i) { return expert_of(D.ids, i, D.E, D.wide_ids); };
+    sort_place<kSortWaves>(l, begin, end, D.E, D.align, D.hist, groups, group, bin, [&](int64_t i, int, int at) {
+        D.pos[i] = at;
+        if (at < D.max_rows)
+            D.order[at] = int32_t(i);
+    });
+    for (int64_t i = begin + tid; i < end; i += kSortBlock)
+        if (bin(i) < 0)
+            D.pos[i] = -1;
+    // rows without a slot: the padding of this group's share of the experts,
+    // and its share of what lies behind the last one
+    for (int e = group; e < D.E; e += groups)
+        for (int r = l.start[e] + l.total[e] + tid; r < l.start[e + 1]; r += kSortBlock)
+            D.order[r] = -1;
+    for (int64_t r = l.start[D.E] + int64_t{group} * kSortBlock + tid; r < D.max_rows; r += int64_t{groups} * kSortBlock)
+        D.order[r] = -1;
+    if (group == 0) {
+        for (int e = tid; e < D.E; e += kSortBlock)
+            D.counts[e] = l.total[e];
+        for (int e = tid; e <= D.E; e += kSortBlock)
+            D.offsets[e] = l.start[e];
+    }
+}
+
+// Rows of `row` bytes in vectors of VW bytes, `per_row` of them each.
+struct MoveDesc {
+    const char *x;
+    char *out;
+    const int32_t *pos, *order;
+    int64_t nvec;                   // vectors of the tokens of this launch
+    uint32_t row;
+    FastDiv per_row;
+    int32_t K;
+    uint32_t max_rows, slots;
+    uint32_t move_groups;           // work-groups of the tokens; the others write zeros
+};
+
+// Rows without a slot are written by work-groups of their own, which look
+// through `order` 64 rows at a time.
+constexpr int kZeroRows = 64;
+constexpr int64_t kZeroGroups = 1 << 20;
+
+uint32_t zero_groups(const basp_expert_plan &p)
+{
+    return uint32_t(std::min<int64_t>(kZeroGroups, (p.max_rows + kZeroRows - 1) / kZeroRows));
+}
+
+// The share of work-group `group` of `groups`.
+__device__ inline void zero_rows(char *out, const int32_t *order, uint32_t group, uint32_t groups, uint32_t max_rows,
+                                 uint32_t slots, uint32_t row)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (uint32_t r0 = group * kZeroRows; r0 < max_rows; r0 += groups * kZeroRows) {
+        const uint32_t r = r0 + lane;
+        const bool none = r < max_rows && uint32_t(order[r]) >= slots;
+        uint64_t m = __ballot(none);
+        for (int n = 0; m; ++n, m &= m - 1)
+            if (n % (kThreads / 64) == wave)
+                zero_row(out + uint64_t(r0 + __builtin_ctzll(m)) * row, row, lane);
+    }
+}
+
+// seq -> expert: each lane reads one vector of a token and writes it to the
+// rows of the token's slots.  UNI: a row is a whole number of waves, so the
+// token is the same for a wave and its index comes through scalar loads.
+template <int VW, bool UNI>
+__global__ __launch_bounds__(kThreads) void scatter_kernel(const MoveDesc D)
+{
+    if (blockIdx.x >= D.move_groups) {
+        zero_rows(D.out, D.order, blockIdx.x - D.move_groups, gridDim.x - D.move_groups, D.max_rows, D.slots, D.row);
+        return;
+    }
+    const uint32_t v = blockIdx.x * kThreads + threadIdx.x;
+    if (v >= D.nvec)
+        return;
+    uint32_t t = fastdiv(v, D.per_row);
+    if constexpr (UNI)
+        t = scalar(t);
+    const uint32_t off = vec_offset<VW>(v - t * D.per_row.d, D.row);
+    const auto x = load_vec<VW>(D.x + uint64_t(t) * D.row + off);
+    const int32_t *pos = D.pos + uint64_t(t) * D.K;
+    for (int k = 0; k < D.K; ++k) {
+        const uint32_t p = pos[k];
+        if (p < D.max_rows)
+            store_vec<VW>(D.out + uint64_t(p) * D.row + off, x);
+    }
+}
+
+struct SumDesc {
+    const char *rows;
+    char *out;
+    const int32_t *pos;
+    const void *weights;            // at the launch's first slot
+    int64_t nvec;
+    uint32_t row;
+    FastDiv per_row;
+    int32_t K;
+    uint32_t max_rows;
+    basp_dtype weight_dtype;
+};
+
+// expert -> seq and the gradient of seq -> expert: out[t] = sum over k of
+// (weights[t][k] *) rows[pos[t][k]] in fp32, k ascending.  KB loads are in
+// flight at a time; dropped slots are not read.
+template <typename E, int VW, int KB, bool WEIGHTED, bool UNI>
+__global__ __launch_bounds__(kThreads) void gather_sum_kernel(const SumDesc D)
+{
+    constexpr int N = VW / sizeof(E);
+    const uint32_t v = blockIdx.x * kThreads + threadIdx.x;
+    if (v >= D.nvec)
+        return;
+    uint32_t t = fastdiv(v, D.per_row);
+    if constexpr (UNI)
+        t = scalar(t);
+    const uint32_t off = vec_offset<VW>(v - t * D.per_row.d, D.row);
+    const uint64_t slot = uint64_t(t) * D.K;
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        acc[i] = 0.f;
+    for (int k0 = 0; k0 < D.K; k0 += KB) {
+        uint32_t p[KB];
+        float w[KB];
+        typename MemVec<VW>::type x[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            const bool in = k0 + j < D.K;
+            p[j] = in ? uint32_t(D.pos[slot + k0 + j]) : 0xffffffffu;
+            if constexpr (WEIGHTED)
+                w[j] = in ? load_number(D.weights, slot + k0 + j, D.weight_dtype) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+            if (p[j] < D.max_rows)
+                x[j] = load_vec<VW>(D.rows + uint64_t(p[j]) * D.row + off);
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+            if (p[j] < D.max_rows) {
+                float f[N];
+                unpack<E, VW>(x[j], f);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    acc[i] = WEIGHTED ? fmaf(w[j], f[i], acc[i]) : acc[i] + f[i];
+            }
+    }
+    store_vec<VW>(D.out + uint64_t(t) * D.row + off, pack<E, VW>(acc));
+}
+
+struct GradDesc {
+    const char *dout, *rows;
+    char *drows;
+    const int32_t *pos, *order;
+    const void *weights;
+    void *dweights;
+    uint32_t tokens, row, vecs;
+    int32_t K, lanes_log2;          // lanes that share a token
+    uint32_t max_rows, slots;
+    uint32_t token_groups;
+    basp_dtype weight_dtype;
+};
+
+// The gradient of expert -> seq.  2^lanes_log2 lanes (up to the whole work-
+// group) take a token: each reads its vectors of dout once, and per slot
+// reads the row's vector, adds the product to the slot's dot product and
+// writes the weighted dout.  The dot products are then summed over the lanes.
+template <typename E, int VW, int KB>
+__global__ __launch_bounds__(kThreads) void combine_grad_kernel(const GradDesc D)
+{
+    constexpr int N = VW / sizeof(E), WAVES = kThreads / 64;
+    __shared__ float part[WAVES][KB];
+    if (blockIdx.x >= D.token_groups) {
+        zero_rows(D.drows, D.order, blockIdx.x - D.token_groups, gridDim.x - D.token_groups, D.max_rows, D.slots,
+                  D.row);
+        return;
+    }
+    const uint32_t lanes = 1u << D.lanes_log2, lane = threadIdx.x & (lanes - 1);
+    const uint32_t t = blockIdx.x * (kThreads >> D.lanes_log2) + (threadIdx.x >> D.lanes_log2);
+    const bool live = t < D.tokens;
+    const uint64_t slot = uint64_t(t) * D.K;
+    const char *dout = D.dout + uint64_t(t) * D.row;
+    for (int k0 = 0; k0 < D.K; k0 += KB) {
+        uint32_t p[KB];
+        float w[KB], dot[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            const bool in = live && k0 + j < D.K;
+            p[j] = in ? uint32_t(D.pos[slot + k0 + j]) : 0xffffffffu;
+            w[j] = in ? load_number(D.weights, slot + k0 + j, D.weight_dtype) : 0.f;
+            dot[j] = 0.f;
+        }
+        for (uint32_t a = lane; live && a < D.vecs; a += lanes) {
+            const uint32_t off = vec_offset<VW>(a, D.row);
+            const uint32_t seen = (a * VW - off) / sizeof(E);   // elements the vector before holds too
+            float g[N];
+            unpack<E, VW>(load_vec<VW>(dout + off), g);
+            typename MemVec<VW>::type x[KB];
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+                if (p[j] < D.max_rows)
+                    x[j] = load_vec<VW>(D.rows + uint64_t(p[j]) * D.row + off);
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+                if (p[j] < D.max_rows) {
+                    float f[N], y[N];
+                    unpack<E, VW>(x[j], f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        dot[j] = uint32_t(i) < seen ? dot[j] : fmaf(g[i], f[i], dot[j]);
+                        y[i] = w[j] * g[i];
+                    }
+                    store_vec<VW>(D.drows + uint64_t(p[j]) * D.row + off, pack<E, VW>(y));
+                }
+        }
+        const uint32_t span = lanes < 64 ? lanes : 64;
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+            for (uint32_t d = 1; d < 64; d <<= 1) {
+                const float o = __shfl_xor(dot[j], d);
+                dot[j] += d < span ? o : 0.f;
+            }
+        if (lanes > 64) {
+            __syncthreads();           // the last batch's sums have been read
+            if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                for (int j = 0; j < KB; ++j)
+                    part[threadIdx.x >> 6][j] = dot[j];
+            __syncthreads();
+            const uint32_t w0 = (threadIdx.x >> D.lanes_log2) << (D.lanes_log2 - 6), nw = lanes >> 6;
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                dot[j] = 0.f;
+                for (uint32_t i = 0; i < nw; ++i)
+                    dot[j] += part[w0 + i][j];
+            }
+        }
+        if (lane == 0 && live)
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+                if (k0 + j < D.K)
+                    store_number(D.dweights, slot + k0 + j, D.weight_dtype, dot[j]);
+    }
+}
+
+// ------------------------------------------------------------- launches --
+
+basp_status launch_sort(const basp_expert_plan &p, const void *ids, int32_t *pos, int32_t *order, int32_t *offsets,
+                        int32_t *counts, void *ws, void *stream, bool last)
+{
+    const SortDesc D = {ids, pos, order, offsets, counts, static_cast<int32_t *>(ws), p.slots, p.block_items,
+                        p.E, p.align, int32_t(p.max_rows), p.id_bytes == 8};
+    const dim3 grid(p.sort_blocks);
+    basp_status s = BASP_OK;
+    if (p.sort_blocks > 1)
+        s = launch_kernel(reinterpret_cast<const void *>(expert_count_kernel), grid, kSortBlock, D, stream, true, false,
+                          size_t(4) * p.E);
+    if (s == BASP_OK)
+        s = launch_kernel(reinterpret_cast<const void *>(expert_place_kernel), grid, kSortBlock, D, stream,
+                          p.sort_blocks == 1, last, sort_lds_bytes(kSortWaves, p.E));
+    return s;
+}
+
+// f(token0, tokens, first, last) for launches of at most kLaunchVectors
+// vectors each.
+template <typename F>
+basp_status by_launch(int64_t T, int64_t per_row, F f)
+{
+    const int64_t step = std::max<int64_t>(1, kLaunchVectors / per_row);
+    basp_status s = BASP_OK;
+    for (int64_t t = 0; t < T && s == BASP_OK; t += step)
+        s = f(t, std::min(step, T - t), t == 0, t + step >= T);
+    return s;
+}
+
+uint32_t groups_of(int64_t n, int64_t per) { return uint32_t((n + per - 1) / per); }
+
+struct RowShape {
+    int vw;
+    int64_t row, vecs;
+};
+
+RowShape row_shape(const basp_expert_plan &p)
+{
+    RowShape r;
+    r.vw = row_vector(p.D, p.es);
+    r.row = p.D * p.es;
+    r.vecs = (r.row + r.vw - 1) / r.vw;
+    return r;
+}
+
+template <int VW>
+const void *scatter_fn(bool uni)
+{
+    return uni ? reinterpret_cast<const void *>(scatter_kernel<VW, true>)
+               : reinterpret_cast<const void *>(scatter_kernel<VW, false>);
+}
+
+template <typename E, int VW, int KB>
+const void *sum_fn(bool weighted, bool uni)
+{
+    if (weighted)
+        return uni ? reinterpret_cast<const void *>(gather_sum_kernel<E, VW, KB, true, true>)
+                   : reinterpret_cast<const void *>(gather_sum_kernel<E, VW, KB, true, false>);
+    return uni ? reinterpret_cast<const void *>(gather_sum_kernel<E, VW, KB, false, true>)
+               : reinterpret_cast<const void *>(gather_sum_kernel<E, VW, KB, false, false>);
+}
+
+template <typename E, int VW>
+const void *sum_fn(int K, bool weighted, bool uni)
+{
+    return K == 1   ? sum_fn<E, VW, 1>(weighted, uni)
+           : K == 2 ? sum_fn<E, VW, 2>(weighted, uni)
+           : K <= 4 ? sum_fn<E, VW, 4>(weighted, uni)
+                    : sum_fn<E, VW, 8>(weighted, uni);
+}
+
+template <typename E, int VW>
+const void *grad_fn(int K)
+{
+    return K == 1   ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 1>)
+           : K == 2 ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 2>)
+           : K <= 4 ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 4>)
+                    : reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 8>);
+}
+
+basp_status launch_scatter(const basp_expert_plan &p, const void *x, const int32_t *pos, const int32_t *order,
+                           void *out, void *stream, bool first_call)
+{
+    const RowShape r = row_shape(p);
+    const bool uni = r.vecs % 64 == 0;
+    const void *fn = r.vw == 16  ? scatter_fn<16>(uni)
+                     : r.vw == 8 ? scatter_fn<8>(uni)
+                     : r.vw == 4 ? scatter_fn<4>(uni)
+                                 : scatter_fn<2>(uni);
+    return by_launch(p.T, r.vecs, [&](int64_t t0, int64_t n, bool first, bool last) {
+        MoveDesc D = {};
+        D.x = static_cast<const char *>(x) + t0 * r.row;
+        D.out = static_cast<char *>(out);
+        D.pos = pos + t0 * p.K;
+        D.order = order;
+        D.nvec = n * r.vecs;
+        D.row = uint32_t(r.row);
+        D.per_row = make_fastdiv(uint32_t(r.vecs));
+        D.K = p.K;
+        D.max_rows = uint32_t(p.max_rows);
+        D.slots = uint32_t(p.slots);
+        D.move_groups = groups_of(D.nvec, kThreads);
+        const uint32_t zeros = last ? zero_groups(p) : 0;
+        return launch_kernel(fn, dim3(D.move_groups + zeros), kThreads, D, stream, first && first_call, last);
+    });
+}
+
+basp_status launch_sum(const basp_expert_plan &p, const void *rows, const int32_t *pos, const void *weights, void *out,
+                       void *stream)
+{
+    const RowShape r = row_shape(p);
+    const void *fn = BASP_BY_ROW(sum_fn, p.dtype, r.vw, p.K, weights != nullptr, r.vecs % 64 == 0);
+    return by_launch(p.T, r.vecs, [&](int64_t t0, int64_t n, bool first, bool last) {
+        SumDesc D = {};
+        D.rows = static_cast<const char *>(rows);
+        D.out = static_cast<char *>(out) + t0 * r.row;
+        D.pos = pos + t0 * p.K;
+        D.weights = weights ? static_cast<const char *>(weights) + t0 * p.K * p.ws_es : nullptr;
+        D.nvec = n * r.vecs;
+        D.row = uint32_t(r.row);
+        D.per_row = make_fastdiv(uint32_t(r.vecs));
+        D.K = p.K;
+        D.max_rows = uint32_t(p.max_rows);
+        D.weight_dtype = p.weight_dtype;
+        return launch_kernel(fn, dim3(groups_of(D.nvec, kThreads)), kThreads, D, stream, first, last);
+    });
+}
+
+basp_status launch_grad(const basp_expert_plan &p, const void *dout, const void *rows, const int32_t *pos,
+                        const int32_t *order, const void *weights, void *drows, void *dweights, void *stream)
+{
+    const RowShape r = row_shape(p);
+    const void *fn = BASP_BY_ROW(grad_fn, p.dtype, r.vw, p.K);
+    GradDesc D = {};
+    D.row = uint32_t(r.row);
+    D.vecs = uint32_t(r.vecs);
+    D.K = p.K;
+    D.max_rows = uint32_t(p.max_rows);
+    D.slots = uint32_t(p.slots);
+    D.weight_dtype = p.weight_dtype;
+    D.rows = static_cast<const char *>(rows);
+    D.drows = static_cast<char *>(drows);
+    D.order = order;
+    while (D.lanes_log2 < 8 && (int64_t{1} << D.lanes_log2) < r.vecs)
+        ++D.lanes_log2;
+    const int64_t per_group = kThreads >> D.lanes_log2, step = (int64_t{1} << 22) * per_group;
+    basp_status s = BASP_OK;
+    for (int64_t t0 = 0; t0 < p.T && s == BASP_OK; t0 += step) {
+        const int64_t n = std::min(step, p.T - t0);
+        const bool last = t0 + n == p.T;
+        D.dout = static_cast<const char *>(dout) + t0 * r.row;
+        D.pos = pos + t0 * p.K;
+        D.weights = static_cast<const char *>(weights) + t0 * p.K * p.ws_es;
+        D.dweights = static_cast<char *>(dweights) + t0 * p.K * p.ws_es;
+        D.tokens = uint32_t(n);
+        D.token_groups = groups_of(n, per_group);
+        const uint32_t zeros = last ? zero_groups(p) : 0;
+        s = launch_kernel(fn, dim3(D.token_groups + zeros), kThreads, D, stream, t0 == 0, last);
+    }
+    return s;
+}
+
+// ------------------------------------------------------------- the checks --
+
+struct ExpertBytes {
+    int64_t x, rows, pos, order, offsets, counts, ids, weights;
+};
+
+ExpertBytes bytes_of(const basp_expert_plan &p)
+{
+    return {p.T * p.D * p.es, p.max_rows * p.D * p.es, p.slots * 4, p.max_rows * 4, (int64_t{p.E} + 1) * 4,
+            int64_t{p.E} * 4, p.slots * p.id_bytes, p.slots * p.ws_es};
+}
+
+}  // namespace
+}  // namespace basp
+
+using basp::CallBuf;
+
+extern "C" basp_status basp_expert_sort(const basp_expert_plan *p, const void *ids, int32_t *pos, int32_t *order,
+                                        int32_t *offsets, int32_t *counts, void *ws, void *stream)
+{
+    return basp::timed_call([&]() -> basp_status {
+        if (!p)
+            return BASP_ERR_INVALID;
+        const basp::ExpertBytes n = basp::bytes_of(*p);
+        const CallBuf in[] = {{ids, n.ids, p->id_bytes}};
+        const CallBuf out[] = {{pos, n.pos, 4}, {order, n.order, 4}, {offsets, n.offsets, 4}, {counts, n.counts, 4},
+                               {ws, p->workspace_bytes, 16}};
+        const basp_status s = basp::check_call(in, 1, out, 5);
+        return s != BASP_OK ? s : basp::launch_sort(*p, ids, pos, order, offsets, counts, ws, stream, true);
+    });
+}
+
+extern "C" basp_status basp_seq_to_expert(const basp_expert_plan *p, const void *x, const int32_t *pos,
+                                          const int32_t *order, void *out, void *stream)
+{
+    return basp::timed_call([&]() -> basp_status {
+        if (!p)
+            return BASP_ERR_INVALID;
+        const basp::ExpertBytes n = basp::bytes_of(*p);
+        const CallBuf in[] = {{x, n.x, p->es}, {pos, n.pos, 4}, {order, n.order, 4}};
+        const CallBuf o[] = {{out, n.rows, p->es}};
+        const basp_status s = basp::check_call(in, 3, o, 1);
+        return s != BASP_OK ? s : basp::launch_scatter(*p, x, pos, order, out, stream, true);
+    });
+}
+
+extern "C" basp_status basp_route_to_expert(const basp_expert_plan *p, const void *x, const void *ids, int32_t *pos,
+                                            int32_t *order, int32_t *offsets, int32_t *counts, void *out, void *ws,
+                                            void *stream)
+{
+    return basp::timed_call([&]() -> basp_status {
+        if (!p)
+            return BASP_ERR_INVALID;
+        const basp::ExpertBytes n = basp::bytes_of(*p);
+        const CallBuf in[] = {{x, n.x, p->es}, {ids, n.ids, p->id_bytes}};
+        const CallBuf o[] = {{pos, n.pos, 4}, {order, n.order, 4}, {offsets, n.offsets, 4}, {counts, n.counts, 4},
+                             {out, n.rows, p->es}, {ws, p->workspace_bytes, 16}};
+        basp_status s = basp::check_call(in, 2, o, 6);
+        if (s == BASP_OK)
+            s = basp::launch_sort(*p, ids, pos, order, offsets, counts, ws, stream, p->T == 0);
+        return s != BASP_OK ? s : basp::launch_scatter(*p, x, pos, order, out, stream, false);
+    });
+}
+
+extern "C" basp_status basp_seq_to_expert_grad(const basp_expert_plan *p, const void *dout, const int32_t *pos,
+                                               void *dx, void *stream)
+{
+    return basp::timed_call([&]() -> basp_status {
+        if (!p)
+            return BASP_ERR_INVALID;
+        const basp::ExpertBytes n = basp::bytes_of(*p);
+        const CallBuf in[] = {{dout, n.rows, p->es}, {pos, n.pos, 4}};
+        const CallBuf o[] = {{dx, n.x, p->es}};
+        const basp_status s = basp::check_call(in, 2, o, 1);
+        return s != BASP_OK ? s : basp::launch_sum(*p, dout, pos, nullptr, dx, stream);
+    });
+}
+
+extern "C" basp_status basp_expert_to_seq(const basp_expert_plan *p, const void *rows, const int32_t *pos,
+                                          const void *weights, void *out, void *stream)
+{
+    return basp::timed_call([&]() -> basp_status {
+        if (!p)
+            return BASP_ERR_INVALID;
+        const basp::ExpertBytes n = basp::bytes_of(*p);
+        const CallBuf in[] = {{rows, n.rows, p->es}, {pos, n.pos, 4}, {weights, n.weights, p->ws_es}};
+        const CallBuf o[] = {{out, n.x, p->es}};
+        const basp_status s = basp::check_call(in, 3, o, 1);
+        return s != BASP_OK ? s : basp::launch_sum(*p, rows, pos, weights, out, stream);
+    });
+}
+
+extern "C" basp_status basp_expert_to_seq_grad(const basp_expert_plan *p, const void *dout, const void *rows,
+                                               const int32_t *pos, const int32_t *order, const void *weights,
+                                               void *drows, void *dweights, void *stream)
+{
+    return basp::timed_call([&]() -> basp_status {
+        if (!p)
+            return BASP_ERR_INVALID;
+        const basp::ExpertBytes n = basp::bytes_of(*p);
+        const CallBuf in[] = {{dout, n.x, p->es}, {rows, n.rows, p->es}, {pos, n.pos, 4}, {order, n.order, 4},
+                              {weights, n.weights, p->ws_es}};
+        const CallBuf o[] = {{drows, n.rows, p->es}, {dweights, n.weights, p->ws_es}};
+        const basp_status s = basp::check_call(in, 5, o, 2);
+        return s != BASP_OK ? s : basp::launch_grad(*p, dout, rows, pos, order, weights, drows, dweights, stream);
+    });
+}

@@ -14,8 +14,6 @@
 // descriptor, so they need no branch either.
 #include <hip/hip_runtime.h>
 
-#include <hip/hip_ext.h>
-
 #include <algorithm>
 #include <cstddef>
 #include <cstdint>
@@ -25,6 +23,7 @@
 #define BASP_HD __host__ __device__
 #include "launch.hpp"
 #include "plan_internal.hpp"
+#include "runtime.hpp"
 
 namespace basp {
 namespace {
@@ -373,30 +372,6 @@ TileFn tile_fn(const TileLaunch &L)
     }
 }
 
-// Events set by basp_time_next_call for the next call of this thread.
-struct Timing {
-    hipEvent_t start = nullptr, stop = nullptr;
-};
-thread_local Timing t_timing;
-
-// The launch's own status (not the thread's sticky last error, which other
-// code in the process may have left set).  first/last: this launch opens or
-// closes the current entry-point call, for the timing events.
-template <typename Desc>
-basp_status launch_kernel(const void *fn, dim3 grid, int block, const Desc &D, void *stream,
-                          bool first, bool last)
-{
-    void *args[] = {const_cast<Desc *>(&D)};
-    const hipStream_t st = static_cast<hipStream_t>(stream);
-    hipError_t e;
-    if (t_timing.start || t_timing.stop)
-        e = hipExtLaunchKernel(fn, grid, dim3(block), args, 0, st,
-                               first ? t_timing.start : nullptr, last ? t_timing.stop : nullptr, 0);
-    else
-        e = hipLaunchKernel(fn, grid, dim3(block), args, 0, st);
-    return e == hipSuccess ? BASP_OK : BASP_ERR_HIP;
-}
-
 basp_status launch(const TileLaunch &L, void *stream)
 {
     if (L.grid == 0)
@@ -418,15 +393,6 @@ basp_status launch(const PermLaunch &L, void *stream, bool first, bool last)
     default: fn = reinterpret_cast<const void *>(perm_kernel<2>); break;
     }
     return launch_kernel(fn, dim3(L.grid), kBlock, L.D, stream, first, last);
-}
-
-// Runs f, the body of an entry point, and clears the timing request after it.
-template <typename F>
-basp_status timed_call(F f)
-{
-    const basp_status s = f();
-    t_timing = Timing();
-    return record(s);
 }
 
 // ---------------------------------------------------------------- autotune --

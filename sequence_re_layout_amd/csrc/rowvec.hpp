@@ -1,0 +1,159 @@
+// rowvec.hpp -- device helpers of the kernels that move and sum token rows:
+// vectors of a row at any element-aligned address, their values in fp32, and
+// rows of zeros.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "index_plan.hpp"
+
+namespace basp {
+
+// Memory vectors are declared with the alignment of a 2-byte element: rows
+// need start on no 16-byte boundary, and the last vector of a row that is no
+// whole number of vectors starts anywhere.  Compute queues run in the
+// unaligned access mode, so these are still single instructions.
+typedef uint32_t u32x4m __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2m __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32m __attribute__((aligned(2)));
+template <int VW> struct MemVec;
+template <> struct MemVec<16> { typedef u32x4m type; };
+template <> struct MemVec<8> { typedef u32x2m type; };
+template <> struct MemVec<4> { typedef u32m type; };
+template <> struct MemVec<2> { typedef uint16_t type; };
+
+// NT: a line that is not expected to be reused.
+template <int VW, bool NT = true>
+__device__ inline typename MemVec<VW>::type load_vec(const char *p)
+{
+    typedef typename MemVec<VW>::type V;
+    if constexpr (NT)
+        return __builtin_nontemporal_load(reinterpret_cast<const V *>(p));
+    else
+        return *reinterpret_cast<const V *>(p);
+}
+
+template <int VW, bool NT = true>
+__device__ inline void store_vec(char *p, typename MemVec<VW>::type x)
+{
+    typedef typename MemVec<VW>::type V;
+    if constexpr (NT)
+        __builtin_nontemporal_store(x, reinterpret_cast<V *>(p));
+    else
+        *reinterpret_cast<V *>(p) = x;
+}
+
+// The values of a vector in fp32, and back with one rounding to nearest even.
+template <typename E, int VW>
+__device__ inline void unpack(typename MemVec<VW>::type x, float (&f)[VW / sizeof(E)])
+{
+    constexpr int N = VW / sizeof(E);
+    typedef E ev __attribute__((ext_vector_type(N)));
+    const ev v = __builtin_bit_cast(ev, x);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        f[i] = static_cast<float>(v[i]);
+}
+
+template <typename E, int VW>
+__device__ inline typename MemVec<VW>::type pack(const float (&f)[VW / sizeof(E)])
+{
+    constexpr int N = VW / sizeof(E);
+    typedef E ev __attribute__((ext_vector_type(N)));
+    ev v;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = static_cast<E>(f[i]);
+    typedef typename MemVec<VW>::type V;
+    return __builtin_bit_cast(V, v);
+}
+
+// N values of any type, in vectors of at most 16 bytes.
+template <typename E, int N>
+__device__ inline void store_values(char *p, const float (&f)[N])
+{
+    constexpr int VW = N * sizeof(E) > 16 ? 16 : N * sizeof(E), M = VW / sizeof(E);
+#pragma unroll
+    for (int i = 0; i < N; i += M) {
+        float part[M];
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+            part[j] = f[i + j];
+        store_vec<VW>(p + i * sizeof(E), pack<E, VW>(part));
+    }
+}
+
+template <typename E, int N>
+__device__ inline void load_values(const char *p, float (&f)[N])
+{
+    constexpr int VW = N * sizeof(E) > 16 ? 16 : N * sizeof(E), M = VW / sizeof(E);
+#pragma unroll
+    for (int i = 0; i < N; i += M) {
+        float part[M];
+        unpack<E, VW>(load_vec<VW>(p + i * sizeof(E)), part);
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+            f[i + j] = part[j];
+    }
+}
+
+// Byte offset of vector a of a row of `row` bytes: the last one ends with it.
+template <int VW>
+__device__ inline uint32_t vec_offset(uint32_t a, uint32_t row)
+{
+    const uint32_t off = a * VW, last = row - VW;
+    return off < last ? off : last;
+}
+
+// A row of zeros, written by the 64 lanes of a wave.
+__device__ inline void zero_row(char *p, uint32_t row, int lane)
+{
+    if (row >= 16) {
+        const u32x4m z = {0, 0, 0, 0};
+        for (uint32_t off = lane * 16; off < row; off += 64 * 16)
+            store_vec<16>(p + (off < row - 16 ? off : row - 16), z);
+    } else if (uint32_t(lane) * 2 < row) {
+        store_vec<2>(p + lane * 2, uint16_t(0));
+    }
+}
+
+// Lane-uniform values as scalars.
+__device__ inline uint32_t scalar(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// One number of 2 or 4 bytes (a router's weight) in fp32, and back.
+__device__ inline float load_number(const void *p, int64_t i, basp_dtype t)
+{
+    if (t == BASP_FP32)
+        return static_cast<const float *>(p)[i];
+    if (t == BASP_BF16)
+        return static_cast<float>(static_cast<const __bf16 *>(p)[i]);
+    return static_cast<float>(static_cast<const _Float16 *>(p)[i]);
+}
+
+__device__ inline void store_number(void *p, int64_t i, basp_dtype t, float x)
+{
+    if (t == BASP_FP32)
+        static_cast<float *>(p)[i] = x;
+    else if (t == BASP_BF16)
+        static_cast<__bf16 *>(p)[i] = static_cast<__bf16>(x);
+    else
+        static_cast<_Float16 *>(p)[i] = static_cast<_Float16>(x);
+}
+
+// fn<E, VW>(...) for a row type and vector width.
+#define BASP_BY_ROW(fn, dtype, vw, ...)                                                       \
+    ((dtype) == BASP_FP32   ? ((vw) == 16  ? fn<float, 16>(__VA_ARGS__)                       \
+                               : (vw) == 8 ? fn<float, 8>(__VA_ARGS__)                        \
+                                           : fn<float, 4>(__VA_ARGS__))                       \
+     : (dtype) == BASP_BF16 ? ((vw) == 16  ? fn<__bf16, 16>(__VA_ARGS__)                      \
+                               : (vw) == 8 ? fn<__bf16, 8>(__VA_ARGS__)                       \
+                               : (vw) == 4 ? fn<__bf16, 4>(__VA_ARGS__)                       \
+                                           : fn<__bf16, 2>(__VA_ARGS__))                      \
+                            : ((vw) == 16  ? fn<_Float16, 16>(__VA_ARGS__)                    \
+                               : (vw) == 8 ? fn<_Float16, 8>(__VA_ARGS__)                     \
+                               : (vw) == 4 ? fn<_Float16, 4>(__VA_ARGS__)                     \
+                                           : fn<_Float16, 2>(__VA_ARGS__)))
+
+}  // namespace basp
