@@ -330,10 +330,15 @@ def _ptr(x, plan: Plan, numel: int, name: str):
     return x.data_ptr() if numel else None
 
 
+# The current stream's handle on a device, without building a torch.cuda.Stream
+# for it, which takes longer than a small call (2.8 against 0.1 us).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -67,44 +67,134 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(const LookupDesc D)
     store_vec<VW>(D.out + uint64_t(seq_row(D.order, token)) * D.row + off, pack<E, VW>(f));
 }
 
+// ----------------------------------------------- rows that no token names --
+
+// While a token's id is first read, its number is left at tags[id].  A row of
+// the table has a token if and only if its tag is a token with that id,
+// whatever the tags held before and whichever token wrote last: no memory has
+// to be cleared for this, and no sorted list searched.
+struct ZeroDesc {
+    const void *ids;
+    uint32_t *tags;
+    char *dtable;
+    int64_t T, V, padding;
+    uint32_t begin, end;            // rows of this launch
+    uint32_t row;                   // bytes
+    int32_t wide_ids;
+};
+
+// The rows without a token in the share of work-group `group` of `groups` of
+// WAVES waves, as zeros.
+template <int WAVES>
+__device__ inline void zero_unnamed(const ZeroDesc &D, uint32_t group, uint32_t groups)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (uint32_t r0 = D.begin + group * 64; r0 < D.end; r0 += groups * 64) {
+        const uint32_t r = r0 + lane;
+        bool none = r < D.end;
+        if (none) {
+            const uint32_t t = D.T ? D.tags[r] : 0;
+            none = t >= D.T || row_of_id(D.ids, t, D.V, D.padding, D.wide_ids) != r;
+        }
+        uint64_t m = __ballot(none);
+        for (int n = 0; m; ++n, m &= m - 1)
+            if (n % WAVES == wave)
+                zero_row(D.dtable + uint64_t(r0 + __builtin_ctzll(m)) * D.row, D.row, lane);
+    }
+}
+
 // ------------------------------------------------------- tokens by their id --
 
-// One pass of the sort by id, least significant digit first.
+// One pass of the sort by id, least significant digit first.  The launches
+// of a pass are bound by latency and use a few work-groups; the others write
+// rows of zeros meanwhile, which is what the whole call spends most on where
+// the table is larger than the batch.
 struct PassDesc {
-    const void *ids;                // first pass: ids as given
     const uint32_t *keys_in, *tokens_in;
     uint32_t *keys_out, *tokens_out;
     int32_t *hist;
-    int64_t T, items, V, padding;
-    int32_t first, wide_ids, shift, bins;
+    int64_t items;
+    int32_t first, shift, bins;
+    int32_t groups;                 // work-groups of the pass
+    ZeroDesc zero;
 };
 
 __device__ inline uint32_t pass_key(const PassDesc &D, int64_t i)
 {
-    return D.first ? row_of_id(D.ids, i, D.V, D.padding, D.wide_ids) : D.keys_in[i];
+    return D.first ? row_of_id(D.zero.ids, i, D.zero.V, D.zero.padding, D.zero.wide_ids) : D.keys_in[i];
+}
+
+__device__ inline void pass_emit(const PassDesc &D, int64_t i, uint32_t key, int at)
+{
+    if (at >= 0 && at < D.zero.T) {
+        D.keys_out[at] = key;
+        D.tokens_out[at] = D.first ? uint32_t(i) : D.tokens_in[i];
+    }
 }
 
 __global__ __launch_bounds__(kSortBlock) void digit_count_kernel(const PassDesc D)
 {
     extern __shared__ int lds[];
-    const int64_t begin = blockIdx.x * D.items, end = begin + D.items < D.T ? begin + D.items : D.T;
-    sort_count<kSortWaves>(lds, begin, end, D.bins, D.hist + int64_t{blockIdx.x} * D.bins,
-                           [&](int64_t i) { return int(pass_key(D, i) >> D.shift) & (D.bins - 1); });
+    if (blockIdx.x >= uint32_t(D.groups)) {
+        zero_unnamed<kSortWaves>(D.zero, blockIdx.x - D.groups, gridDim.x - D.groups);
+        return;
+    }
+    const int64_t T = D.zero.T, begin = blockIdx.x * D.items, end = begin + D.items < T ? begin + D.items : T;
+    sort_count<kSortWaves>(lds, begin, end, D.bins, D.hist + int64_t{blockIdx.x} * D.bins, [&](int64_t i) {
+        const uint32_t key = pass_key(D, i);
+        if (D.first && key < D.zero.V)
+            D.zero.tags[key] = uint32_t(i);
+        return int(key >> D.shift) & (D.bins - 1);
+    });
 }
 
+template <int R>
 __global__ __launch_bounds__(kSortBlock) void digit_place_kernel(const PassDesc D)
 {
     extern __shared__ int lds[];
-    const int64_t begin = blockIdx.x * D.items, end = begin + D.items < D.T ? begin + D.items : D.T;
-    sort_place<kSortWaves>(
-        sort_lds(lds, kSortWaves, D.bins), begin, end, D.bins, 1, D.hist, gridDim.x, blockIdx.x,
-        [&](int64_t i) { return int(pass_key(D, i) >> D.shift) & (D.bins - 1); },
-        [&](int64_t i, int, int at) {
-            if (at < D.T) {
-                D.keys_out[at] = pass_key(D, i);
-                D.tokens_out[at] = D.first ? uint32_t(i) : D.tokens_in[i];
-            }
-        });
+    if (blockIdx.x >= uint32_t(D.groups)) {
+        zero_unnamed<kSortWaves>(D.zero, blockIdx.x - D.groups, gridDim.x - D.groups);
+        return;
+    }
+    const int64_t T = D.zero.T, begin = blockIdx.x * D.items, end = begin + D.items < T ? begin + D.items : T;
+    sort_place<kSortWaves, R>(
+        sort_lds(lds, kSortWaves, D.bins), begin, end, D.bins, 1, D.hist, D.groups, blockIdx.x,
+        [&](int64_t i) { return pass_key(D, i); },
+        [&](uint32_t key) { return int(key >> D.shift) & (D.bins - 1); },
+        [&](int64_t i, uint32_t key, int at) { pass_emit(D, i, key, at); });
+}
+
+// All passes of a small sort in one work-group.
+struct OneDesc {
+    uint32_t *keys[2], *tokens[2];  // pass p writes the buffers p & 1
+    int32_t passes, digit_bits;
+    ZeroDesc zero;                  // ids and tags
+};
+
+__global__ __launch_bounds__(64 * kOneWaves) void digit_sort_kernel(const OneDesc D)
+{
+    extern __shared__ int lds[];
+    PassDesc P = {};
+    P.zero = D.zero;
+    P.bins = 1 << D.digit_bits;
+    const SortLds l = sort_lds(lds, kOneWaves, P.bins);
+    for (int pass = 0; pass < D.passes; ++pass) {
+        P.first = pass == 0;
+        P.shift = pass * D.digit_bits;
+        P.keys_in = D.keys[1 - (pass & 1)];
+        P.tokens_in = D.tokens[1 - (pass & 1)];
+        P.keys_out = D.keys[pass & 1];
+        P.tokens_out = D.tokens[pass & 1];
+        sort_place<kOneWaves, kOneSteps>(
+            l, 0, D.zero.T, P.bins, 1, nullptr, 1, 0, [&](int64_t i) { return pass_key(P, i); },
+            [&](uint32_t key) { return int(key >> P.shift) & (P.bins - 1); },
+            [&](int64_t i, uint32_t key, int at) {
+                if (P.first && key < D.zero.V)
+                    D.zero.tags[key] = uint32_t(i);
+                pass_emit(P, i, key, at);
+            });
+        __syncthreads();               // the next pass reads what this one wrote
+    }
 }
 
 // ------------------------------------------------------- sums by their id --
@@ -113,16 +203,16 @@ struct GradDesc {
     const uint32_t *keys, *tokens;  // sorted
     const char *dout;
     char *dtable;
-    float *partials;                // [chunks][2][width]
-    int64_t T, width;
-    uint32_t V, chunks, row, vecs, grad_row, elems;
-    FastDiv col_groups;             // column groups of a chunk: vecs / lanes, rounded up
-    int32_t lanes_log2;             // lanes of a column group
-    int64_t items;                  // chunks * column groups
+    float *partials;                // [blocks][2][width]
+    int64_t T, width, block_tokens;
+    uint32_t V, blocks, row, vecs, grad_row, elems;
+    FastDiv col_groups;
+    int32_t lanes_log2, chunk;
     uint32_t sum_groups;            // work-groups that sum; the others write zeros
     basp_seq_order order;
     float scale;
     int32_t accumulate;
+    ZeroDesc zero;
 };
 
 // The channels of vector a of table row `key`, scaled, as they are written.
@@ -152,107 +242,174 @@ __device__ inline void write_grad(const GradDesc &D, uint32_t key, uint32_t a, c
     store_values<G, N>(p, f);
 }
 
-// Rows of the table that no token names, as zeros: 64 rows a work-group.
-template <typename G>
-__device__ inline void zero_unnamed(const GradDesc &D, uint32_t group, uint32_t groups)
+template <int N>
+__device__ inline void clear(float (&f)[N])
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (uint32_t r0 = group * 64; r0 < D.V; r0 += groups * 64) {
-        const uint32_t r = r0 + lane;
-        // the first sorted key that is not below r
-        int64_t lo = 0, hi = D.T;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (D.keys[mid] < r)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        uint64_t m = __ballot(r < D.V && (lo == D.T || D.keys[lo] != r));
-        for (int n = 0; m; ++n, m &= m - 1)
-            if (n % (kThreads / 64) == wave)
-                zero_row(D.dtable + uint64_t(r0 + __builtin_ctzll(m)) * D.grad_row, D.grad_row, lane);
-    }
-}
-
-// The sorted tokens in chunks of kChunk: a lane sums one vector of channels
-// over its chunk and writes the sum wherever the id changes.  An id whose
-// tokens lie in several chunks leaves one fp32 partial sum per chunk: slot 0
-// where it began in an earlier chunk, slot 1 where it begins in this one.
-template <typename E, typename G, int VW>
-__global__ __launch_bounds__(kThreads) void chunk_sum_kernel(const GradDesc D)
-{
-    constexpr int N = VW / sizeof(E), U = 8;
-    if (blockIdx.x >= D.sum_groups) {
-        zero_unnamed<G>(D, blockIdx.x - D.sum_groups, gridDim.x - D.sum_groups);
-        return;
-    }
-    const uint32_t lanes = 1u << D.lanes_log2;
-    const int64_t item = int64_t{blockIdx.x} * (kThreads >> D.lanes_log2) + (threadIdx.x >> D.lanes_log2);
-    if (item >= D.items)
-        return;
-    const uint32_t chunk = fastdiv(uint32_t(item), D.col_groups);
-    const uint32_t a = (uint32_t(item) - chunk * D.col_groups.d) * lanes + (threadIdx.x & (lanes - 1));
-    if (a >= D.vecs)
-        return;
-    const uint32_t off = vec_offset<VW>(a, D.row);
-    const int64_t begin = int64_t{chunk} * kChunk, end = begin + kChunk < D.T ? begin + kChunk : D.T;
-    float *partial = D.partials + int64_t{chunk} * 2 * D.width + int64_t{a} * N;
-
-    uint32_t key = D.keys[begin];
-    bool began_before = begin > 0 && D.keys[begin - 1] == key;
-    float acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        acc[i] = 0.f;
-    for (int64_t i0 = begin; i0 < end && key < D.V; i0 += U) {
+        f[i] = 0.f;
+}
+
+template <int N>
+__device__ inline void add(float (&f)[N], const float (&g)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        f[i] += g[i];
+}
+
+constexpr uint32_t kNoKey = 0xffffffffu;    // no id: V is at most 2^30
+
+// The sorted tokens, `chunk` to a team of lanes; the teams of a work-group
+// follow each other.  A lane adds one vector of channels over its team's
+// chunk and writes the sum wherever the id changes.  The sum of an id that
+// reaches over an end of the chunk goes to LDS, where the first team joins
+// the work-group's; one that reaches over an end of the work-group's tokens
+// leaves an fp32 partial sum in each work-group: slot 0 where it began in an
+// earlier one, slot 1 where it begins in this one.
+// UNI: teams are whole waves; the chunk's ids and rows are loaded at once, one
+// token a lane, and read from there as scalars.
+template <typename E, typename G, int VW, bool UNI>
+__global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D)
+{
+    constexpr int N = VW / sizeof(E), U = 8;
+    constexpr int HEAD = 1, ON = 2, TAIL = 4;  // of a team: a sum that began before its chunk, one that
+                                               // goes on from there behind it, one that begins in it and goes on
+    __shared__ float sums[2][kSumThreads][N];
+    __shared__ uint32_t key_of[2][UNI ? 4 : kSumThreads];
+    __shared__ int state[UNI ? 4 : kSumThreads];
+    if (blockIdx.x >= D.sum_groups) {
+        zero_unnamed<kSumThreads / 64>(D.zero, blockIdx.x - D.sum_groups, gridDim.x - D.sum_groups);
+        return;
+    }
+    const int lanes_log2 = UNI ? 6 : D.lanes_log2, lanes = 1 << lanes_log2, teams = kSumThreads >> lanes_log2;
+    const int lane = threadIdx.x & (lanes - 1);
+    int team = threadIdx.x >> lanes_log2;
+    if constexpr (UNI)
+        team = scalar(team);
+    const uint32_t block = fastdiv(blockIdx.x, D.col_groups);
+    const uint32_t a = (blockIdx.x - block * D.col_groups.d) * lanes + lane;
+    const bool live = a < D.vecs;
+    const uint32_t off = vec_offset<VW>(live ? a : 0, D.row);
+    const int64_t begin = block * D.block_tokens + int64_t{team} * D.chunk;
+    const int n = begin >= D.T ? 0 : D.T - begin < D.chunk ? int(D.T - begin) : D.chunk;
+
+    uint32_t my_key = D.V, my_row = 0;          // UNI: of the chunk's token number `lane`
+    if constexpr (UNI)
+        if (lane < n) {
+            my_key = D.keys[begin + lane];
+            my_row = seq_row(D.order, D.tokens[begin + lane]);
+        }
+    const uint32_t before = n && begin ? D.keys[begin - 1] : kNoKey;
+    const uint32_t after = n && begin + n < D.T ? D.keys[begin + n] : kNoKey;
+    const auto key_at = [&](int j) -> uint32_t {
+        if constexpr (UNI)
+            return __builtin_amdgcn_readlane(my_key, j);
+        return D.keys[begin + j];
+    };
+    const auto row_at = [&](int j) -> uint32_t {
+        if constexpr (UNI)
+            return __builtin_amdgcn_readlane(my_row, j);
+        return seq_row(D.order, D.tokens[begin + j]);
+    };
+    uint32_t key = n ? key_at(0) : D.V;
+    bool head = key == before;
+    int flags = 0;
+    float acc[N];
+    clear(acc);
+    const auto keep = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            sums[slot][threadIdx.x][i] = acc[i];
+        if (lane == 0)
+            key_of[slot][team] = key;
+    };
+    for (int j0 = 0; j0 < n && key < D.V; j0 += U) {
         uint32_t k[U];
         typename MemVec<VW>::type x[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            k[j] = i0 + j < end ? D.keys[i0 + j] : D.V;
+            k[j] = j0 + j < n ? key_at(j0 + j) : D.V;
             if (k[j] < D.V)
-                x[j] = load_vec<VW>(D.dout + uint64_t(seq_row(D.order, D.tokens[i0 + j])) * D.row + off);
+                x[j] = load_vec<VW>(D.dout + uint64_t(row_at(j0 + j)) * D.row + off);
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            if (i0 + j >= end)
+            if (j0 + j >= n)
                 break;
             if (k[j] != key) {
-                if (began_before)
-                    store_values<float, N>(reinterpret_cast<char *>(partial), acc);
-                else
+                if (head) {
+                    keep(0);
+                    flags = HEAD;
+                } else if (live) {
                     write_grad<G, N>(D, key, a, acc);
-                began_before = false;
+                }
+                head = false;
                 key = k[j];
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    acc[i] = 0.f;
+                clear(acc);
             }
             if (key >= D.V)            // ignored ids come last
                 break;
             float f[N];
             unpack<E, VW>(x[j], f);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                acc[i] += f[i];
+            add(acc, f);
         }
     }
-    if (key >= D.V)
+    if (key < D.V) {
+        const bool on = key == after;
+        if (head) {
+            keep(0);
+            flags = HEAD | (on ? ON : 0);
+        } else if (on) {
+            keep(1);
+            flags |= TAIL;
+        } else if (live) {
+            write_grad<G, N>(D, key, a, acc);
+        }
+    }
+    if (lane == 0)
+        state[team] = flags;
+    __syncthreads();
+    if (team != 0)
         return;
-    const bool goes_on = end < D.T && D.keys[end] == key;
-    if (began_before)
-        store_values<float, N>(reinterpret_cast<char *>(partial), acc);
-    else if (goes_on)
-        store_values<float, N>(reinterpret_cast<char *>(partial + D.width), acc);
-    else
-        write_grad<G, N>(D, key, a, acc);
+    float *partial = D.partials + int64_t{block} * 2 * D.width + int64_t{a} * N;
+    bool open = false;                  // a sum that goes on into the next team
+    head = false;
+    clear(acc);
+    for (int t = 0; t < teams; ++t) {
+        const int s = state[t];
+        const float(&h)[N] = sums[0][(t << lanes_log2) + lane], (&tail)[N] = sums[1][(t << lanes_log2) + lane];
+        if (s & HEAD) {
+            key = key_of[0][t];
+            head = open ? head : true;
+            open = s & ON;
+            add(acc, h);
+            if (!open) {
+                if (live) {
+                    if (head)
+                        store_values<float, N>(reinterpret_cast<char *>(partial), acc);
+                    else
+                        write_grad<G, N>(D, key, a, acc);
+                }
+                head = false;
+                clear(acc);
+            }
+        }
+        if (s & TAIL) {
+            clear(acc);
+            add(acc, tail);
+            open = true;
+            head = false;
+        }
+    }
+    if (open && live)
+        store_values<float, N>(reinterpret_cast<char *>(head ? partial : partial + D.width), acc);
 }
 
-// The ids whose tokens lie in several chunks: the work-group of the chunk in
-// which one begins adds its partial sums, each wave a consecutive part of
-// them and then the waves' sums in order.
-constexpr int kJoinWaves = 8;
+// The ids whose tokens lie in several work-groups of chunk_sum_kernel: the
+// work-group for the one in which an id begins adds its partial sums, each
+// wave a consecutive part of them, and then the waves' sums in order.
+constexpr int kJoinWaves = 4;
 
 template <typename E, typename G, int VW>
 __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const GradDesc D)
@@ -260,38 +417,33 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const GradDesc D)
     constexpr int N = VW / sizeof(E);
     __shared__ float sums[kJoinWaves][64][N];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (uint32_t chunk = blockIdx.x; chunk + 1 < D.chunks; chunk += gridDim.x) {
-        const int64_t begin = int64_t{chunk} * kChunk, end = begin + kChunk;
+    for (uint32_t block = blockIdx.x; block + 1 < D.blocks; block += gridDim.x) {
+        const int64_t begin = block * D.block_tokens, end = begin + D.block_tokens;
         const uint32_t key = D.keys[end - 1];
         if (key >= D.V || D.keys[end] != key || (begin > 0 && D.keys[begin - 1] == key))
             continue;
-        // past the last token with this key
-        int64_t lo = end, hi = D.T;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (D.keys[mid] <= key)
-                lo = mid + 1;
-            else
-                hi = mid;
+        // work-groups whose first token still has this id
+        int64_t n = 1;
+        for (;;) {
+            const int64_t first = (block + n + lane) * D.block_tokens;
+            const uint64_t same = __ballot(first < D.T && D.keys[first] == key);
+            n += __popcll(same);
+            if (~same)
+                break;
         }
-        const int64_t last = (lo - 1) / kChunk, n = last - chunk + 1;   // chunks with a part of it
         const int64_t per = (n + kJoinWaves - 1) / kJoinWaves, i0 = wave * per, i1 = i0 + per < n ? i0 + per : n;
         for (uint32_t a0 = blockIdx.y * 64; a0 < D.vecs; a0 += gridDim.y * 64) {
             const uint32_t a = a0 + lane;
             float acc[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                acc[i] = 0.f;
+            clear(acc);
             if (a < D.vecs) {
                 const float *p = D.partials + int64_t{a} * N;
 #pragma unroll 4
                 for (int64_t i = i0; i < i1; ++i) {
                     float f[N];
-                    load_values<float, N>(
-                        reinterpret_cast<const char *>(p + ((chunk + i) * 2 + (i == 0)) * D.width), f);
-#pragma unroll
-                    for (int e = 0; e < N; ++e)
-                        acc[e] += f[e];
+                    load_values<float, N>(reinterpret_cast<const char *>(p + ((block + i) * 2 + (i == 0)) * D.width),
+                                          f);
+                    add(acc, f);
                 }
             }
 #pragma unroll
@@ -300,9 +452,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const GradDesc D)
             __syncthreads();
             if (wave == 0 && a < D.vecs) {
                 for (int w = 1; w < kJoinWaves; ++w)
-#pragma unroll
-                    for (int e = 0; e < N; ++e)
-                        acc[e] += sums[w][lane][e];
+                    add(acc, sums[w][lane]);
                 write_grad<G, N>(D, key, a, acc);
             }
             __syncthreads();
@@ -325,17 +475,20 @@ struct GradFns {
     const void *sum, *join;
 };
 
-template <typename E, int VW>
-GradFns grad_fns(basp_dtype grad)
+template <typename E, typename G, int VW>
+GradFns grad_fns_of(bool uni)
 {
-    if (grad == BASP_FP32)
-        return {reinterpret_cast<const void *>(chunk_sum_kernel<E, float, VW>),
-                reinterpret_cast<const void *>(join_kernel<E, float, VW>)};
-    if (grad == BASP_BF16)
-        return {reinterpret_cast<const void *>(chunk_sum_kernel<E, __bf16, VW>),
-                reinterpret_cast<const void *>(join_kernel<E, __bf16, VW>)};
-    return {reinterpret_cast<const void *>(chunk_sum_kernel<E, _Float16, VW>),
-            reinterpret_cast<const void *>(join_kernel<E, _Float16, VW>)};
+    return {uni ? reinterpret_cast<const void *>(chunk_sum_kernel<E, G, VW, true>)
+                : reinterpret_cast<const void *>(chunk_sum_kernel<E, G, VW, false>),
+            reinterpret_cast<const void *>(join_kernel<E, G, VW>)};
+}
+
+template <typename E, int VW>
+GradFns grad_fns(basp_dtype grad, bool uni)
+{
+    return grad == BASP_FP32   ? grad_fns_of<E, float, VW>(uni)
+           : grad == BASP_BF16 ? grad_fns_of<E, __bf16, VW>(uni)
+                               : grad_fns_of<E, _Float16, VW>(uni);
 }
 
 basp_status launch_lookup(const basp_embed_plan &p, const void *ids, const void *table, float scale, void *out,
@@ -364,6 +517,8 @@ basp_status launch_lookup(const basp_embed_plan &p, const void *ids, const void 
     return s;
 }
 
+constexpr uint32_t kZeroGroups = 1 << 20;   // work-groups of a launch that write zeros, at most
+
 basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *dout, float scale, int accumulate,
                         void *dtable, void *ws, void *stream)
 {
@@ -373,6 +528,16 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
         keys[i] = reinterpret_cast<uint32_t *>(base + p.keys[i]);
         tokens[i] = reinterpret_cast<uint32_t *>(base + p.tokens[i]);
     }
+    ZeroDesc Z = {};
+    Z.ids = ids;
+    Z.tags = reinterpret_cast<uint32_t *>(base + p.tags);
+    Z.dtable = static_cast<char *>(dtable);
+    Z.T = p.T;
+    Z.V = p.V;
+    Z.padding = p.padding;
+    Z.row = uint32_t(p.D * p.grad_es);
+    Z.wide_ids = p.id_bytes == 8;
+
     basp_status s = BASP_OK;
     bool first = true;
     const auto go = [&](const void *fn, dim3 grid, int block, const auto &D, bool last, size_t lds) {
@@ -380,62 +545,84 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
             s = launch_kernel(fn, grid, block, D, stream, first, last, lds);
         first = false;
     };
-    int from = 1;                       // the pass before wrote keys[from]
-    for (int pass = 0; pass < p.passes && p.T; ++pass) {
+    // The table's rows are shared out over the launches that may write zeros:
+    // those of the sort after the one that writes the tags, a count a third
+    // of a placement's share, or else the one that sums.
+    const int64_t rows = accumulate ? 0 : p.V;
+    int64_t done = 0;
+    const auto share = [&](int64_t part, int64_t of) {
+        Z.begin = uint32_t(done);
+        done = part == of ? rows : std::min(rows, done + (rows - done) / of * part / 64 * 64);
+        Z.end = uint32_t(done);
+        return std::min(kZeroGroups, groups_of(Z.end - Z.begin, 64));
+    };
+    if (p.T && p.sort_blocks == 0) {
+        OneDesc D = {};
+        for (int i = 0; i < 2; ++i) {
+            D.keys[i] = keys[i];
+            D.tokens[i] = tokens[i];
+        }
+        D.passes = p.passes;
+        D.digit_bits = p.digit_bits;
+        D.zero = Z;
+        go(reinterpret_cast<const void *>(digit_sort_kernel), dim3(1), 64 * kOneWaves, D, false,
+           sort_lds_bytes(kOneWaves, 1 << p.digit_bits));
+    }
+    for (int pass = 0; pass < p.passes && p.sort_blocks > 0 && p.T; ++pass) {
         PassDesc D = {};
-        D.ids = ids;
-        D.keys_in = keys[from];
-        D.tokens_in = tokens[from];
-        D.keys_out = keys[1 - from];
-        D.tokens_out = tokens[1 - from];
+        D.keys_in = keys[1 - (pass & 1)];
+        D.tokens_in = tokens[1 - (pass & 1)];
+        D.keys_out = keys[pass & 1];
+        D.tokens_out = tokens[pass & 1];
         D.hist = reinterpret_cast<int32_t *>(base + p.hist);
-        D.T = p.T;
         D.items = p.block_items;
-        D.V = p.V;
-        D.padding = p.padding;
         D.first = pass == 0;
-        D.wide_ids = p.id_bytes == 8;
         D.shift = pass * p.digit_bits;
         D.bins = 1 << p.digit_bits;
-        if (p.sort_blocks > 1)
-            go(reinterpret_cast<const void *>(digit_count_kernel), dim3(p.sort_blocks), kSortBlock, D, false,
-               size_t(4) * D.bins);
-        go(reinterpret_cast<const void *>(digit_place_kernel), dim3(p.sort_blocks), kSortBlock, D, false,
-           sort_lds_bytes(kSortWaves, D.bins));
-        from = 1 - from;
+        D.groups = p.sort_blocks;
+        const int64_t left = 4 * (p.passes - pass);         // shares from this pass on: 1 a count, 3 a placement
+        const uint32_t with_count = pass == 0 ? (Z.begin = Z.end = 0) : share(1, left);
+        D.zero = Z;
+        go(reinterpret_cast<const void *>(digit_count_kernel), dim3(p.sort_blocks + with_count), kSortBlock, D, false,
+           size_t(4) * D.bins);
+        const uint32_t with_place = share(3, left - 1);
+        D.zero = Z;
+        go(p.block_items <= kSortItems ? reinterpret_cast<const void *>(digit_place_kernel<kSortSteps>)
+                                       : reinterpret_cast<const void *>(digit_place_kernel<0>),
+           dim3(p.sort_blocks + with_place), kSortBlock, D, false, sort_lds_bytes(kSortWaves, D.bins));
     }
-    const int vw = row_vector(p.D, p.es);
-    const GradFns fn = BASP_BY_ROW(grad_fns, p.dtype, vw, p.grad_dtype);
+    const int vw = row_vector(p.D, p.es), sorted = (p.passes - 1) & 1;
+    const GradFns fn = BASP_BY_ROW(grad_fns, p.dtype, vw, p.grad_dtype, p.lanes_log2 == 6);
     GradDesc D = {};
-    D.keys = keys[from];
-    D.tokens = tokens[from];
+    D.keys = keys[sorted];
+    D.tokens = tokens[sorted];
     D.dout = static_cast<const char *>(dout);
     D.dtable = static_cast<char *>(dtable);
     D.partials = reinterpret_cast<float *>(base + p.partials);
     D.T = p.T;
     D.width = p.width;
+    D.block_tokens = int64_t{p.chunk} * (kSumThreads >> p.lanes_log2);
     D.V = uint32_t(p.V);
-    D.chunks = uint32_t(p.chunks);
+    D.blocks = uint32_t(p.blocks);
     D.row = uint32_t(p.D * p.es);
     D.grad_row = uint32_t(p.D * p.grad_es);
     D.elems = uint32_t(p.D);
     D.vecs = uint32_t((int64_t{D.row} + vw - 1) / vw);
-    while (D.lanes_log2 < 6 && (1u << D.lanes_log2) < D.vecs)
-        ++D.lanes_log2;
-    const uint32_t col_groups = groups_of(D.vecs, 1 << D.lanes_log2);
-    D.col_groups = make_fastdiv(col_groups);
-    D.items = p.chunks * col_groups;
-    D.sum_groups = groups_of(D.items, kThreads >> D.lanes_log2);
+    D.col_groups = make_fastdiv(uint32_t(p.col_groups));
+    D.lanes_log2 = p.lanes_log2;
+    D.chunk = p.chunk;
+    D.sum_groups = uint32_t(p.blocks * p.col_groups);
     D.order = p.order;
     D.scale = scale;
     D.accumulate = accumulate != 0;
-    const uint32_t zeros = accumulate ? 0 : uint32_t(std::min<int64_t>(1 << 20, (p.V + 63) / 64));
-    const bool joins = p.chunks > 1;
+    const uint32_t zeros = share(1, 1);
+    D.zero = Z;
+    const bool joins = p.blocks > 1;
     if (D.sum_groups + zeros)
-        go(fn.sum, dim3(D.sum_groups + zeros), kThreads, D, !joins, 0);
+        go(fn.sum, dim3(D.sum_groups + zeros), kSumThreads, D, !joins, 0);
     if (joins)
-        go(fn.join, dim3(uint32_t(std::min<int64_t>(p.chunks - 1, 1 << 20)), std::min<uint32_t>(groups_of(D.vecs, 64), 1024)), 64 * kJoinWaves, D,
-           true, 0);
+        go(fn.join, dim3(uint32_t(std::min<int64_t>(p.blocks - 1, 1 << 20)), std::min<uint32_t>(groups_of(D.vecs, 64), 1024)),
+           64 * kJoinWaves, D, true, 0);
     return s;
 }
 

@@ -44,21 +44,22 @@ __global__ __launch_bounds__(kSortBlock) void expert_count_kernel(const SortDesc
                            [&](int64_t i) { return expert_of(D.ids, i, D.E, D.wide_ids); });
 }
 
+// R: 64-item steps of a wave whose experts stay in registers, or 0 (sort.hpp).
+template <int R>
 __global__ __launch_bounds__(kSortBlock) void expert_place_kernel(const SortDesc D)
 {
     extern __shared__ int lds[];
     const SortLds l = sort_lds(lds, kSortWaves, D.E);
     const int group = blockIdx.x, groups = gridDim.x, tid = threadIdx.x;
     const int64_t begin = group * D.items, end = begin + D.items < D.slots ? begin + D.items : D.slots;
-    const auto bin = [&](int64_t i) { return expert_of(D.ids, i, D.E, D.wide_ids); };
-    sort_place<kSortWaves>(l, begin, end, D.E, D.align, D.hist, groups, group, bin, [&](int64_t i, int, int at) {
-        D.pos[i] = at;
-        if (at < D.max_rows)
-            D.order[at] = int32_t(i);
-    });
-    for (int64_t i = begin + tid; i < end; i += kSortBlock)
-        if (bin(i) < 0)
-            D.pos[i] = -1;
+    sort_place<kSortWaves, R>(
+        l, begin, end, D.E, D.align, D.hist, groups, group,
+        [&](int64_t i) { return expert_of(D.ids, i, D.E, D.wide_ids); }, [](int e) { return e; },
+        [&](int64_t i, int, int at) {
+            D.pos[i] = at;
+            if (at >= 0 && at < D.max_rows)
+                D.order[at] = int32_t(i);
+        });
     // rows without a slot: the padding of this group's share of the experts,
     // and its share of what lies behind the last one
     for (int e = group; e < D.E; e += groups)
@@ -135,6 +136,62 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(const MoveDesc D)
         const uint32_t p = pos[k];
         if (p < D.max_rows)
             store_vec<VW>(D.out + uint64_t(p) * D.row + off, x);
+    }
+}
+
+// The sort and the move of a small call in one launch: every work-group ranks
+// all the slots, keeps those of its own rows, and copies these rows.
+constexpr int kRouteWaves = kThreads / 64, kRouteSteps = 4;
+constexpr int kRouteSlots = kThreads * kRouteSteps;
+constexpr int kRouteRows = 64;      // rows of a work-group at most
+constexpr int64_t kRouteGroups = 1024;
+
+struct RouteDesc {
+    SortDesc sort;
+    const char *x;
+    char *out;
+    uint32_t row;
+    FastDiv per_row, K;
+    int32_t rows;                   // of a work-group
+};
+
+template <int VW>
+__global__ __launch_bounds__(kThreads) void route_kernel(const RouteDesc D)
+{
+    extern __shared__ int lds[];
+    __shared__ int slot_of[kRouteRows];
+    const SortDesc &S = D.sort;
+    const SortLds l = sort_lds(lds, kRouteWaves, S.E);
+    const int tid = threadIdx.x, first = blockIdx.x * D.rows;
+    const int rows = first + D.rows < S.max_rows ? D.rows : S.max_rows - first;
+    if (tid < kRouteRows)
+        slot_of[tid] = -1;
+    sort_place<kRouteWaves, kRouteSteps>(
+        l, 0, S.slots, S.E, S.align, nullptr, 1, 0,
+        [&](int64_t i) { return expert_of(S.ids, i, S.E, S.wide_ids); }, [](int e) { return e; },
+        [&](int64_t i, int, int at) {
+            if (blockIdx.x == 0)
+                S.pos[i] = at;
+            if (at >= first && at < first + rows)
+                slot_of[at - first] = int(i);
+        });
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (int e = tid; e < S.E; e += kThreads)
+            S.counts[e] = l.total[e];
+        for (int e = tid; e <= S.E; e += kThreads)
+            S.offsets[e] = l.start[e];
+    }
+    if (tid < rows)
+        S.order[first + tid] = slot_of[tid];
+    const uint32_t n = rows * D.per_row.d;
+    for (uint32_t v = tid; v < n; v += kThreads) {
+        const uint32_t r = fastdiv(v, D.per_row), off = vec_offset<VW>(v - r * D.per_row.d, D.row);
+        const int slot = slot_of[r];
+        typename MemVec<VW>::type x = {};
+        if (slot >= 0)
+            x = load_vec<VW, false>(D.x + uint64_t(fastdiv(slot, D.K)) * D.row + off);
+        store_vec<VW, false>(D.out + uint64_t(first + r) * D.row + off, x);
     }
 }
 
@@ -296,19 +353,25 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const GradDesc D
 
 // ------------------------------------------------------------- launches --
 
-basp_status launch_sort(const basp_expert_plan &p, const void *ids, int32_t *pos, int32_t *order, int32_t *offsets,
-                        int32_t *counts, void *ws, void *stream, bool last)
+SortDesc sort_desc(const basp_expert_plan &p, const void *ids, int32_t *pos, int32_t *order, int32_t *offsets,
+                   int32_t *counts, void *ws)
 {
-    const SortDesc D = {ids, pos, order, offsets, counts, static_cast<int32_t *>(ws), p.slots, p.block_items,
-                        p.E, p.align, int32_t(p.max_rows), p.id_bytes == 8};
+    return {ids, pos, order, offsets, counts, static_cast<int32_t *>(ws), p.slots, p.block_items,
+            p.E, p.align, int32_t(p.max_rows), p.id_bytes == 8};
+}
+
+basp_status launch_sort(const basp_expert_plan &p, const SortDesc &D, void *stream, bool last)
+{
     const dim3 grid(p.sort_blocks);
+    const void *place = p.block_items <= kSortItems ? reinterpret_cast<const void *>(expert_place_kernel<kSortSteps>)
+                                                    : reinterpret_cast<const void *>(expert_place_kernel<0>);
     basp_status s = BASP_OK;
     if (p.sort_blocks > 1)
         s = launch_kernel(reinterpret_cast<const void *>(expert_count_kernel), grid, kSortBlock, D, stream, true, false,
                           size_t(4) * p.E);
     if (s == BASP_OK)
-        s = launch_kernel(reinterpret_cast<const void *>(expert_place_kernel), grid, kSortBlock, D, stream,
-                          p.sort_blocks == 1, last, sort_lds_bytes(kSortWaves, p.E));
+        s = launch_kernel(place, grid, kSortBlock, D, stream, p.sort_blocks == 1, last,
+                          sort_lds_bytes(kSortWaves, p.E));
     return s;
 }
 
@@ -373,6 +436,38 @@ const void *grad_fn(int K)
            : K == 2 ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 2>)
            : K <= 4 ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 4>)
                     : reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 8>);
+}
+
+template <int VW>
+const void *route_fn()
+{
+    return reinterpret_cast<const void *>(route_kernel<VW>);
+}
+
+// Whether a call is one launch of route_kernel.
+bool route_in_one(const basp_expert_plan &p, const RowShape &r)
+{
+    return p.slots <= kRouteSlots && p.max_rows > 0 && p.max_rows <= kRouteGroups * kRouteRows &&
+           p.max_rows * r.vecs <= kLaunchVectors;
+}
+
+basp_status launch_route(const basp_expert_plan &p, const RowShape &r, const SortDesc &S, const void *x, void *out,
+                         void *stream)
+{
+    const void *fn = r.vw == 16  ? route_fn<16>()
+                     : r.vw == 8 ? route_fn<8>()
+                     : r.vw == 4 ? route_fn<4>()
+                                 : route_fn<2>();
+    RouteDesc D = {};
+    D.sort = S;
+    D.x = static_cast<const char *>(x);
+    D.out = static_cast<char *>(out);
+    D.row = uint32_t(r.row);
+    D.per_row = make_fastdiv(uint32_t(r.vecs));
+    D.K = make_fastdiv(uint32_t(p.K));
+    D.rows = int32_t((p.max_rows + kRouteGroups - 1) / kRouteGroups);
+    return launch_kernel(fn, dim3(groups_of(p.max_rows, D.rows)), kThreads, D, stream, true, true,
+                         sort_lds_bytes(kRouteWaves, p.E));
 }
 
 basp_status launch_scatter(const basp_expert_plan &p, const void *x, const int32_t *pos, const int32_t *order,
@@ -485,7 +580,7 @@ extern "C" basp_status basp_expert_sort(const basp_expert_plan *p, const void *i
         const CallBuf out[] = {{pos, n.pos, 4}, {order, n.order, 4}, {offsets, n.offsets, 4}, {counts, n.counts, 4},
                                {ws, p->workspace_bytes, 16}};
         const basp_status s = basp::check_call(in, 1, out, 5);
-        return s != BASP_OK ? s : basp::launch_sort(*p, ids, pos, order, offsets, counts, ws, stream, true);
+        return s != BASP_OK ? s : basp::launch_sort(*p, basp::sort_desc(*p, ids, pos, order, offsets, counts, ws), stream, true);
     });
 }
 
@@ -515,8 +610,13 @@ extern "C" basp_status basp_route_to_expert(const basp_expert_plan *p, const voi
         const CallBuf o[] = {{pos, n.pos, 4}, {order, n.order, 4}, {offsets, n.offsets, 4}, {counts, n.counts, 4},
                              {out, n.rows, p->es}, {ws, p->workspace_bytes, 16}};
         basp_status s = basp::check_call(in, 2, o, 6);
-        if (s == BASP_OK)
-            s = basp::launch_sort(*p, ids, pos, order, offsets, counts, ws, stream, p->T == 0);
+        if (s != BASP_OK)
+            return s;
+        const basp::SortDesc D = basp::sort_desc(*p, ids, pos, order, offsets, counts, ws);
+        const basp::RowShape r = basp::row_shape(*p);
+        if (basp::route_in_one(*p, r))
+            return basp::launch_route(*p, r, D, x, out, stream);
+        s = basp::launch_sort(*p, D, stream, p->T == 0);
         return s != BASP_OK ? s : basp::launch_scatter(*p, x, pos, order, out, stream, false);
     });
 }

@@ -14,7 +14,8 @@ namespace {
 constexpr int64_t kRowLimit = int64_t{1} << 30;     // bytes of a row
 constexpr int64_t kIndexLimit = 0x7fffffff - 1;     // slots, rows, tokens: int32 with -1, and 31-bit division
 constexpr int64_t kVocabLimit = int64_t{1} << 30;
-constexpr int64_t kSumItems = int64_t{1} << 25;
+constexpr int64_t kSumGroups = 512;                 // two work-groups a compute unit
+constexpr int64_t kSumLimit = int64_t{1} << 23;     // work-groups of a launch's 32-bit extent
 
 int float_size(basp_dtype t)
 {
@@ -24,14 +25,14 @@ int float_size(basp_dtype t)
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
 
-// Items per work-group of a sort: at least kItems, and more where the call
+// Items per work-group of a sort: at least kSortItems, and more where the call
 // would otherwise take over kBlocks groups (each reads the counts of all the
 // others).  A multiple of the group's threads, so that waves take whole
 // multiples of 64.
 void split_sort(int64_t n, int32_t &blocks, int64_t &items)
 {
-    constexpr int64_t kItems = 2048, kBlocks = 256;
-    items = round_up(std::max<int64_t>(kItems, ceil_div(n, kBlocks)), basp::kSortBlock);
+    constexpr int64_t kBlocks = 256;
+    items = round_up(std::max<int64_t>(basp::kSortItems, ceil_div(n, kBlocks)), basp::kSortBlock);
     blocks = int32_t(std::max<int64_t>(1, ceil_div(n, items)));
 }
 
@@ -149,11 +150,21 @@ extern "C" basp_embed_plan *basp_embed_plan_create(const basp_plan *layout, int6
         record(BASP_ERR_UNSUPPORTED);
         return nullptr;
     }
-    // the gradient's sums are one launch: a wave per chunk of tokens and 64
-    // vectors of channels, four to a work-group
+    // the gradient's sums are one launch of 256-thread work-groups: a team of
+    // up to 64 lanes takes one vector of channels each and `chunk` sorted
+    // tokens, and the teams of a work-group follow each other.  Short chunks
+    // where long ones would leave compute units without a few waves each.
     const int epv = basp::row_vector(D, es) / es;
-    const int64_t chunks = ceil_div(T, basp::kChunk), vecs = ceil_div(D, epv);
-    if (vecs > 32 && chunks > kSumItems / ceil_div(vecs, 64)) {
+    const int64_t vecs = ceil_div(D, epv);
+    int lanes_log2 = 0;
+    while (lanes_log2 < 6 && (int64_t{1} << lanes_log2) < vecs)
+        ++lanes_log2;
+    const int64_t teams = basp::kSumThreads >> lanes_log2, cols = ceil_div(vecs, int64_t{1} << lanes_log2);
+    int chunk = 32;
+    while (chunk > 8 && ceil_div(T, chunk * teams) * cols < kSumGroups)
+        chunk /= 2;
+    const int64_t blocks = ceil_div(T, chunk * teams);
+    if (blocks > kSumLimit / cols) {
         record(BASP_ERR_UNSUPPORTED);
         return nullptr;
     }
@@ -183,14 +194,19 @@ extern "C" basp_embed_plan *basp_embed_plan_create(const basp_plan *layout, int6
     o.by_St = basp::make_fastdiv(o.St);
 
     // sort by id, least significant digit first, ignored ids as V: as few
-    // passes of at most 1024 digits as the ids need, of equal width
+    // passes of at most kDigitBits as the ids need, of equal width
     int bits = 1;
     while ((V >> bits) != 0)
         ++bits;
-    p->passes = (bits + 9) / 10;
+    p->passes = (bits + basp::kDigitBits - 1) / basp::kDigitBits;
     p->digit_bits = (bits + p->passes - 1) / p->passes;
     split_sort(T, p->sort_blocks, p->block_items);
-    p->chunks = chunks;
+    if (T <= basp::kOneItems)
+        p->sort_blocks = 0;
+    p->lanes_log2 = lanes_log2;
+    p->chunk = chunk;
+    p->blocks = blocks;
+    p->col_groups = int32_t(cols);
     p->width = vecs * epv;
     int64_t at = 0;
     const auto take = [&at](int64_t bytes) {
@@ -203,8 +219,9 @@ extern "C" basp_embed_plan *basp_embed_plan_create(const basp_plan *layout, int6
             p->keys[i] = take(4 * T);
             p->tokens[i] = take(4 * T);
         }
-        p->hist = take(p->sort_blocks > 1 ? (int64_t{4} << p->digit_bits) * p->sort_blocks : 0);
-        p->partials = take(p->chunks * 2 * p->width * 4);
+        p->tags = take(4 * V);
+        p->hist = take((int64_t{4} << p->digit_bits) * p->sort_blocks);
+        p->partials = take(p->blocks * 2 * p->width * 4);
     }
     p->workspace_bytes = at;
     record(BASP_OK);
