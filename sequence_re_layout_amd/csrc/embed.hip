@@ -78,29 +78,17 @@ struct ZeroDesc {
     uint32_t *tags;
     char *dtable;
     int64_t T, V, padding;
-    uint32_t begin, end;            // rows of this launch
-    uint32_t row;                   // bytes
     int32_t wide_ids;
+    ZeroPieces z;                   // rows of this launch
 };
 
-// The rows without a token in the share of work-group `group` of `groups` of
-// WAVES waves, as zeros.
 template <int WAVES>
-__device__ inline void zero_unnamed(const ZeroDesc &D, uint32_t group, uint32_t groups)
+__device__ inline void zero_unnamed(const ZeroDesc &D, uint32_t group)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (uint32_t r0 = D.begin + group * 64; r0 < D.end; r0 += groups * 64) {
-        const uint32_t r = r0 + lane;
-        bool none = r < D.end;
-        if (none) {
-            const uint32_t t = D.T ? D.tags[r] : 0;
-            none = t >= D.T || row_of_id(D.ids, t, D.V, D.padding, D.wide_ids) != r;
-        }
-        uint64_t m = __ballot(none);
-        for (int n = 0; m; ++n, m &= m - 1)
-            if (n % WAVES == wave)
-                zero_row(D.dtable + uint64_t(r0 + __builtin_ctzll(m)) * D.row, D.row, lane);
-    }
+    write_zeros<WAVES>(D.dtable, D.z, group, [&](uint32_t r) {
+        const uint32_t t = D.T ? D.tags[r] : 0;
+        return t >= D.T || row_of_id(D.ids, t, D.V, D.padding, D.wide_ids) != r;
+    });
 }
 
 // ------------------------------------------------------- tokens by their id --
@@ -136,7 +124,7 @@ __global__ __launch_bounds__(kSortBlock) void digit_count_kernel(const PassDesc 
 {
     extern __shared__ int lds[];
     if (blockIdx.x >= uint32_t(D.groups)) {
-        zero_unnamed<kSortWaves>(D.zero, blockIdx.x - D.groups, gridDim.x - D.groups);
+        zero_unnamed<kSortWaves>(D.zero, blockIdx.x - D.groups);
         return;
     }
     const int64_t T = D.zero.T, begin = blockIdx.x * D.items, end = begin + D.items < T ? begin + D.items : T;
@@ -153,7 +141,7 @@ __global__ __launch_bounds__(kSortBlock) void digit_place_kernel(const PassDesc 
 {
     extern __shared__ int lds[];
     if (blockIdx.x >= uint32_t(D.groups)) {
-        zero_unnamed<kSortWaves>(D.zero, blockIdx.x - D.groups, gridDim.x - D.groups);
+        zero_unnamed<kSortWaves>(D.zero, blockIdx.x - D.groups);
         return;
     }
     const int64_t T = D.zero.T, begin = blockIdx.x * D.items, end = begin + D.items < T ? begin + D.items : T;
@@ -279,7 +267,7 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D
     __shared__ uint32_t key_of[2][UNI ? 4 : kSumThreads];
     __shared__ int state[UNI ? 4 : kSumThreads];
     if (blockIdx.x >= D.sum_groups) {
-        zero_unnamed<kSumThreads / 64>(D.zero, blockIdx.x - D.sum_groups, gridDim.x - D.sum_groups);
+        zero_unnamed<kSumThreads / 64>(D.zero, blockIdx.x - D.sum_groups);
         return;
     }
     const int lanes_log2 = UNI ? 6 : D.lanes_log2, lanes = 1 << lanes_log2, teams = kSumThreads >> lanes_log2;
@@ -517,7 +505,7 @@ basp_status launch_lookup(const basp_embed_plan &p, const void *ids, const void 
     return s;
 }
 
-constexpr uint32_t kZeroGroups = 1 << 20;   // work-groups of a launch that write zeros, at most
+constexpr int64_t kBesideCount = int64_t{24} << 20, kBesidePlace = int64_t{64} << 20;  // bytes of zeros
 
 basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *dout, float scale, int accumulate,
                         void *dtable, void *ws, void *stream)
@@ -535,7 +523,6 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
     Z.T = p.T;
     Z.V = p.V;
     Z.padding = p.padding;
-    Z.row = uint32_t(p.D * p.grad_es);
     Z.wide_ids = p.id_bytes == 8;
 
     basp_status s = BASP_OK;
@@ -545,16 +532,16 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
             s = launch_kernel(fn, grid, block, D, stream, first, last, lds);
         first = false;
     };
-    // The table's rows are shared out over the launches that may write zeros:
-    // those of the sort after the one that writes the tags, a count a third
-    // of a placement's share, or else the one that sums.
-    const int64_t rows = accumulate ? 0 : p.V;
+    // Rows of the table are zeroed by the launches after the one that writes
+    // the tags: as many beside the sort as its launches have time for, the
+    // others beside the sums.
+    const int64_t rows = accumulate ? 0 : p.V, row = p.D * p.grad_es;
     int64_t done = 0;
-    const auto share = [&](int64_t part, int64_t of) {
-        Z.begin = uint32_t(done);
-        done = part == of ? rows : std::min(rows, done + (rows - done) / of * part / 64 * 64);
-        Z.end = uint32_t(done);
-        return std::min(kZeroGroups, groups_of(Z.end - Z.begin, 64));
+    const auto share = [&](int64_t bytes, int waves) {
+        const int64_t end = std::min(rows, done + bytes / row);
+        Z.z = zero_pieces(done, end, row, waves);
+        done = end;
+        return Z.z.groups;
     };
     if (p.T && p.sort_blocks == 0) {
         OneDesc D = {};
@@ -580,12 +567,11 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
         D.shift = pass * p.digit_bits;
         D.bins = 1 << p.digit_bits;
         D.groups = p.sort_blocks;
-        const int64_t left = 4 * (p.passes - pass);         // shares from this pass on: 1 a count, 3 a placement
-        const uint32_t with_count = pass == 0 ? (Z.begin = Z.end = 0) : share(1, left);
+        const uint32_t with_count = share(pass == 0 ? 0 : kBesideCount, kSortWaves);
         D.zero = Z;
         go(reinterpret_cast<const void *>(digit_count_kernel), dim3(p.sort_blocks + with_count), kSortBlock, D, false,
            size_t(4) * D.bins);
-        const uint32_t with_place = share(3, left - 1);
+        const uint32_t with_place = share(kBesidePlace, kSortWaves);
         D.zero = Z;
         go(p.block_items <= kSortItems ? reinterpret_cast<const void *>(digit_place_kernel<kSortSteps>)
                                        : reinterpret_cast<const void *>(digit_place_kernel<0>),
@@ -615,7 +601,7 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
     D.order = p.order;
     D.scale = scale;
     D.accumulate = accumulate != 0;
-    const uint32_t zeros = share(1, 1);
+    const uint32_t zeros = share(INT64_MAX, kSumThreads / 64);
     D.zero = Z;
     const bool joins = p.blocks > 1;
     if (D.sum_groups + zeros)

@@ -75,43 +75,42 @@ __global__ __launch_bounds__(kSortBlock) void expert_place_kernel(const SortDesc
     }
 }
 
+// Rows without a slot are few as a rule: work-groups of their own look
+// through `order`, 64 rows in one go, and share out what they find.
+struct ZeroDesc {
+    char *out;
+    const int32_t *order;
+    uint32_t max_rows, slots, row, groups;
+};
+
+constexpr int64_t kZeroGroups = 1 << 20;
+
+__device__ inline void zero_unnamed(const ZeroDesc &D, uint32_t group)
+{
+    constexpr int WAVES = kThreads / 64;
+    const int lane = threadIdx.x & 63, wave = scalar(threadIdx.x >> 6);
+    for (uint32_t r0 = group * 64; r0 < D.max_rows; r0 += D.groups * 64) {
+        const uint32_t r = r0 + lane;
+        uint64_t m = __ballot(r < D.max_rows && uint32_t(D.order[r]) >= D.slots);
+        for (int n = 0; m; ++n, m &= m - 1)
+            if (n % WAVES == wave)
+                zero_span(D.out + uint64_t(r0 + __builtin_ctzll(m)) * D.row, D.row, lane);
+    }
+}
+
 // Rows of `row` bytes in vectors of VW bytes, `per_row` of them each.
 struct MoveDesc {
     const char *x;
     char *out;
-    const int32_t *pos, *order;
+    const int32_t *pos;
     int64_t nvec;                   // vectors of the tokens of this launch
     uint32_t row;
     FastDiv per_row;
     int32_t K;
-    uint32_t max_rows, slots;
+    uint32_t max_rows;
     uint32_t move_groups;           // work-groups of the tokens; the others write zeros
+    ZeroDesc zero;
 };
-
-// Rows without a slot are written by work-groups of their own, which look
-// through `order` 64 rows at a time.
-constexpr int kZeroRows = 64;
-constexpr int64_t kZeroGroups = 1 << 20;
-
-uint32_t zero_groups(const basp_expert_plan &p)
-{
-    return uint32_t(std::min<int64_t>(kZeroGroups, (p.max_rows + kZeroRows - 1) / kZeroRows));
-}
-
-// The share of work-group `group` of `groups`.
-__device__ inline void zero_rows(char *out, const int32_t *order, uint32_t group, uint32_t groups, uint32_t max_rows,
-                                 uint32_t slots, uint32_t row)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (uint32_t r0 = group * kZeroRows; r0 < max_rows; r0 += groups * kZeroRows) {
-        const uint32_t r = r0 + lane;
-        const bool none = r < max_rows && uint32_t(order[r]) >= slots;
-        uint64_t m = __ballot(none);
-        for (int n = 0; m; ++n, m &= m - 1)
-            if (n % (kThreads / 64) == wave)
-                zero_row(out + uint64_t(r0 + __builtin_ctzll(m)) * row, row, lane);
-    }
-}
 
 // seq -> expert: each lane reads one vector of a token and writes it to the
 // rows of the token's slots.  UNI: a row is a whole number of waves, so the
@@ -120,7 +119,7 @@ template <int VW, bool UNI>
 __global__ __launch_bounds__(kThreads) void scatter_kernel(const MoveDesc D)
 {
     if (blockIdx.x >= D.move_groups) {
-        zero_rows(D.out, D.order, blockIdx.x - D.move_groups, gridDim.x - D.move_groups, D.max_rows, D.slots, D.row);
+        zero_unnamed(D.zero, blockIdx.x - D.move_groups);
         return;
     }
     const uint32_t v = blockIdx.x * kThreads + threadIdx.x;
@@ -130,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(const MoveDesc D)
     if constexpr (UNI)
         t = scalar(t);
     const uint32_t off = vec_offset<VW>(v - t * D.per_row.d, D.row);
-    const auto x = load_vec<VW>(D.x + uint64_t(t) * D.row + off);
+    const auto x = load_vec<VW, false>(D.x + uint64_t(t) * D.row + off);
     const int32_t *pos = D.pos + uint64_t(t) * D.K;
     for (int k = 0; k < D.K; ++k) {
         const uint32_t p = pos[k];
@@ -258,14 +257,15 @@ __global__ __launch_bounds__(kThreads) void gather_sum_kernel(const SumDesc D)
 struct GradDesc {
     const char *dout, *rows;
     char *drows;
-    const int32_t *pos, *order;
+    const int32_t *pos;
     const void *weights;
     void *dweights;
     uint32_t tokens, row, vecs;
     int32_t K, lanes_log2;          // lanes that share a token
-    uint32_t max_rows, slots;
-    uint32_t token_groups;
+    uint32_t max_rows;
+    uint32_t token_groups;          // work-groups of the tokens; the others write zeros
     basp_dtype weight_dtype;
+    ZeroDesc zero;
 };
 
 // The gradient of expert -> seq.  2^lanes_log2 lanes (up to the whole work-
@@ -278,8 +278,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const GradDesc D
     constexpr int N = VW / sizeof(E), WAVES = kThreads / 64;
     __shared__ float part[WAVES][KB];
     if (blockIdx.x >= D.token_groups) {
-        zero_rows(D.drows, D.order, blockIdx.x - D.token_groups, gridDim.x - D.token_groups, D.max_rows, D.slots,
-                  D.row);
+        zero_unnamed(D.zero, blockIdx.x - D.token_groups);
         return;
     }
     const uint32_t lanes = 1u << D.lanes_log2, lane = threadIdx.x & (lanes - 1);
@@ -403,6 +402,12 @@ RowShape row_shape(const basp_expert_plan &p)
     return r;
 }
 
+ZeroDesc zero_desc(const basp_expert_plan &p, int64_t row, const int32_t *order, void *out)
+{
+    return {static_cast<char *>(out), order, uint32_t(p.max_rows), uint32_t(p.slots), uint32_t(row),
+            uint32_t(std::min(kZeroGroups, (p.max_rows + 63) / 64))};
+}
+
 template <int VW>
 const void *scatter_fn(bool uni)
 {
@@ -484,15 +489,14 @@ basp_status launch_scatter(const basp_expert_plan &p, const void *x, const int32
         D.x = static_cast<const char *>(x) + t0 * r.row;
         D.out = static_cast<char *>(out);
         D.pos = pos + t0 * p.K;
-        D.order = order;
         D.nvec = n * r.vecs;
         D.row = uint32_t(r.row);
         D.per_row = make_fastdiv(uint32_t(r.vecs));
         D.K = p.K;
         D.max_rows = uint32_t(p.max_rows);
-        D.slots = uint32_t(p.slots);
+        D.zero = zero_desc(p, r.row, order, out);
         D.move_groups = groups_of(D.nvec, kThreads);
-        const uint32_t zeros = last ? zero_groups(p) : 0;
+        const uint32_t zeros = last ? D.zero.groups : 0;
         return launch_kernel(fn, dim3(D.move_groups + zeros), kThreads, D, stream, first && first_call, last);
     });
 }
@@ -528,11 +532,10 @@ basp_status launch_grad(const basp_expert_plan &p, const void *dout, const void 
     D.vecs = uint32_t(r.vecs);
     D.K = p.K;
     D.max_rows = uint32_t(p.max_rows);
-    D.slots = uint32_t(p.slots);
+    D.zero = zero_desc(p, r.row, order, drows);
     D.weight_dtype = p.weight_dtype;
     D.rows = static_cast<const char *>(rows);
     D.drows = static_cast<char *>(drows);
-    D.order = order;
     while (D.lanes_log2 < 8 && (int64_t{1} << D.lanes_log2) < r.vecs)
         ++D.lanes_log2;
     const int64_t per_group = kThreads >> D.lanes_log2, step = (int64_t{1} << 22) * per_group;
@@ -546,7 +549,7 @@ basp_status launch_grad(const basp_expert_plan &p, const void *dout, const void 
         D.dweights = static_cast<char *>(dweights) + t0 * p.K * p.ws_es;
         D.tokens = uint32_t(n);
         D.token_groups = groups_of(n, per_group);
-        const uint32_t zeros = last ? zero_groups(p) : 0;
+        const uint32_t zeros = last ? D.zero.groups : 0;
         s = launch_kernel(fn, dim3(D.token_groups + zeros), kThreads, D, stream, t0 == 0, last);
     }
     return s;
