@@ -152,36 +152,52 @@ __global__ __launch_bounds__(kSortBlock) void digit_place_kernel(const PassDesc 
         [&](int64_t i, uint32_t key, int at) { pass_emit(D, i, key, at); });
 }
 
-// All passes of a small sort in one work-group.
-struct OneDesc {
-    uint32_t *keys[2], *tokens[2];  // pass p writes the buffers p & 1
-    int32_t passes, digit_bits;
+// A small sort in one launch, by counting: a token's place is the number of
+// (id, token) pairs below its own.  Every work-group holds all T pairs in LDS
+// and places kRankTokens of them: a lane compares one of its tokens with every
+// kRankParts-th pair.  T^2 comparisons cost less than the passes of the
+// general sort up to kRankMost tokens (4095 tokens: 7 us, one work-group
+// sorting by digits 15 us; four launches 24 us).
+constexpr int kRankThreads = 1024, kRankTokens = 16, kRankParts = kRankThreads / kRankTokens;
+
+struct RankDesc {
+    uint32_t *keys, *tokens;
     ZeroDesc zero;                  // ids and tags
 };
 
-__global__ __launch_bounds__(64 * kOneWaves) void digit_sort_kernel(const OneDesc D)
+__global__ __launch_bounds__(kRankThreads) void rank_kernel(const RankDesc D)
 {
-    extern __shared__ int lds[];
-    PassDesc P = {};
-    P.zero = D.zero;
-    P.bins = 1 << D.digit_bits;
-    const SortLds l = sort_lds(lds, kOneWaves, P.bins);
-    for (int pass = 0; pass < D.passes; ++pass) {
-        P.first = pass == 0;
-        P.shift = pass * D.digit_bits;
-        P.keys_in = D.keys[1 - (pass & 1)];
-        P.tokens_in = D.tokens[1 - (pass & 1)];
-        P.keys_out = D.keys[pass & 1];
-        P.tokens_out = D.tokens[pass & 1];
-        sort_place<kOneWaves, kOneSteps>(
-            l, 0, D.zero.T, P.bins, 1, nullptr, 1, 0, [&](int64_t i) { return pass_key(P, i); },
-            [&](uint32_t key) { return int(key >> P.shift) & (P.bins - 1); },
-            [&](int64_t i, uint32_t key, int at) {
-                if (P.first && key < D.zero.V)
-                    D.zero.tags[key] = uint32_t(i);
-                pass_emit(P, i, key, at);
-            });
-        __syncthreads();               // the next pass reads what this one wrote
+    __shared__ uint64_t pairs[kRankMost];
+    __shared__ int place[kRankTokens];
+    const int T = int(D.zero.T), first = blockIdx.x * kRankTokens;
+    const int filled = (T + kRankParts - 1) / kRankParts * kRankParts;
+    for (int i = threadIdx.x; i < filled; i += kRankThreads) {
+        uint64_t p = ~uint64_t{0};
+        if (i < T) {
+            const uint32_t key = row_of_id(D.zero.ids, i, D.zero.V, D.zero.padding, D.zero.wide_ids);
+            p = uint64_t(key) << 32 | uint32_t(i);
+            if (i >= first && i < first + kRankTokens && key < D.zero.V)
+                D.zero.tags[key] = uint32_t(i);
+        }
+        pairs[i] = p;
+    }
+    if (threadIdx.x < kRankTokens)
+        place[threadIdx.x] = 0;
+    __syncthreads();
+    const int token = threadIdx.x % kRankTokens;
+    const uint64_t mine = pairs[first + token < T ? first + token : first];
+    int below = 0;
+#pragma unroll 8
+    for (int i = threadIdx.x / kRankTokens; i < filled; i += kRankParts)
+        below += pairs[i] < mine;
+    below += __shfl_xor(below, 16);
+    below += __shfl_xor(below, 32);
+    if ((threadIdx.x & 63) < kRankTokens)
+        atomicAdd(&place[token], below);
+    __syncthreads();
+    if (threadIdx.x < kRankTokens && first + token < T) {
+        D.keys[place[token]] = uint32_t(mine >> 32);
+        D.tokens[place[token]] = uint32_t(mine);
     }
 }
 
@@ -248,13 +264,13 @@ __device__ inline void add(float (&f)[N], const float (&g)[N])
 
 constexpr uint32_t kNoKey = 0xffffffffu;    // no id: V is at most 2^30
 
-// The sorted tokens, `chunk` to a team of lanes; the teams of a work-group
-// follow each other.  A lane adds one vector of channels over its team's
-// chunk and writes the sum wherever the id changes.  The sum of an id that
-// reaches over an end of the chunk goes to LDS, where the first team joins
-// the work-group's; one that reaches over an end of the work-group's tokens
-// leaves an fp32 partial sum in each work-group: slot 0 where it began in an
-// earlier one, slot 1 where it begins in this one.
+// The sorted tokens, `chunk` to a team of lanes; up to kMerge teams of a work-
+// group that follow each other make a block.  A lane adds one vector of
+// channels over its team's chunk and writes the sum wherever the id changes.
+// The sum of an id that reaches over an end of the chunk goes to LDS, where
+// the block's first team joins them; one that reaches over an end of the
+// block's tokens leaves an fp32 partial sum in each block: slot 0 where it
+// began in an earlier one, slot 1 where it begins in this one.
 // UNI: teams are whole waves; the chunk's ids and rows are loaded at once, one
 // token a lane, and read from there as scalars.
 template <typename E, typename G, int VW, bool UNI>
@@ -275,11 +291,11 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D
     int team = threadIdx.x >> lanes_log2;
     if constexpr (UNI)
         team = scalar(team);
-    const uint32_t block = fastdiv(blockIdx.x, D.col_groups);
-    const uint32_t a = (blockIdx.x - block * D.col_groups.d) * lanes + lane;
+    const uint32_t group = fastdiv(blockIdx.x, D.col_groups);
+    const uint32_t a = (blockIdx.x - group * D.col_groups.d) * lanes + lane;
     const bool live = a < D.vecs;
     const uint32_t off = vec_offset<VW>(live ? a : 0, D.row);
-    const int64_t begin = block * D.block_tokens + int64_t{team} * D.chunk;
+    const int64_t begin = (int64_t{group} * teams + team) * D.chunk;
     const int n = begin >= D.T ? 0 : D.T - begin < D.chunk ? int(D.T - begin) : D.chunk;
 
     uint32_t my_key = D.V, my_row = 0;          // UNI: of the chunk's token number `lane`
@@ -358,13 +374,15 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D
     if (lane == 0)
         state[team] = flags;
     __syncthreads();
-    if (team != 0)
+    const int merge = teams < kMerge ? teams : kMerge;
+    if (team % merge != 0 || n == 0)
         return;
-    float *partial = D.partials + int64_t{block} * 2 * D.width + int64_t{a} * N;
+    const int64_t block = (int64_t{group} * teams + team) / merge;
+    float *partial = D.partials + block * 2 * D.width + int64_t{a} * N;
     bool open = false;                  // a sum that goes on into the next team
     head = false;
     clear(acc);
-    for (int t = 0; t < teams; ++t) {
+    for (int t = team; t < team + merge; ++t) {
         const int s = state[t];
         const float(&h)[N] = sums[0][(t << lanes_log2) + lane], (&tail)[N] = sums[1][(t << lanes_log2) + lane];
         if (s & HEAD) {
@@ -394,9 +412,9 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D
         store_values<float, N>(reinterpret_cast<char *>(head ? partial : partial + D.width), acc);
 }
 
-// The ids whose tokens lie in several work-groups of chunk_sum_kernel: the
-// work-group for the one in which an id begins adds its partial sums, each
-// wave a consecutive part of them, and then the waves' sums in order.
+// The ids whose tokens lie in several blocks of chunk_sum_kernel: the work-
+// group for the block in which an id begins adds its partial sums, each wave a
+// consecutive part of them, and then the waves' sums in order.
 constexpr int kJoinWaves = 4;
 
 template <typename E, typename G, int VW>
@@ -410,7 +428,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const GradDesc D)
         const uint32_t key = D.keys[end - 1];
         if (key >= D.V || D.keys[end] != key || (begin > 0 && D.keys[begin - 1] == key))
             continue;
-        // work-groups whose first token still has this id
+        // blocks whose first token still has this id
         int64_t n = 1;
         for (;;) {
             const int64_t first = (block + n + lane) * D.block_tokens;
@@ -505,7 +523,7 @@ basp_status launch_lookup(const basp_embed_plan &p, const void *ids, const void 
     return s;
 }
 
-constexpr int64_t kBesideCount = int64_t{24} << 20, kBesidePlace = int64_t{64} << 20;  // bytes of zeros
+constexpr int64_t kBesideCount = int64_t{32} << 20, kBesidePlace = int64_t{96} << 20;  // bytes of zeros
 
 basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *dout, float scale, int accumulate,
                         void *dtable, void *ws, void *stream)
@@ -544,16 +562,8 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
         return Z.z.groups;
     };
     if (p.T && p.sort_blocks == 0) {
-        OneDesc D = {};
-        for (int i = 0; i < 2; ++i) {
-            D.keys[i] = keys[i];
-            D.tokens[i] = tokens[i];
-        }
-        D.passes = p.passes;
-        D.digit_bits = p.digit_bits;
-        D.zero = Z;
-        go(reinterpret_cast<const void *>(digit_sort_kernel), dim3(1), 64 * kOneWaves, D, false,
-           sort_lds_bytes(kOneWaves, 1 << p.digit_bits));
+        const RankDesc D = {keys[(p.passes - 1) & 1], tokens[(p.passes - 1) & 1], Z};
+        go(reinterpret_cast<const void *>(rank_kernel), dim3(groups_of(p.T, kRankTokens)), kRankThreads, D, false, 0);
     }
     for (int pass = 0; pass < p.passes && p.sort_blocks > 0 && p.T; ++pass) {
         PassDesc D = {};
@@ -573,8 +583,9 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
            size_t(4) * D.bins);
         const uint32_t with_place = share(kBesidePlace, kSortWaves);
         D.zero = Z;
-        go(p.block_items <= kSortItems ? reinterpret_cast<const void *>(digit_place_kernel<kSortSteps>)
-                                       : reinterpret_cast<const void *>(digit_place_kernel<0>),
+        go(p.block_items <= kSortItems       ? reinterpret_cast<const void *>(digit_place_kernel<kSortSteps>)
+           : p.block_items <= 4 * kSortItems ? reinterpret_cast<const void *>(digit_place_kernel<4 * kSortSteps>)
+                                             : reinterpret_cast<const void *>(digit_place_kernel<0>),
            dim3(p.sort_blocks + with_place), kSortBlock, D, false, sort_lds_bytes(kSortWaves, D.bins));
     }
     const int vw = row_vector(p.D, p.es), sorted = (p.passes - 1) & 1;
@@ -587,7 +598,7 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
     D.partials = reinterpret_cast<float *>(base + p.partials);
     D.T = p.T;
     D.width = p.width;
-    D.block_tokens = int64_t{p.chunk} * (kSumThreads >> p.lanes_log2);
+    D.block_tokens = int64_t{p.chunk} * merged_teams(p.lanes_log2);
     D.V = uint32_t(p.V);
     D.blocks = uint32_t(p.blocks);
     D.row = uint32_t(p.D * p.es);
@@ -597,7 +608,7 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
     D.col_groups = make_fastdiv(uint32_t(p.col_groups));
     D.lanes_log2 = p.lanes_log2;
     D.chunk = p.chunk;
-    D.sum_groups = uint32_t(p.blocks * p.col_groups);
+    D.sum_groups = uint32_t(p.sum_groups);
     D.order = p.order;
     D.scale = scale;
     D.accumulate = accumulate != 0;

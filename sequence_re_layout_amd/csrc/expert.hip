@@ -76,11 +76,12 @@ __global__ __launch_bounds__(kSortBlock) void expert_place_kernel(const SortDesc
 }
 
 // Rows without a slot are few as a rule: work-groups of their own look
-// through `order`, 64 rows in one go, and share out what they find.
+// through `order`, up to 64 rows in one go, and share out what they find.
 struct ZeroDesc {
     char *out;
     const int32_t *order;
-    uint32_t max_rows, slots, row, groups;
+    uint32_t max_rows, slots, row;
+    uint32_t look, groups;          // rows in one go, work-groups
 };
 
 constexpr int64_t kZeroGroups = 1 << 20;
@@ -89,12 +90,12 @@ __device__ inline void zero_unnamed(const ZeroDesc &D, uint32_t group)
 {
     constexpr int WAVES = kThreads / 64;
     const int lane = threadIdx.x & 63, wave = scalar(threadIdx.x >> 6);
-    for (uint32_t r0 = group * 64; r0 < D.max_rows; r0 += D.groups * 64) {
+    for (uint32_t r0 = group * D.look; r0 < D.max_rows; r0 += D.groups * D.look) {
         const uint32_t r = r0 + lane;
-        uint64_t m = __ballot(r < D.max_rows && uint32_t(D.order[r]) >= D.slots);
+        uint64_t m = __ballot(uint32_t(lane) < D.look && r < D.max_rows && uint32_t(D.order[r]) >= D.slots);
         for (int n = 0; m; ++n, m &= m - 1)
             if (n % WAVES == wave)
-                zero_span(D.out + uint64_t(r0 + __builtin_ctzll(m)) * D.row, D.row, lane);
+                zero_span(D.out + uint64_t(r0 + __builtin_ctzll(m)) * D.row, D.row, lane, 64);
     }
 }
 
@@ -300,7 +301,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const GradDesc D
             const uint32_t off = vec_offset<VW>(a, D.row);
             const uint32_t seen = (a * VW - off) / sizeof(E);   // elements the vector before holds too
             float g[N];
-            unpack<E, VW>(load_vec<VW>(dout + off), g);
+            unpack<E, VW>(load_vec<VW, false>(dout + off), g);
             typename MemVec<VW>::type x[KB];
 #pragma unroll
             for (int j = 0; j < KB; ++j)
@@ -362,8 +363,10 @@ SortDesc sort_desc(const basp_expert_plan &p, const void *ids, int32_t *pos, int
 basp_status launch_sort(const basp_expert_plan &p, const SortDesc &D, void *stream, bool last)
 {
     const dim3 grid(p.sort_blocks);
-    const void *place = p.block_items <= kSortItems ? reinterpret_cast<const void *>(expert_place_kernel<kSortSteps>)
-                                                    : reinterpret_cast<const void *>(expert_place_kernel<0>);
+    const void *place =
+        p.block_items <= kSortItems       ? reinterpret_cast<const void *>(expert_place_kernel<kSortSteps>)
+        : p.block_items <= 4 * kSortItems ? reinterpret_cast<const void *>(expert_place_kernel<4 * kSortSteps>)
+                                          : reinterpret_cast<const void *>(expert_place_kernel<0>);
     basp_status s = BASP_OK;
     if (p.sort_blocks > 1)
         s = launch_kernel(reinterpret_cast<const void *>(expert_count_kernel), grid, kSortBlock, D, stream, true, false,
@@ -404,8 +407,10 @@ RowShape row_shape(const basp_expert_plan &p)
 
 ZeroDesc zero_desc(const basp_expert_plan &p, int64_t row, const int32_t *order, void *out)
 {
-    return {static_cast<char *>(out), order, uint32_t(p.max_rows), uint32_t(p.slots), uint32_t(row),
-            uint32_t(std::min(kZeroGroups, (p.max_rows + 63) / 64))};
+    // one row a wave while that does not fill the device
+    const int64_t look = std::min<int64_t>(64, std::max<int64_t>(kThreads / 64, p.max_rows / 1024));
+    return {static_cast<char *>(out), order, uint32_t(p.max_rows), uint32_t(p.slots), uint32_t(row), uint32_t(look),
+            uint32_t(std::min(kZeroGroups, (p.max_rows + look - 1) / look))};
 }
 
 template <int VW>

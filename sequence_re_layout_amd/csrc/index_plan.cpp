@@ -163,8 +163,8 @@ extern "C" basp_embed_plan *basp_embed_plan_create(const basp_plan *layout, int6
     int chunk = 32;
     while (chunk > 8 && ceil_div(T, chunk * teams) * cols < kSumGroups)
         chunk /= 2;
-    const int64_t blocks = ceil_div(T, chunk * teams);
-    if (blocks > kSumLimit / cols) {
+    const int64_t groups = ceil_div(T, chunk * teams);
+    if (groups > kSumLimit / cols) {
         record(BASP_ERR_UNSUPPORTED);
         return nullptr;
     }
@@ -201,12 +201,13 @@ extern "C" basp_embed_plan *basp_embed_plan_create(const basp_plan *layout, int6
     p->passes = (bits + basp::kDigitBits - 1) / basp::kDigitBits;
     p->digit_bits = (bits + p->passes - 1) / p->passes;
     split_sort(T, p->sort_blocks, p->block_items);
-    if (T <= basp::kOneItems)
+    if (T <= basp::kRankMost)
         p->sort_blocks = 0;
     p->lanes_log2 = lanes_log2;
     p->chunk = chunk;
-    p->blocks = blocks;
+    p->blocks = ceil_div(T, int64_t{chunk} * basp::merged_teams(lanes_log2));
     p->col_groups = int32_t(cols);
+    p->sum_groups = groups * cols;
     p->width = vecs * epv;
     int64_t at = 0;
     const auto take = [&at](int64_t bytes) {

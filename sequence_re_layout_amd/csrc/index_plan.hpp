@@ -38,12 +38,13 @@ struct basp_embed_plan {
     int32_t es, grad_es;
     basp_seq_order order;
     int32_t passes, digit_bits;     // of the sort by id
-    int32_t sort_blocks;            // work-groups of a pass; 0: one does all passes
+    int32_t sort_blocks;            // work-groups of a pass; 0: sorted by counting alone
     int64_t block_items;
     int32_t lanes_log2;             // lanes of a team: one vector of channels each
     int32_t chunk;                  // sorted tokens that a team sums
-    int64_t blocks;                 // work-groups along the tokens
-    int32_t col_groups;             // and along the channels
+    int64_t blocks;                 // of tokens, each with two partial sums
+    int32_t col_groups;             // work-groups along the channels
+    int64_t sum_groups;             // and of all
     int64_t width;                  // channels of a partial sum, whole vectors
     // byte offsets in the workspace
     int64_t keys[2], tokens[2], tags, hist, partials;
@@ -54,14 +55,19 @@ namespace basp {
 
 constexpr int kSortWaves = 8;               // waves of a sort's work-group
 constexpr int kSortBlock = 64 * kSortWaves;
-constexpr int kSortSteps = 4;               // items of a lane that it keeps in registers
+constexpr int kSortSteps = 2;               // items of a lane that it keeps in registers: 2 or 8
 constexpr int kSortItems = kSortBlock * kSortSteps;
 constexpr int kMaxExperts = 1024;
 constexpr int kDigitBits = 9;               // of one pass of a sort by id
-constexpr int kOneWaves = 16;               // of the work-group that sorts by itself
-constexpr int kOneSteps = 8;
-constexpr int kOneItems = 64 * kOneWaves * kOneSteps;
+constexpr int kRankMost = 8192;             // tokens that are sorted by counting alone
 constexpr int kSumThreads = 256;
+constexpr int kMerge = 8;                   // teams that join their sums in LDS, at most
+
+// Teams of 2^lanes_log2 lanes.
+inline int merged_teams(int lanes_log2)
+{
+    return (kSumThreads >> lanes_log2) < kMerge ? kSumThreads >> lanes_log2 : kMerge;
+}
 
 BASP_HD inline uint32_t seq_row(const basp_seq_order &o, uint32_t t)
 {

@@ -110,14 +110,14 @@ __device__ inline uint32_t vec_offset(uint32_t a, uint32_t row)
 // Lane-uniform values as scalars.
 __device__ inline uint32_t scalar(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// Zeros, written by the 64 lanes of a wave: n bytes (an even number).
-__device__ inline void zero_span(char *p, uint32_t n, int lane)
+// n bytes of zeros (an even number), written by `lanes` lanes (at least 8).
+__device__ inline void zero_span(char *p, uint32_t n, uint32_t lane, uint32_t lanes)
 {
     if (n >= 16) {
         const u32x4m z = {0, 0, 0, 0};
-        for (uint32_t off = lane * 16; off < n; off += 64 * 16)
+        for (uint32_t off = lane * 16; off < n; off += lanes * 16)
             store_vec<16>(p + (off < n - 16 ? off : n - 16), z);
-    } else if (uint32_t(lane) * 2 < n) {
+    } else if (lane * 2 < n) {
         store_vec<2>(p + lane * 2, uint16_t(0));
     }
 }
@@ -130,17 +130,18 @@ __device__ inline void zero_rows_of(char *buffer, uint32_t first, uint64_t which
         const int i = __builtin_ctzll(which);
         const uint64_t from = which >> i;
         const int n = ~from ? __builtin_ctzll(~from) : 64;
-        zero_span(buffer + uint64_t(first + i) * row, n * row, lane);
+        zero_span(buffer + uint64_t(first + i) * row, n * row, lane, 64);
         which = i + n < 64 ? from >> n << (i + n) : 0;
     }
 }
 
 // Writing zeros into some rows of a buffer.  The buffer is cut into pieces of
-// up to 4 KiB: several short rows, one row, or a part of a long one.  A wave
-// writes a piece; neighbouring pieces belong to neighbouring work-groups, and
-// a work-group's own `per` pieces lie `stride` pieces apart.  Measured on
-// 512 MiB: 6.4-6.8 TB/s in this order, against 5.0-5.8 TB/s where a work-group
-// writes 16 KiB or more in a row, and 4.1-4.7 TB/s from a grid that loops.
+// up to 4 KiB: several short rows, one row, or a part of a long one.  Four
+// waves write a piece (or one wave a piece of short rows); neighbouring pieces
+// belong to neighbouring work-groups, and a work-group's own `per` pieces lie
+// `stride` pieces apart.  Measured on 512 MiB: 6.4-6.8 TB/s in this order,
+// against 5.0-5.8 TB/s where a work-group writes 16 KiB or more in a row, and
+// 4.1-4.7 TB/s from a grid that loops.
 struct ZeroPieces {
     uint32_t row, rows, parts;      // bytes of a row; rows of a piece, or pieces of a row
     uint32_t begin, end;            // rows of the buffer
@@ -160,8 +161,8 @@ inline ZeroPieces zero_pieces(int64_t begin, int64_t end, int64_t row, int waves
     z.begin = uint32_t(begin);
     z.end = uint32_t(end);
     z.pieces = (n + z.rows - 1) / z.rows * z.parts;
-    // one piece a wave while that does not fill the device
-    z.per = z.pieces >= 8192 ? 8 : uint32_t(waves);
+    // few pieces a work-group while that does not fill the device
+    z.per = z.pieces >= 4096 ? 8 : z.rows > 1 ? uint32_t(waves) : uint32_t(waves / 4);
     const uint64_t share = (z.pieces + z.per - 1) / z.per;
     z.stride = uint32_t(share > 256 ? 256 : share);
     const uint64_t sweeps = z.stride ? (share + z.stride - 1) / z.stride : 0;
@@ -174,22 +175,28 @@ template <int WAVES, typename None>
 __device__ inline void write_zeros(char *buffer, const ZeroPieces &z, uint32_t group, None none)
 {
     const uint32_t lane = threadIdx.x & 63, wave = scalar(threadIdx.x >> 6), sweep = z.groups / z.stride;
-    for (uint64_t s = group / z.stride; s * z.stride * z.per < z.pieces; s += sweep)
-        for (uint32_t i = wave; i < z.per; i += WAVES) {
-            const uint64_t piece = (s * z.per + i) * z.stride + group % z.stride;
-            if (piece >= z.pieces)
-                break;
-            if (z.rows > 1) {
-                const uint32_t r0 = z.begin + uint32_t(piece) * z.rows, r = r0 + lane;
+    for (uint64_t s = group / z.stride; s * z.stride * z.per < z.pieces; s += sweep) {
+        const auto piece_of = [&](uint32_t i) { return (s * z.per + i) * z.stride + group % z.stride; };
+        if (z.rows > 1) {
+            for (uint32_t i = wave; i < z.per && piece_of(i) < z.pieces; i += WAVES) {
+                const uint32_t r0 = z.begin + uint32_t(piece_of(i)) * z.rows, r = r0 + lane;
                 const bool is = lane < z.rows && r < z.end && none(r);
                 zero_rows_of(buffer, r0, __ballot(is), z.row, lane);
-            } else {
-                const uint32_t i = uint32_t(piece / z.parts), part = uint32_t(piece - uint64_t(i) * z.parts) * kPiece;
-                if (none(z.begin + i))
-                    zero_span(buffer + uint64_t(z.begin + i) * z.row + part,
-                              z.row - part < kPiece ? z.row - part : kPiece, lane);
             }
+            continue;
         }
+        // every wave looks at all the pieces, a lane at one
+        const uint64_t mine = piece_of(lane);
+        const uint32_t r = z.begin + uint32_t(mine / z.parts), part = uint32_t(mine % z.parts) * kPiece;
+        const bool is = lane < z.per && mine < z.pieces && none(r);
+        const uint64_t which = __ballot(is);
+        for (uint32_t i = wave / 4; i < z.per; i += WAVES / 4)
+            if (which >> i & 1) {
+                const uint32_t row = __builtin_amdgcn_readlane(r, i), at = __builtin_amdgcn_readlane(part, i);
+                zero_span(buffer + uint64_t(row) * z.row + at, z.row - at < kPiece ? z.row - at : kPiece,
+                          threadIdx.x & 255, 256);
+            }
+    }
 }
 
 // One number of 2 or 4 bytes (a router's weight) in fp32, and back.

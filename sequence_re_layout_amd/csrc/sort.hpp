@@ -53,9 +53,10 @@ __device__ inline uint64_t same_bin(int bin, int bits)
 {
     uint64_t m = __ballot(bin >= 0);
     for (int b = 0; b < bits; ++b) {
-        const bool one = (bin >> b) & 1;
-        const uint64_t v = __ballot(one);
-        m &= one ? v : ~v;
+        const int bit = (bin >> b) & 1;
+        const uint64_t v = __ballot(bit);
+        const uint32_t flip = bit - 1;      // all ones where the bit is clear
+        m &= v ^ (uint64_t{flip} << 32 | flip);
     }
     return m;
 }
@@ -95,6 +96,8 @@ __device__ inline void sort_sum_groups(const SortLds &l, const int *hist, int bi
     }
 }
 
+__device__ inline int round_up(int n, int to) { return to == 1 ? n : (n + to - 1) / to * to; }
+
 // From the waves' counts (l.count), and with more than one group the totals
 // and the counts before this group: the starts, an exclusive sum over the
 // bins, a few consecutive ones a thread; and in l.count the place of each
@@ -105,38 +108,48 @@ __device__ inline void sort_starts(const SortLds &l, int bins, int align, int gr
     constexpr int NT = WAVES * 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int per = (bins + NT - 1) / NT, e0 = tid * per;
+    const bool has = wave * 64 * per < bins;     // the wave has bins
     int sum = 0;
-    for (int j = 0; j < per && e0 + j < bins; ++j) {
-        const int e = e0 + j;
-        if (groups == 1) {
-            int n = 0;
+    if (has) {
+        for (int j = 0; j < per && e0 + j < bins; ++j) {
+            const int e = e0 + j;
+            if (groups == 1) {
+                int n = 0;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w)
+                    n += l.count[w * bins + e];
+                l.total[e] = n;
+            }
+            sum += round_up(l.total[e], align);
+        }
+        const int upto = wave_inclusive_sum(sum, lane);
+        if (lane == 63)
+            l.scan[wave] = upto;
+        sum = upto - sum;
+    }
+    __syncthreads();
+    if (has) {
+        int at = sum;
+        for (int w = 0; w < wave; ++w)
+            at += l.scan[w];
+        for (int j = 0; j < per && e0 + j < bins; ++j) {
+            const int e = e0 + j;
+            int next = at + (groups == 1 ? 0 : l.start[e]);
+            int n[WAVES];               // read before the first is written: one wait for all
 #pragma unroll
             for (int w = 0; w < WAVES; ++w)
-                n += l.count[w * bins + e];
-            l.total[e] = n;
-        }
-        sum += (l.total[e] + align - 1) / align * align;
-    }
-    const int upto = wave_inclusive_sum(sum, lane);
-    if (lane == 63)
-        l.scan[wave] = upto;
-    __syncthreads();
-    int at = upto - sum;
-    for (int w = 0; w < wave; ++w)
-        at += l.scan[w];
-    for (int j = 0; j < per && e0 + j < bins; ++j) {
-        const int e = e0 + j;
-        int next = at + (groups == 1 ? 0 : l.start[e]);
-        l.start[e] = at;
+                n[w] = l.count[w * bins + e];
+            const int total = l.total[e];
+            l.start[e] = at;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            const int n = l.count[w * bins + e];
-            l.count[w * bins + e] = next;
-            next += n;
+            for (int w = 0; w < WAVES; ++w) {
+                l.count[w * bins + e] = next;
+                next += n[w];
+            }
+            at += round_up(total, align);
+            if (e == bins - 1)
+                l.start[bins] = at;
         }
-        at += (l.total[e] + align - 1) / align * align;
-        if (e == bins - 1)
-            l.start[bins] = at;
     }
     __syncthreads();
 }
