@@ -183,7 +183,7 @@ __global__ __launch_bounds__(kRankThreads) void rank_kernel(const RankDesc D)
     }
     if (threadIdx.x < kRankTokens)
         place[threadIdx.x] = 0;
-    __syncthreads();
+    lds_barrier();
     const int token = threadIdx.x % kRankTokens;
     const uint64_t mine = pairs[first + token < T ? first + token : first];
     int below = 0;
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kRankThreads) void rank_kernel(const RankDesc D)
     below += __shfl_xor(below, 32);
     if ((threadIdx.x & 63) < kRankTokens)
         atomicAdd(&place[token], below);
-    __syncthreads();
+    lds_barrier();
     if (threadIdx.x < kRankTokens && first + token < T) {
         D.keys[place[token]] = uint32_t(mine >> 32);
         D.tokens[place[token]] = uint32_t(mine);
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D
     }
     if (lane == 0)
         state[team] = flags;
-    __syncthreads();
+    lds_barrier();
     const int merge = teams < kMerge ? teams : kMerge;
     if (team % merge != 0 || n == 0)
         return;
@@ -455,13 +455,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const GradDesc D)
 #pragma unroll
             for (int e = 0; e < N; ++e)
                 sums[wave][lane][e] = acc[e];
-            __syncthreads();
+            lds_barrier();
             if (wave == 0 && a < D.vecs) {
                 for (int w = 1; w < kJoinWaves; ++w)
                     add(acc, sums[w][lane]);
                 write_grad<G, N>(D, key, a, acc);
             }
-            __syncthreads();
+            lds_barrier();
         }
     }
 }

@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const RouteDesc D)
             if (at >= first && at < first + rows)
                 slot_of[at - first] = int(i);
         });
-    __syncthreads();
+    lds_barrier();
     if (blockIdx.x == 0) {
         for (int e = tid; e < S.E; e += kThreads)
             S.counts[e] = l.total[e];
@@ -262,28 +262,66 @@ struct GradDesc {
     const void *weights;
     void *dweights;
     uint32_t tokens, row, vecs;
-    int32_t K, lanes_log2;          // lanes that share a token
+    int32_t K, lanes_log2;          // lanes that share a token: 8 to 256
     uint32_t max_rows;
     uint32_t token_groups;          // work-groups of the tokens; the others write zeros
     basp_dtype weight_dtype;
     ZeroDesc zero;
 };
 
-// The gradient of expert -> seq.  2^lanes_log2 lanes (up to the whole work-
-// group) take a token: each reads its vectors of dout once, and per slot
-// reads the row's vector, adds the product to the slot's dot product and
-// writes the weighted dout.  The dot products are then summed over the lanes.
-template <typename E, int VW, int KB>
+// The sums of KB values over `span` lanes (a power of two, at least KB), one
+// of them to a lane: lane l gets that of value summed_by<KB>(l).  Half of the
+// values go to the other lane of a pair in each of the first steps, so that
+// a wave sums 8 values in 10 exchanges instead of 48.
+template <int KB>
+__device__ inline int summed_by(int lane)
+{
+    int j = 0;
+#pragma unroll
+    for (int b = 1; b < KB; b <<= 1)
+        j = j << 1 | ((lane & b) != 0);
+    return j;
+}
+
+template <int KB>
+__device__ inline float sum_over_lanes(float (&v)[KB], int lane, int span)
+{
+#pragma unroll
+    for (int b = 1; b < KB; b <<= 1) {
+        const bool upper = lane & b;
+        const int half = KB / (2 * b);
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float keep = upper ? v[i + half] : v[i], send = upper ? v[i] : v[i + half];
+            v[i] = keep + __shfl_xor(send, b);
+        }
+    }
+    float sum = v[0];
+#pragma unroll
+    for (int d = KB; d < 64; d <<= 1)
+        if (d < span)
+            sum += __shfl_xor(sum, d);
+    return sum;
+}
+
+// The gradient of expert -> seq.  2^lanes_log2 lanes (8 up to the whole work-
+// group) take a token: each reads its vectors of dout, and per slot reads the
+// row's vector, adds the product to the slot's dot product and writes the
+// weighted dout.  The dot products are then summed over the lanes.
+// UNI: a token takes whole waves, so that its index and weights are scalars.
+template <typename E, int VW, int KB, bool UNI>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const GradDesc D)
 {
     constexpr int N = VW / sizeof(E), WAVES = kThreads / 64;
-    __shared__ float part[WAVES][KB];
+    __shared__ float part[2][WAVES][KB];
     if (blockIdx.x >= D.token_groups) {
         zero_unnamed(D.zero, blockIdx.x - D.token_groups);
         return;
     }
     const uint32_t lanes = 1u << D.lanes_log2, lane = threadIdx.x & (lanes - 1);
-    const uint32_t t = blockIdx.x * (kThreads >> D.lanes_log2) + (threadIdx.x >> D.lanes_log2);
+    uint32_t t = blockIdx.x * (kThreads >> D.lanes_log2) + (threadIdx.x >> D.lanes_log2);
+    if constexpr (UNI)
+        t = scalar(t);
     const bool live = t < D.tokens;
     const uint64_t slot = uint64_t(t) * D.K;
     const char *dout = D.dout + uint64_t(t) * D.row;
@@ -320,34 +358,23 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const GradDesc D
                     store_vec<VW>(D.drows + uint64_t(p[j]) * D.row + off, pack<E, VW>(y));
                 }
         }
-        const uint32_t span = lanes < 64 ? lanes : 64;
-#pragma unroll
-        for (int j = 0; j < KB; ++j)
-#pragma unroll
-            for (uint32_t d = 1; d < 64; d <<= 1) {
-                const float o = __shfl_xor(dot[j], d);
-                dot[j] += d < span ? o : 0.f;
-            }
+        const int wave = threadIdx.x >> 6, l = threadIdx.x & 63, j = summed_by<KB>(l);
+        float sum = sum_over_lanes<KB>(dot, l, lanes < 64 ? lanes : 64);
         if (lanes > 64) {
-            __syncthreads();           // the last batch's sums have been read
-            if ((threadIdx.x & 63) == 0)
-#pragma unroll
-                for (int j = 0; j < KB; ++j)
-                    part[threadIdx.x >> 6][j] = dot[j];
-            __syncthreads();
-            const uint32_t w0 = (threadIdx.x >> D.lanes_log2) << (D.lanes_log2 - 6), nw = lanes >> 6;
-#pragma unroll
-            for (int j = 0; j < KB; ++j) {
-                dot[j] = 0.f;
-                for (uint32_t i = 0; i < nw; ++i)
-                    dot[j] += part[w0 + i][j];
+            // batches use the two halves of `part` in turn: the barrier of the
+            // next one lies between a read here and the write after it
+            float(&mine)[WAVES][KB] = part[k0 / KB & 1];
+            if (l < KB)
+                mine[wave][j] = sum;
+            lds_barrier();
+            if (lane < KB) {
+                sum = mine[wave][j];
+                for (uint32_t i = 1; i < lanes >> 6; ++i)
+                    sum += mine[wave + i][j];
             }
         }
-        if (lane == 0 && live)
-#pragma unroll
-            for (int j = 0; j < KB; ++j)
-                if (k0 + j < D.K)
-                    store_number(D.dweights, slot + k0 + j, D.weight_dtype, dot[j]);
+        if (lane < KB && live && k0 + j < D.K)
+            store_number(D.dweights, slot + k0 + j, D.weight_dtype, sum);
     }
 }
 
@@ -439,13 +466,23 @@ const void *sum_fn(int K, bool weighted, bool uni)
                     : sum_fn<E, VW, 8>(weighted, uni);
 }
 
-template <typename E, int VW>
-const void *grad_fn(int K)
+// Slots of a token that are in flight at a time: up to 8, or 4 in fp32 (4092
+// tokens of 777 channels, 5 choices: 29.5 us with 4, 33.4 with 8; 16384 tokens
+// of 2048 in bf16, 8 choices: 208 with 4, 205 with 8).
+template <typename E, int VW, bool UNI>
+const void *grad_fn_of(int K)
 {
-    return K == 1   ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 1>)
-           : K == 2 ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 2>)
-           : K <= 4 ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 4>)
-                    : reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 8>);
+    constexpr int MOST = sizeof(E) == 4 ? 4 : 8;
+    return K == 1   ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 1, UNI>)
+           : K == 2 ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 2, UNI>)
+           : K <= 4 ? reinterpret_cast<const void *>(combine_grad_kernel<E, VW, 4, UNI>)
+                    : reinterpret_cast<const void *>(combine_grad_kernel<E, VW, MOST, UNI>);
+}
+
+template <typename E, int VW>
+const void *grad_fn(int K, bool uni)
+{
+    return uni ? grad_fn_of<E, VW, true>(K) : grad_fn_of<E, VW, false>(K);
 }
 
 template <int VW>
@@ -531,7 +568,6 @@ basp_status launch_grad(const basp_expert_plan &p, const void *dout, const void 
                         const int32_t *order, const void *weights, void *drows, void *dweights, void *stream)
 {
     const RowShape r = row_shape(p);
-    const void *fn = BASP_BY_ROW(grad_fn, p.dtype, r.vw, p.K);
     GradDesc D = {};
     D.row = uint32_t(r.row);
     D.vecs = uint32_t(r.vecs);
@@ -541,8 +577,10 @@ basp_status launch_grad(const basp_expert_plan &p, const void *dout, const void 
     D.weight_dtype = p.weight_dtype;
     D.rows = static_cast<const char *>(rows);
     D.drows = static_cast<char *>(drows);
+    D.lanes_log2 = 3;
     while (D.lanes_log2 < 8 && (int64_t{1} << D.lanes_log2) < r.vecs)
         ++D.lanes_log2;
+    const void *fn = BASP_BY_ROW(grad_fn, p.dtype, r.vw, p.K, D.lanes_log2 >= 6);
     const int64_t per_group = kThreads >> D.lanes_log2, step = (int64_t{1} << 22) * per_group;
     basp_status s = BASP_OK;
     for (int64_t t0 = 0; t0 < p.T && s == BASP_OK; t0 += step) {

@@ -19,6 +19,16 @@
 
 namespace basp {
 
+// A barrier for what the work-group has in LDS alone.  __syncthreads() also
+// waits until every store to memory has arrived, which takes microseconds and
+// which nobody here reads.
+__device__ inline void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // LDS of one work-group: counters [waves][bins], the bins' totals, starts
 // (bins + 1) and a scratch word per wave.
 struct SortLds {
@@ -127,7 +137,7 @@ __device__ inline void sort_starts(const SortLds &l, int bins, int align, int gr
             l.scan[wave] = upto;
         sum = upto - sum;
     }
-    __syncthreads();
+    lds_barrier();
     if (has) {
         int at = sum;
         for (int w = 0; w < wave; ++w)
@@ -151,7 +161,7 @@ __device__ inline void sort_starts(const SortLds &l, int bins, int align, int gr
                 l.start[bins] = at;
         }
     }
-    __syncthreads();
+    lds_barrier();
 }
 
 __device__ inline int bits_of(int bins)
@@ -212,7 +222,7 @@ __device__ inline void sort_place(const SortLds &l, int64_t begin, int64_t end, 
             l.count[i] = 0;
         for (int i = tid; i < bins; i += NT)
             l.total[i] = l.start[i] = 0;
-        __syncthreads();
+        lds_barrier();
         if (groups > 1)
             sort_sum_groups<WAVES>(l, hist, bins, groups, group);
         int rank[R > 0 ? R : 1];
@@ -220,7 +230,7 @@ __device__ inline void sort_place(const SortLds &l, int64_t begin, int64_t end, 
         for (int r = 0; r < R; ++r)
             if (w0 + r * 64 < w1)        // the same for all lanes of a wave
                 rank[r] = wave_rank(mine, w0 + r * 64 + lane < w1 ? bin(k[r]) : -1, bits, below);
-        __syncthreads();
+        lds_barrier();
         sort_starts<WAVES>(l, bins, align, groups);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -235,7 +245,7 @@ __device__ inline void sort_place(const SortLds &l, int64_t begin, int64_t end, 
             l.count[i] = 0;
         for (int i = tid; i < bins; i += NT)
             l.total[i] = l.start[i] = 0;
-        __syncthreads();
+        lds_barrier();
         if (groups > 1)
             sort_sum_groups<WAVES>(l, hist, bins, groups, group);
         for (int64_t i = w0 + lane; i < w1; i += 64) {
@@ -243,7 +253,7 @@ __device__ inline void sort_place(const SortLds &l, int64_t begin, int64_t end, 
             if (e >= 0)
                 atomicAdd(&mine[e], 1);
         }
-        __syncthreads();
+        lds_barrier();
         sort_starts<WAVES>(l, bins, align, groups);
         for (int64_t i0 = w0; i0 < w1; i0 += 64) {   // the same for all lanes of a wave
             const int64_t i = i0 + lane;
@@ -268,7 +278,7 @@ __device__ inline void sort_count(int *count, int64_t begin, int64_t end, int bi
     constexpr int NT = WAVES * 64, U = 4;
     for (int i = threadIdx.x; i < bins; i += NT)
         count[i] = 0;
-    __syncthreads();
+    lds_barrier();
     for (int64_t i0 = begin + threadIdx.x; i0 < end; i0 += NT * U) {
         int e[U];
 #pragma unroll
@@ -279,7 +289,7 @@ __device__ inline void sort_count(int *count, int64_t begin, int64_t end, int bi
             if (e[u] >= 0)
                 atomicAdd(&count[e[u]], 1);
     }
-    __syncthreads();
+    lds_barrier();
     for (int i = threadIdx.x; i < bins; i += NT)
         hist[i] = count[i];
 }
