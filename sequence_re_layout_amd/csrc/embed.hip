@@ -112,14 +112,6 @@ __device__ inline uint32_t pass_key(const PassDesc &D, int64_t i)
     return D.first ? row_of_id(D.zero.ids, i, D.zero.V, D.zero.padding, D.zero.wide_ids) : D.keys_in[i];
 }
 
-__device__ inline void pass_emit(const PassDesc &D, int64_t i, uint32_t key, int at)
-{
-    if (at >= 0 && at < D.zero.T) {
-        D.keys_out[at] = key;
-        D.tokens_out[at] = D.first ? uint32_t(i) : D.tokens_in[i];
-    }
-}
-
 __global__ __launch_bounds__(kSortBlock) void digit_count_kernel(const PassDesc D)
 {
     extern __shared__ int lds[];
@@ -147,9 +139,16 @@ __global__ __launch_bounds__(kSortBlock) void digit_place_kernel(const PassDesc 
     const int64_t T = D.zero.T, begin = blockIdx.x * D.items, end = begin + D.items < T ? begin + D.items : T;
     sort_place<kSortWaves, R>(
         sort_lds(lds, kSortWaves, D.bins), begin, end, D.bins, 1, D.hist, D.groups, blockIdx.x,
-        [&](int64_t i) { return pass_key(D, i); },
-        [&](uint32_t key) { return int(key >> D.shift) & (D.bins - 1); },
-        [&](int64_t i, uint32_t key, int at) { pass_emit(D, i, key, at); });
+        [&](int64_t i) -> uint64_t {
+            return uint64_t(D.first ? uint32_t(i) : D.tokens_in[i]) << 32 | pass_key(D, i);
+        },
+        [&](uint64_t pair) { return int(uint32_t(pair) >> D.shift) & (D.bins - 1); },
+        [&](int64_t, uint64_t pair, int at) {
+            if (at >= 0 && at < T) {
+                D.keys_out[at] = uint32_t(pair);
+                D.tokens_out[at] = uint32_t(pair >> 32);
+            }
+        });
 }
 
 // A small sort in one launch, by counting: a token's place is the number of

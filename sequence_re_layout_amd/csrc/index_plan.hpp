@@ -58,7 +58,7 @@ constexpr int kSortBlock = 64 * kSortWaves;
 constexpr int kSortSteps = 2;               // items of a lane that it keeps in registers: 2 or 8
 constexpr int kSortItems = kSortBlock * kSortSteps;
 constexpr int kMaxExperts = 1024;
-constexpr int kDigitBits = 9;               // of one pass of a sort by id
+constexpr int kDigitBits = 10;              // of one pass of a sort by id
 constexpr int kRankMost = 8192;             // tokens that are sorted by counting alone
 constexpr int kSumThreads = 256;
 constexpr int kMerge = 8;                   // teams that join their sums in LDS, at most

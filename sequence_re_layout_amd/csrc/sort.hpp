@@ -88,13 +88,21 @@ __device__ inline void sort_sum_groups(const SortLds &l, const int *hist, int bi
     while (span < bins && span < NT)
         span <<= 1;
     const int rows = NT / span, g0 = threadIdx.x / span;
+    constexpr int U = 16;               // counts in flight
     for (int e = threadIdx.x & (span - 1); e < bins; e += span) {
         int total = 0, before = 0;
-#pragma unroll 8
-        for (int g = g0; g < groups; g += rows) {
-            const int n = hist[int64_t{g} * bins + e];
-            total += n;
-            before += g < group ? n : 0;
+        for (int g1 = g0; g1 < groups; g1 += U * rows) {
+            int n[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int g = g1 + u * rows;
+                n[u] = g < groups ? hist[int64_t{g} * bins + e] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                total += n[u];
+                before += g1 + u * rows < group ? n[u] : 0;
+            }
         }
         if (rows == 1) {
             l.total[e] = total;
