@@ -214,12 +214,12 @@ struct GradDesc {
     uint32_t sum_groups;            // work-groups that sum; the others write zeros
     basp_seq_order order;
     float scale;
-    int32_t accumulate;
     ZeroDesc zero;
 };
 
-// The channels of vector a of table row `key`, scaled, as they are written.
-template <typename G, int N>
+// The channels of vector a of table row `key`, scaled: written, or with ACC
+// added to what is there.
+template <typename G, bool ACC, int N>
 __device__ inline void write_grad(const GradDesc &D, uint32_t key, uint32_t a, const float (&sum)[N])
 {
     const uint32_t first = a * N, last = D.elems - N, at = first < last ? first : last;
@@ -228,7 +228,7 @@ __device__ inline void write_grad(const GradDesc &D, uint32_t key, uint32_t a, c
 #pragma unroll
     for (int i = 0; i < N; ++i)
         f[i] = sum[i] * D.scale;
-    if (D.accumulate) {
+    if constexpr (ACC) {
         if (at != first) {             // the vector before adds the channels both hold
             for (int i = int(first - at); i < N; ++i) {
                 G *q = reinterpret_cast<G *>(p) + i;
@@ -272,7 +272,7 @@ constexpr uint32_t kNoKey = 0xffffffffu;    // no id: V is at most 2^30
 // began in an earlier one, slot 1 where it begins in this one.
 // UNI: teams are whole waves; the chunk's ids and rows are loaded at once, one
 // token a lane, and read from there as scalars.
-template <typename E, typename G, int VW, bool UNI>
+template <typename E, typename G, int VW, bool UNI, bool ACC>
 __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D)
 {
     constexpr int N = VW / sizeof(E), U = 8;
@@ -345,7 +345,7 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D
                     keep(0);
                     flags = HEAD;
                 } else if (live) {
-                    write_grad<G, N>(D, key, a, acc);
+                    write_grad<G, ACC, N>(D, key, a, acc);
                 }
                 head = false;
                 key = k[j];
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D
             keep(1);
             flags |= TAIL;
         } else if (live) {
-            write_grad<G, N>(D, key, a, acc);
+            write_grad<G, ACC, N>(D, key, a, acc);
         }
     }
     if (lane == 0)
@@ -394,7 +394,7 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D
                     if (head)
                         store_values<float, N>(reinterpret_cast<char *>(partial), acc);
                     else
-                        write_grad<G, N>(D, key, a, acc);
+                        write_grad<G, ACC, N>(D, key, a, acc);
                 }
                 head = false;
                 clear(acc);
@@ -416,7 +416,7 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(const GradDesc D
 // consecutive part of them, and then the waves' sums in order.
 constexpr int kJoinWaves = 4;
 
-template <typename E, typename G, int VW>
+template <typename E, typename G, int VW, bool ACC>
 __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const GradDesc D)
 {
     constexpr int N = VW / sizeof(E);
@@ -458,7 +458,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const GradDesc D)
             if (wave == 0 && a < D.vecs) {
                 for (int w = 1; w < kJoinWaves; ++w)
                     add(acc, sums[w][lane]);
-                write_grad<G, N>(D, key, a, acc);
+                write_grad<G, ACC, N>(D, key, a, acc);
             }
             lds_barrier();
         }
@@ -480,20 +480,28 @@ struct GradFns {
     const void *sum, *join;
 };
 
-template <typename E, typename G, int VW>
+template <typename E, typename G, int VW, bool ACC>
 GradFns grad_fns_of(bool uni)
 {
-    return {uni ? reinterpret_cast<const void *>(chunk_sum_kernel<E, G, VW, true>)
-                : reinterpret_cast<const void *>(chunk_sum_kernel<E, G, VW, false>),
-            reinterpret_cast<const void *>(join_kernel<E, G, VW>)};
+    const void *join = reinterpret_cast<const void *>(join_kernel<E, G, VW, ACC>);
+    if constexpr (VW == 16)            // narrower vectors are for rows of less than 16 bytes
+        if (uni)
+            return {reinterpret_cast<const void *>(chunk_sum_kernel<E, G, VW, true, ACC>), join};
+    return {reinterpret_cast<const void *>(chunk_sum_kernel<E, G, VW, false, ACC>), join};
+}
+
+template <typename E, typename G, int VW>
+GradFns grad_fns_of(bool uni, bool acc)
+{
+    return acc ? grad_fns_of<E, G, VW, true>(uni) : grad_fns_of<E, G, VW, false>(uni);
 }
 
 template <typename E, int VW>
-GradFns grad_fns(basp_dtype grad, bool uni)
+GradFns grad_fns(basp_dtype grad, bool uni, bool acc)
 {
-    return grad == BASP_FP32   ? grad_fns_of<E, float, VW>(uni)
-           : grad == BASP_BF16 ? grad_fns_of<E, __bf16, VW>(uni)
-                               : grad_fns_of<E, _Float16, VW>(uni);
+    return grad == BASP_FP32   ? grad_fns_of<E, float, VW>(uni, acc)
+           : grad == BASP_BF16 ? grad_fns_of<E, __bf16, VW>(uni, acc)
+                               : grad_fns_of<E, _Float16, VW>(uni, acc);
 }
 
 basp_status launch_lookup(const basp_embed_plan &p, const void *ids, const void *table, float scale, void *out,
@@ -522,7 +530,7 @@ basp_status launch_lookup(const basp_embed_plan &p, const void *ids, const void 
     return s;
 }
 
-constexpr int64_t kBesideCount = int64_t{32} << 20, kBesidePlace = int64_t{96} << 20;  // bytes of zeros
+constexpr int64_t kBesideCount = int64_t{64} << 20, kBesidePlace = int64_t{160} << 20;  // bytes of zeros
 
 basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *dout, float scale, int accumulate,
                         void *dtable, void *ws, void *stream)
@@ -588,7 +596,7 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
            dim3(p.sort_blocks + with_place), kSortBlock, D, false, sort_lds_bytes(kSortWaves, D.bins));
     }
     const int vw = row_vector(p.D, p.es), sorted = (p.passes - 1) & 1;
-    const GradFns fn = BASP_BY_ROW(grad_fns, p.dtype, vw, p.grad_dtype, p.lanes_log2 == 6);
+    const GradFns fn = BASP_BY_ROW(grad_fns, p.dtype, vw, p.grad_dtype, p.lanes_log2 == 6, accumulate != 0);
     GradDesc D = {};
     D.keys = keys[sorted];
     D.tokens = tokens[sorted];
@@ -610,7 +618,6 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
     D.sum_groups = uint32_t(p.sum_groups);
     D.order = p.order;
     D.scale = scale;
-    D.accumulate = accumulate != 0;
     const uint32_t zeros = share(INT64_MAX, kSumThreads / 64);
     D.zero = Z;
     const bool joins = p.blocks > 1;

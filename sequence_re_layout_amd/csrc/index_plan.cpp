@@ -14,7 +14,7 @@ namespace {
 constexpr int64_t kRowLimit = int64_t{1} << 30;     // bytes of a row
 constexpr int64_t kIndexLimit = 0x7fffffff - 1;     // slots, rows, tokens: int32 with -1, and 31-bit division
 constexpr int64_t kVocabLimit = int64_t{1} << 30;
-constexpr int64_t kSumGroups = 512;                 // two work-groups a compute unit
+constexpr int64_t kSumGroups = 1024;                // four work-groups a compute unit
 constexpr int64_t kSumLimit = int64_t{1} << 23;     // work-groups of a launch's 32-bit extent
 
 int float_size(basp_dtype t)

@@ -117,8 +117,8 @@ inline ZeroPieces zero_pieces(int64_t begin, int64_t end, int64_t row, int waves
     z.begin = uint32_t(begin);
     z.end = uint32_t(end);
     z.pieces = (n + z.rows - 1) / z.rows * z.parts;
-    // few pieces a work-group while that does not fill the device
-    z.per = z.pieces >= 4096 ? 8 : z.rows > 1 ? uint32_t(waves) : uint32_t(waves / 4);
+    // one piece a wave, or four waves, while that does not fill the device
+    z.per = z.rows > 1 ? uint32_t(z.pieces >= 4096 ? 8 : waves) : uint32_t(z.pieces >= 4096 ? waves / 2 : waves / 4);
     const uint64_t share = (z.pieces + z.per - 1) / z.per;
     z.stride = uint32_t(share > 256 ? 256 : share);
     const uint64_t sweeps = z.stride ? (share + z.stride - 1) / z.stride : 0;
