@@ -63,7 +63,7 @@ __global__ __launch_bounds__(kSortBlock) void expert_place_kernel(const SortDesc
     // rows without a slot: the padding of this group's share of the experts,
     // and its share of what lies behind the last one
     for (int e = group; e < D.E; e += groups)
-        for (int r = l.start[e] + l.total[e] + tid; r < l.start[e + 1]; r += kSortBlock)
+        for (int64_t r = int64_t{l.start[e]} + l.total[e] + tid; r < l.start[e + 1]; r += kSortBlock)
             D.order[r] = -1;
     for (int64_t r = l.start[D.E] + int64_t{group} * kSortBlock + tid; r < D.max_rows; r += int64_t{groups} * kSortBlock)
         D.order[r] = -1;

@@ -75,6 +75,7 @@ SIZES = [  # layout (N, B, S, groups) or tokens, V, D, dtype, grad, id_bytes, pa
     (5001, 2000, 8, "bf16", "bf16", 8, -1, 0.0),
     (3000, 1500000, 16, "bf16", "bf16", 8, -1, 0.0),
     (700, 40, 9001, "fp16", "fp32", 8, -1, 0.0),
+    (8192, 300, 40, "bf16", "fp32", 8, -1, 0.01),
     (8193, 300, 40, "bf16", "fp32", 8, -1, 0.01),
     ((2, 2, 10000, 1), 70001, 24, "fp16", "bf16", 4, 5, 0.02),
     (9000, 1500000, 9, "bf16", "bf16", 8, -1, 0.0),
@@ -184,3 +185,23 @@ def test_table_past_four_gib():
                        .expand(6, D))
     table[ids] = 0
     assert not bool(table.any())
+
+
+def test_activations_past_four_gib():
+    """Row offsets above 2^32 bytes in the activations, looked up and summed."""
+    T, D, V = 140000, 16384, 9
+    plan = b.basp_embed_plan_create(None, T, V, D)
+    ids = torch.arange(T, device="cuda") % V
+    table = torch.arange(1, V + 1, device="cuda").bfloat16()[:, None].expand(V, D).contiguous()
+    out = torch.full((T, D), NAN, dtype=torch.bfloat16, device="cuda")
+    assert out.numel() * 2 > 2**32
+    b.basp_embed_to_seq(plan, ids, table, 1.0, out)
+    assert torch.equal(out, table[ids])
+    out.fill_(0)
+    out[T - V:] = table      # only the last token of each id has a gradient
+    ws = torch.empty(plan.info["workspace_bytes"], dtype=torch.uint8, device="cuda")
+    got = torch.full((V, D), NAN, dtype=torch.bfloat16, device="cuda")
+    b.basp_embed_to_seq_grad(plan, ids, out, 1.0, False, got, ws)
+    want = torch.empty_like(table)
+    want[ids[T - V:]] = table
+    assert torch.equal(got, want)

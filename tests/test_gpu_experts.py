@@ -236,3 +236,12 @@ def test_rows_past_four_gib():
     w = torch.full((T, 2), 0.5, device="cuda")
     b.basp_expert_to_seq(plan, rows, index[0], w, y)
     assert torch.equal(y, x)
+    y.fill_(NAN)
+    b.basp_seq_to_expert_grad(plan, rows, index[0], y)
+    assert torch.equal(y, x + x)
+    drows, dw = torch.full_like(rows, NAN), torch.full_like(w, NAN)
+    one = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    one[:, 5] = 2.0
+    b.basp_expert_to_seq_grad(plan, one, rows, index[0], index[1], w, drows, dw)
+    assert torch.equal(dw, (2 * x[:, :1].float()).expand(T, 2))
+    assert bool((drows[:, 5] == 1).all()) and int(torch.count_nonzero(drows)) == 2 * T
