@@ -74,6 +74,8 @@ SIZES = [  # T, K, E, D, align, dtype, weights, id_bytes, drop
     (511, 4, 64, 1000, 1, "fp16", "fp32", 4, 0.0),
     (700, 3, 1000, 24, 3, "fp32", "fp32", 8, 0.1),
     (1023, 5, 40, 777, 4, "fp32", "fp32", 4, 0.2),
+    (512, 4, 512, 40, 5, "bf16", "fp32", 8, 0.1),
+    (683, 3, 77, 40, 128, "bf16", "fp32", 4, 0.0),
     (2049, 2, 8, 520, 1, "bf16", "fp32", 8, 0.0),
     (4099, 3, 20, 1001, 16, "bf16", "fp32", 8, 0.1),
     (5000, 8, 256, 8, 1, "bf16", "fp32", 4, 0.0),
