@@ -154,9 +154,9 @@ __global__ __launch_bounds__(kSortBlock) void digit_place_kernel(const PassDesc 
 // A small sort in one launch, by counting: a token's place is the number of
 // (id, token) pairs below its own.  Every work-group holds all T pairs in LDS
 // and places kRankTokens of them: a lane compares one of its tokens with every
-// kRankParts-th pair.  T^2 comparisons cost less than the passes of the
-// general sort up to kRankMost tokens (4095 tokens: 7 us, one work-group
-// sorting by digits 15 us; four launches 24 us).
+// kRankParts-th vector of pairs.  T^2 comparisons cost less than the launches
+// of the general sort up to kRankNarrow tokens.  Pair: the pairs as whole
+// numbers id * T + token, which 32 bits hold for most plans.
 constexpr int kRankThreads = 1024, kRankTokens = 16, kRankParts = kRankThreads / kRankTokens;
 
 struct RankDesc {
@@ -164,39 +164,55 @@ struct RankDesc {
     ZeroDesc zero;                  // ids and tags
 };
 
+template <typename Pair>
+size_t rank_lds_bytes(int64_t T)
+{
+    constexpr int64_t STEP = kRankParts * (16 / sizeof(Pair));
+    return size_t((T + STEP - 1) / STEP * STEP) * sizeof(Pair);
+}
+
+template <typename Pair>
 __global__ __launch_bounds__(kRankThreads) void rank_kernel(const RankDesc D)
 {
-    __shared__ uint64_t pairs[kRankMost];
+    constexpr int N = 16 / sizeof(Pair), STEP = kRankParts * N;
+    typedef Pair vec __attribute__((ext_vector_type(N)));
+    extern __shared__ uint4 rank_lds[];
     __shared__ int place[kRankTokens];
+    const vec *const pairs = reinterpret_cast<const vec *>(rank_lds);
+    Pair *const one = reinterpret_cast<Pair *>(rank_lds);
     const int T = int(D.zero.T), first = blockIdx.x * kRankTokens;
-    const int filled = (T + kRankParts - 1) / kRankParts * kRankParts;
+    const int filled = (T + STEP - 1) / STEP * STEP;
     for (int i = threadIdx.x; i < filled; i += kRankThreads) {
-        uint64_t p = ~uint64_t{0};
+        Pair p = ~Pair{0};
         if (i < T) {
             const uint32_t key = row_of_id(D.zero.ids, i, D.zero.V, D.zero.padding, D.zero.wide_ids);
-            p = uint64_t(key) << 32 | uint32_t(i);
+            p = Pair(key) * Pair(T) + Pair(i);
             if (i >= first && i < first + kRankTokens && key < D.zero.V)
                 D.zero.tags[key] = uint32_t(i);
         }
-        pairs[i] = p;
+        one[i] = p;
     }
     if (threadIdx.x < kRankTokens)
         place[threadIdx.x] = 0;
     lds_barrier();
     const int token = threadIdx.x % kRankTokens;
-    const uint64_t mine = pairs[first + token < T ? first + token : first];
+    const Pair mine = one[first + token < T ? first + token : first];
     int below = 0;
-#pragma unroll 8
-    for (int i = threadIdx.x / kRankTokens; i < filled; i += kRankParts)
-        below += pairs[i] < mine;
+#pragma unroll 4
+    for (int i = threadIdx.x / kRankTokens; i < filled / N; i += kRankParts) {
+        const vec p = pairs[i];
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            below += p[n] < mine;
+    }
     below += __shfl_xor(below, 16);
     below += __shfl_xor(below, 32);
     if ((threadIdx.x & 63) < kRankTokens)
         atomicAdd(&place[token], below);
     lds_barrier();
     if (threadIdx.x < kRankTokens && first + token < T) {
-        D.keys[place[token]] = uint32_t(mine >> 32);
-        D.tokens[place[token]] = uint32_t(mine);
+        D.keys[place[token]] = uint32_t(mine / Pair(T));
+        D.tokens[place[token]] = uint32_t(first + token);
     }
 }
 
@@ -570,7 +586,11 @@ basp_status launch_grad(const basp_embed_plan &p, const void *ids, const void *d
     };
     if (p.T && p.sort_blocks == 0) {
         const RankDesc D = {keys[(p.passes - 1) & 1], tokens[(p.passes - 1) & 1], Z};
-        go(reinterpret_cast<const void *>(rank_kernel), dim3(groups_of(p.T, kRankTokens)), kRankThreads, D, false, 0);
+        const bool narrow = fits_narrow(p.T, p.V);
+        go(narrow ? reinterpret_cast<const void *>(rank_kernel<uint32_t>)
+                  : reinterpret_cast<const void *>(rank_kernel<uint64_t>),
+           dim3(groups_of(p.T, kRankTokens)), kRankThreads, D, false,
+           narrow ? rank_lds_bytes<uint32_t>(p.T) : rank_lds_bytes<uint64_t>(p.T));
     }
     for (int pass = 0; pass < p.passes && p.sort_blocks > 0 && p.T; ++pass) {
         PassDesc D = {};

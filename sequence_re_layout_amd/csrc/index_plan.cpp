@@ -201,7 +201,7 @@ extern "C" basp_embed_plan *basp_embed_plan_create(const basp_plan *layout, int6
     p->passes = (bits + basp::kDigitBits - 1) / basp::kDigitBits;
     p->digit_bits = (bits + p->passes - 1) / p->passes;
     split_sort(T, p->sort_blocks, p->block_items);
-    if (T <= basp::kRankMost)
+    if (T <= (basp::fits_narrow(T, V) ? basp::kRankNarrow : basp::kRankWide))
         p->sort_blocks = 0;
     p->lanes_log2 = lanes_log2;
     p->chunk = chunk;

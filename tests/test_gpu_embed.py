@@ -77,6 +77,9 @@ SIZES = [  # layout (N, B, S, groups) or tokens, V, D, dtype, grad, id_bytes, pa
     (700, 40, 9001, "fp16", "fp32", 8, -1, 0.0),
     (8192, 300, 40, "bf16", "fp32", 8, -1, 0.01),
     (8193, 300, 40, "bf16", "fp32", 8, -1, 0.01),
+    (11264, 381299, 9, "bf16", "bf16", 8, -1, 0.01),
+    (11265, 40, 33, "bf16", "fp32", 8, -1, 0.01),
+    (7168, 1 << 22, 3, "bf16", "bf16", 8, -1, 0.01),
     ((2, 2, 10000, 1), 70001, 24, "fp16", "bf16", 4, 5, 0.02),
     (9000, 1500000, 9, "bf16", "bf16", 8, -1, 0.0),
     (20001, 511, 520, "bf16", "fp32", 4, -1, 0.0),
