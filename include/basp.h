@@ -583,8 +583,8 @@ typedef struct basp_embed_info {
  *   BASP_ERR_INVALID      an argument out of range, an unknown enum, or T
  *                         other than B*S
  *   BASP_ERR_UNSUPPORTED  V above 2^30, D of 2^28 or more, T of 2^31 - 1 or
- *                         more, or activations of 1 TiB and more with few
- *                         channels short of it (2^23 work-groups)
+ *                         more, or about 1 TiB of activations and more (2^36
+ *                         vectors of 16 bytes)
  */
 basp_embed_plan *basp_embed_plan_create(const basp_plan *layout, int64_t T, int64_t V, int64_t D,
                                         int64_t padding, int id_bytes, basp_dtype dtype, basp_dtype grad_dtype);

@@ -31,6 +31,10 @@ Tensors are contiguous and of the plan's dtype and element counts, as the
 binding checks; outputs are allocated with torch on the inputs' device.  Only
 buffers are marshalled here: every element is moved by the library's kernels.
 The gradients are not themselves differentiable.
+
+In HIP graphs, capture a backward pass together with its forward pass, on leaf
+tensors that no live graph of eager calls holds: torch ties a leaf's gradient to
+the stream of its first use.
 """
 from __future__ import annotations
 
