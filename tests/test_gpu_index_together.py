@@ -328,3 +328,85 @@ def test_binding_refuses():
     with pytest.raises(b.BaspError) as e:
         b.basp_seq_to_expert(s.plan, s.rows.view(-1)[:s.h.numel()].view_as(s.h), pos, order, s.rows)
     assert e.value.status == b.BASP_ERR_ALIAS
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_all_values(dtype):
+    """Every 16-bit pattern: moved bit for bit, and through a factor of one
+    unchanged (subnormals and signed zeros too), NaN staying NaN."""
+    dt = ic.FLOATS[dtype]
+    code = {"bf16": b.BASP_BF16, "fp16": b.BASP_FP16}[dtype]
+    bits = torch.arange(-32768, 32768, device="cuda").to(torch.int16)
+    x = bits.view(dt).view(256, 256)
+    plan = b.basp_expert_plan_create(256, 1, 4, 256, dtype=code)
+    ids = (torch.arange(256, device="cuda") * 7 % 4).view(256, 1)
+    rows, index = ag.route_to_expert(plan, x, ids)
+    assert torch.equal(rows.view(torch.int16), x.view(torch.int16)[index.order.long()])
+    y = ag.expert_to_seq(plan, rows, torch.ones(256, 1, device="cuda"), index)
+    ep = b.basp_embed_plan_create(None, 256, 256, 256, dtype=code, grad_dtype=code)
+    tokens = torch.arange(256, device="cuda")
+    z = ag.embed_to_seq(ep, tokens, x, 1.0)
+    g = torch.empty_like(x)
+    ws = torch.empty(ep.info["workspace_bytes"], dtype=torch.uint8, device="cuda")
+    b.basp_embed_to_seq_grad(ep, tokens, x, 1.0, False, g, ws)
+    nan = torch.isnan(x)
+    for what, got, zeros in (("expert_to_seq", y, False), ("embed_to_seq", z, True), ("gradient", g, False)):
+        assert bool(torch.isnan(got[nan]).all()), what
+        if zeros:
+            assert torch.equal(got.view(torch.int16)[~nan], x.view(torch.int16)[~nan]), what
+        else:               # a sum that starts at +0: the sign of a zero may be lost
+            assert torch.equal(got[~nan], x[~nan]), what
+
+
+def test_one_input_needs_its_gradient():
+    """Gradients of rows or of weights alone, and of expanded inputs."""
+    T, K, E, D = 64, 2, 4, 32
+    plan = b.basp_expert_plan_create(T, K, E, D, dtype=b.BASP_FP32)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(8)
+    ids = torch.randint(0, E, (T, K), generator=gen, device="cuda")
+    index = ag.sort_by_expert(plan, ids)
+    rows = torch.randn(plan.info["max_rows"], D, generator=gen, device="cuda")
+    w = torch.rand(T, K, generator=gen, device="cuda")
+    both = [t.clone().requires_grad_() for t in (rows, w)]
+    want = torch.autograd.grad(ag.expert_to_seq(plan, *both, index).sum(), both)   # an expanded gradient
+    for i in range(2):
+        one = [t.clone().requires_grad_(i == j) for j, t in enumerate((rows, w))]
+        (got,) = torch.autograd.grad(ag.expert_to_seq(plan, *one, index).sum(), (one[i],))
+        assert torch.equal(got, want[i])
+    # one weight for every token: its gradient is the sum over the tokens
+    s = torch.full((1, K), 0.5, device="cuda").requires_grad_()
+    (got,) = torch.autograd.grad(ag.expert_to_seq(plan, rows, s.expand(T, K).contiguous(), index).sum(), (s,))
+    terms = want[1].double().sum(0, keepdim=True)
+    assert torch.allclose(got.double(), terms, rtol=0, atol=2 * (T + D) * 2.0 ** -24 * float(rows.abs().sum()))
+
+
+def test_plan_of_another_thread_and_stream():
+    """One plan used by several threads at once, each on its own stream."""
+    import threading
+    steps = [Step() for _ in range(4)]
+    want = [s.want(40 + i) for i, s in enumerate(steps)]
+    for s in steps:
+        s.plan, s.embed = steps[0].plan, steps[0].embed
+        s.spoil()
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(s):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    s.run()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # noqa: BLE001  (reported by the main thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in steps]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    torch.cuda.synchronize()
+    for s, w in zip(steps, want):
+        assert all(torch.equal(a, x) for a, x in zip(s.outputs(), w))
