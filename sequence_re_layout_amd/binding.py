@@ -426,6 +426,10 @@ def basp_stream_copy(dst, src, nbytes=None, stream=None) -> None:
 
 # ------------------------------------------------ index-driven re-layouts --
 
+def _stream_on(device: int, stream):
+    return _current_stream(device) if stream is None else _stream(stream)
+
+
 class ExpertPlan:
     """Owner of a ``basp_expert_plan*``; destroyed with the object.  ``info``
     holds the ``basp_expert_plan_query`` result as a dict."""
@@ -469,20 +473,22 @@ class EmbedPlan:
 def _addr(x, of, name: str, device: int):
     """Device address of a tensor of the dtype and element count ``of``, or an
     int or None as is."""
-    if x is None or isinstance(x, int):
-        return x
-    dtype, numel = of
-    if x.dtype != dtype:
-        raise TypeError("%s: dtype %s, the plan needs %s" % (name, x.dtype, dtype))
+    try:                             # the call that is right costs one look at each property
+        if x.dtype is of[0] and x.get_device() == device and x.numel() == of[1] and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        if x is None or isinstance(x, int):
+            return x
+        raise
+    if x.dtype != of[0]:
+        raise TypeError("%s: dtype %s, the plan needs %s" % (name, x.dtype, of[0]))
     if not x.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
     if x.get_device() != device:
         raise ValueError("%s is on %s, the current device is cuda:%d" % (name, x.device, device))
     if not x.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if x.numel() != numel:
-        raise ValueError("%s holds %d elements, the plan needs %d" % (name, x.numel(), numel))
-    return x.data_ptr()
+    raise ValueError("%s holds %d elements, the plan needs %d" % (name, x.numel(), of[1]))
 
 
 def _ws_addr(ws, plan, device: int):
@@ -521,14 +527,14 @@ def basp_expert_sort(plan: ExpertPlan, ids, pos, order, offsets, counts, ws, str
     _check(_lib.basp_expert_sort(
         plan.handle, _addr(ids, plan.ids, "ids", d), _addr(pos, plan.pos, "pos", d),
         _addr(order, plan.order, "order", d), _addr(offsets, plan.offsets, "offsets", d),
-        _addr(counts, plan.counts, "counts", d), _ws_addr(ws, plan, d), _stream(stream)), "basp_expert_sort")
+        _addr(counts, plan.counts, "counts", d), _ws_addr(ws, plan, d), _stream_on(d, stream)), "basp_expert_sort")
 
 
 def basp_seq_to_expert(plan: ExpertPlan, x, pos, order, out, stream=None) -> None:
     d = torch.cuda.current_device()
     _check(_lib.basp_seq_to_expert(
         plan.handle, _addr(x, plan.tokens, "x", d), _addr(pos, plan.pos, "pos", d),
-        _addr(order, plan.order, "order", d), _addr(out, plan.rows, "out", d), _stream(stream)),
+        _addr(order, plan.order, "order", d), _addr(out, plan.rows, "out", d), _stream_on(d, stream)),
         "basp_seq_to_expert")
 
 
@@ -538,21 +544,21 @@ def basp_route_to_expert(plan: ExpertPlan, x, ids, pos, order, offsets, counts, 
         plan.handle, _addr(x, plan.tokens, "x", d), _addr(ids, plan.ids, "ids", d), _addr(pos, plan.pos, "pos", d),
         _addr(order, plan.order, "order", d), _addr(offsets, plan.offsets, "offsets", d),
         _addr(counts, plan.counts, "counts", d), _addr(out, plan.rows, "out", d), _ws_addr(ws, plan, d),
-        _stream(stream)), "basp_route_to_expert")
+        _stream_on(d, stream)), "basp_route_to_expert")
 
 
 def basp_seq_to_expert_grad(plan: ExpertPlan, dout, pos, dx, stream=None) -> None:
     d = torch.cuda.current_device()
     _check(_lib.basp_seq_to_expert_grad(
         plan.handle, _addr(dout, plan.rows, "dout", d), _addr(pos, plan.pos, "pos", d),
-        _addr(dx, plan.tokens, "dx", d), _stream(stream)), "basp_seq_to_expert_grad")
+        _addr(dx, plan.tokens, "dx", d), _stream_on(d, stream)), "basp_seq_to_expert_grad")
 
 
 def basp_expert_to_seq(plan: ExpertPlan, rows, pos, weights, out, stream=None) -> None:
     d = torch.cuda.current_device()
     _check(_lib.basp_expert_to_seq(
         plan.handle, _addr(rows, plan.rows, "rows", d), _addr(pos, plan.pos, "pos", d),
-        _addr(weights, plan.weights, "weights", d), _addr(out, plan.tokens, "out", d), _stream(stream)),
+        _addr(weights, plan.weights, "weights", d), _addr(out, plan.tokens, "out", d), _stream_on(d, stream)),
         "basp_expert_to_seq")
 
 
@@ -562,7 +568,7 @@ def basp_expert_to_seq_grad(plan: ExpertPlan, dout, rows, pos, order, weights, d
         plan.handle, _addr(dout, plan.tokens, "dout", d), _addr(rows, plan.rows, "rows", d),
         _addr(pos, plan.pos, "pos", d), _addr(order, plan.order, "order", d),
         _addr(weights, plan.weights, "weights", d), _addr(drows, plan.rows, "drows", d),
-        _addr(dweights, plan.weights, "dweights", d), _stream(stream)), "basp_expert_to_seq_grad")
+        _addr(dweights, plan.weights, "dweights", d), _stream_on(d, stream)), "basp_expert_to_seq_grad")
 
 
 def basp_embed_plan_create(layout, T, V, D, padding=-1, id_bytes=8, dtype=BASP_BF16,
@@ -590,11 +596,11 @@ def basp_embed_to_seq(plan: EmbedPlan, ids, table, scale, out, stream=None) -> N
     d = torch.cuda.current_device()
     _check(_lib.basp_embed_to_seq(
         plan.handle, _addr(ids, plan.ids, "ids", d), _addr(table, plan.table, "table", d), scale,
-        _addr(out, plan.tokens, "out", d), _stream(stream)), "basp_embed_to_seq")
+        _addr(out, plan.tokens, "out", d), _stream_on(d, stream)), "basp_embed_to_seq")
 
 
 def basp_embed_to_seq_grad(plan: EmbedPlan, ids, dout, scale, accumulate, dtable, ws, stream=None) -> None:
     d = torch.cuda.current_device()
     _check(_lib.basp_embed_to_seq_grad(
         plan.handle, _addr(ids, plan.ids, "ids", d), _addr(dout, plan.tokens, "dout", d), scale, bool(accumulate),
-        _addr(dtable, plan.grad, "dtable", d), _ws_addr(ws, plan, d), _stream(stream)), "basp_embed_to_seq_grad")
+        _addr(dtable, plan.grad, "dtable", d), _ws_addr(ws, plan, d), _stream_on(d, stream)), "basp_embed_to_seq_grad")
