@@ -83,6 +83,9 @@ SIZES = [  # layout (N, B, S, groups) or tokens, V, D, dtype, grad, id_bytes, pa
     ((2, 2, 10000, 1), 70001, 24, "fp16", "bf16", 4, 5, 0.02),
     (9000, 1500000, 9, "bf16", "bf16", 8, -1, 0.0),
     (20001, 511, 520, "bf16", "fp32", 4, -1, 0.0),
+    (30000, 1023, 16, "fp16", "fp32", 8, 700, 0.3),
+    (30000, 1024, 16, "bf16", "fp32", 4, -1, 0.3),
+    (12000, 1 << 20, 12, "bf16", "bf16", 8, -1, 0.05),
     (530001, 1000, 2, "fp32", "fp32", 4, -1, 0.1),
 ]
 IDS = ["x".join(map(str, s)).replace(" ", "") for s in SIZES]
@@ -138,11 +141,11 @@ def test_gradient(size, shift):
 
 
 @pytest.mark.parametrize("ids", ["same", "two", "all outside", "distinct", "runs of 32", "runs of 33"])
-@pytest.mark.parametrize("T", [32, 33, 1000, 5000, 10000])
+@pytest.mark.parametrize("T", [32, 33, 1000, 5000, 10000, 20000])
 def test_long_and_short_runs(ids, T):
     """One id for all tokens, ids that fill whole chunks, and none repeated."""
     t = np.arange(T)
-    V = 12000
+    V = 20000
     of = {"same": t * 0 + 17, "two": (t * 7 % 13 > 5) * 5999, "all outside": t * 0 + V, "distinct": t[::-1].copy(),
           "runs of 32": t // 32, "runs of 33": t // 33}[ids]
     r = Lookup(T, V, 72, "bf16", "fp32", ids=of)
