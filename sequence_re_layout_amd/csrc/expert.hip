@@ -256,7 +256,11 @@ __global__ __launch_bounds__(kThreads) void gather_sum_kernel(const SumDesc D)
                     acc[i] = WEIGHTED ? fmaf(w[j], f[i], acc[i]) : acc[i] + f[i];
             }
     }
-    store_vec<VW>(D.out + uint64_t(t) * D.row + off, pack<E, VW>(acc));
+    char *const out = D.out + uint64_t(t) * D.row;
+    if constexpr (UNI && VW == 16)
+        store_streamed(out, D.row, off, pack<E, VW>(acc));
+    else
+        store_vec<VW>(out + off, pack<E, VW>(acc));
 }
 
 struct GradDesc {
