@@ -210,7 +210,12 @@ struct SumDesc {
     int32_t K;
     uint32_t max_rows;
     basp_dtype weight_dtype;
+    int32_t streamed;               // store past the XCD's caches
 };
+
+// Sums of at least this many bytes are stored past the XCD's caches; small
+// calls end later that way (16 tokens x 4096, 8 choices: 5.4 against 4.5 us).
+constexpr int64_t kStreamBytes = int64_t{32} << 20;
 
 // expert -> seq and the gradient of seq -> expert: out[t] = sum over k of
 // (weights[t][k] *) rows[pos[t][k]] in fp32, k ascending.  KB loads are in
@@ -257,10 +262,13 @@ __global__ __launch_bounds__(kThreads) void gather_sum_kernel(const SumDesc D)
             }
     }
     char *const out = D.out + uint64_t(t) * D.row;
-    if constexpr (UNI && VW == 16)
-        store_streamed(out, D.row, off, pack<E, VW>(acc));
-    else
-        store_vec<VW>(out + off, pack<E, VW>(acc));
+    if constexpr (UNI && VW == 16) {
+        if (D.streamed) {
+            store_streamed(out, D.row, off, pack<E, VW>(acc));
+            return;
+        }
+    }
+    store_vec<VW>(out + off, pack<E, VW>(acc));
 }
 
 struct GradDesc {
@@ -568,6 +576,7 @@ basp_status launch_sum(const basp_expert_plan &p, const void *rows, const int32_
         D.K = p.K;
         D.max_rows = uint32_t(p.max_rows);
         D.weight_dtype = p.weight_dtype;
+        D.streamed = p.T * r.row >= kStreamBytes;
         return launch_kernel(fn, dim3(groups_of(D.nvec, kThreads)), kThreads, D, stream, first, last);
     });
 }
