@@ -87,6 +87,7 @@ SIZES = [  # layout (N, B, S, groups) or tokens, V, D, dtype, grad, id_bytes, pa
     (30000, 1024, 16, "bf16", "fp32", 4, -1, 0.3),
     (12000, 1 << 20, 12, "bf16", "bf16", 8, -1, 0.05),
     (530001, 1000, 2, "fp32", "fp32", 4, -1, 0.1),
+    (1100001, 3000, 2, "bf16", "fp32", 8, -1, 0.01),
 ]
 IDS = ["x".join(map(str, s)).replace(" ", "") for s in SIZES]
 

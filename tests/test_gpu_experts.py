@@ -212,9 +212,10 @@ def test_damaged_index_stays_inside():
     assert bool((out.t.view(r.rows, 72)[torch.from_numpy(r.pos[[3, 5]]).cuda()] == 0).all())
 
 
-def test_many_groups_of_the_sort():
-    """More slots than 256 work-groups of 2048: the groups grow."""
-    r = Routing(140001, 4, 300, 1, 1, "bf16", id_bytes=4, drop=0.01)
+@pytest.mark.parametrize("T", [70001, 140001, 290001])
+def test_many_groups_of_the_sort(T):
+    """More slots than 256 work-groups of 1024 (and of 4096): the groups grow."""
+    r = Routing(T, 4, 300, 1, 1, "bf16", id_bytes=4, drop=0.01)
     got = r.out_index()
     b.basp_expert_sort(r.plan, r.ids_d, *[g.t for g in got], r.ws)
     r.check_index(got)
