@@ -85,6 +85,14 @@ BASP_HD inline uint32_t seq_row(const basp_seq_order &o, uint32_t t)
     return ((g * o.P + j) * o.Bl + (seq - g * o.Bl)) * o.St + (at - j * o.St);
 }
 
+// n rounded up to a multiple of `to`, as a plan's slots and align are.  The sum
+// passes 2^31 where one expert has nearly 2^31 slots, and always fits 32 bits
+// without a sign; the result is at most max_rows.
+BASP_HD inline int padded_count(int n, int to)
+{
+    return to == 1 ? n : int((uint32_t(n) + uint32_t(to) - 1) / uint32_t(to) * uint32_t(to));
+}
+
 // Rows are read and written in vectors of vw bytes, the widest power of two
 // up to 16 that a row holds one of.  A row of `elems` elements takes
 // ceil(elems / epv) vectors; the last one ends with the row and so overlaps

@@ -17,6 +17,8 @@
 
 #include <cstdint>
 
+#include "index_plan.hpp"
+
 namespace basp {
 
 // A barrier for what the work-group has in LDS alone.  __syncthreads() also
@@ -114,8 +116,6 @@ __device__ inline void sort_sum_groups(const SortLds &l, const int *hist, int bi
     }
 }
 
-__device__ inline int round_up(int n, int to) { return to == 1 ? n : (n + to - 1) / to * to; }
-
 // From the waves' counts (l.count), and with more than one group the totals
 // and the counts before this group: the starts, an exclusive sum over the
 // bins, a few consecutive ones a thread; and in l.count the place of each
@@ -138,7 +138,7 @@ __device__ inline void sort_starts(const SortLds &l, int bins, int align, int gr
                     n += l.count[w * bins + e];
                 l.total[e] = n;
             }
-            sum += round_up(l.total[e], align);
+            sum += padded_count(l.total[e], align);
         }
         const int upto = wave_inclusive_sum(sum, lane);
         if (lane == 63)
@@ -164,7 +164,7 @@ __device__ inline void sort_starts(const SortLds &l, int bins, int align, int gr
                 l.count[w * bins + e] = next;
                 next += n[w];
             }
-            at += round_up(total, align);
+            at += padded_count(total, align);
             if (e == bins - 1)
                 l.start[bins] = at;
         }
