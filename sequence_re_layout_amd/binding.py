@@ -574,6 +574,10 @@ def basp_expert_to_seq_grad(plan: ExpertPlan, dout, rows, pos, order, weights, d
 def basp_embed_plan_create(layout, T, V, D, padding=-1, id_bytes=8, dtype=BASP_BF16,
                            grad_dtype=BASP_BF16) -> EmbedPlan:
     """``layout``: the Plan whose sequence-sharded order the rows take, or None."""
+    if layout is not None and not isinstance(layout, Plan):
+        raise TypeError("layout must be a Plan or None")
+    if layout is not None and not layout.handle:     # destroyed: NULL would ask for the order of the ids
+        raise BaspError(BASP_ERR_INVALID, "basp_embed_plan_create")
     h = _lib.basp_embed_plan_create(None if layout is None else layout.handle, T, V, D, padding, id_bytes, dtype,
                                     grad_dtype)
     if not h:
