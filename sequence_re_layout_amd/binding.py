@@ -504,7 +504,16 @@ def _ws_addr(ws, plan, device: int):
     return ws.data_ptr()
 
 
+def _check_bits(bits: int, **args) -> None:
+    """ctypes passes the low bits of a whole number that its type cannot hold."""
+    for name, v in args.items():
+        if isinstance(v, int) and not -(1 << bits - 1) <= v < 1 << bits - 1:
+            raise ValueError("%s = %d does not fit in %d bits" % (name, v, bits))
+
+
 def basp_expert_plan_create(T, K, E, D, align=1, id_bytes=8, dtype=BASP_BF16, weight_dtype=BASP_FP32) -> ExpertPlan:
+    _check_bits(64, T=T, D=D)
+    _check_bits(32, K=K, E=E, align=align, id_bytes=id_bytes, dtype=dtype, weight_dtype=weight_dtype)
     h = _lib.basp_expert_plan_create(T, K, E, D, align, id_bytes, dtype, weight_dtype)
     if not h:
         raise BaspError(_lib.basp_last_error(), "basp_expert_plan_create")
@@ -578,6 +587,8 @@ def basp_embed_plan_create(layout, T, V, D, padding=-1, id_bytes=8, dtype=BASP_B
         raise TypeError("layout must be a Plan or None")
     if layout is not None and not layout.handle:     # destroyed: NULL would ask for the order of the ids
         raise BaspError(BASP_ERR_INVALID, "basp_embed_plan_create")
+    _check_bits(64, T=T, V=V, D=D, padding=padding)
+    _check_bits(32, id_bytes=id_bytes, dtype=dtype, grad_dtype=grad_dtype)
     h = _lib.basp_embed_plan_create(None if layout is None else layout.handle, T, V, D, padding, id_bytes, dtype,
                                     grad_dtype)
     if not h:
