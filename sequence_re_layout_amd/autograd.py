@@ -20,8 +20,9 @@ their gradients in the same way:
   returns their rows with the index; ``seq_to_expert(expert_plan, x, index)``
   moves by an index that is there; backward: ``basp_seq_to_expert_grad``;
 * ``expert_to_seq(expert_plan, rows, weights, index)`` returns the weighted
-  sums of the tokens' rows; backward, for rows and weights:
-  ``basp_expert_to_seq_grad``;
+  sums of the tokens' rows; backward: ``basp_expert_to_seq_grad``, one call that
+  computes the gradients of rows and of weights, also where only one of them is
+  asked for (rows and weights are kept until then);
 * ``embed_to_seq(embed_plan, ids, table, scale)`` looks rows up into the
   sequence-sharded layout; backward, for the table (whose gradient has the
   plan's grad_dtype until autograd casts it to the table's):
@@ -30,7 +31,9 @@ their gradients in the same way:
 Tensors are contiguous and of the plan's dtype and element counts, as the
 binding checks; outputs are allocated with torch on the inputs' device.  Only
 buffers are marshalled here: every element is moved by the library's kernels.
-The gradients are not themselves differentiable.
+The gradients are not themselves differentiable.  An index, rows or ids that a
+backward pass still needs must not be written again through the binding's calls
+before it: torch does not see these writes.
 
 In HIP graphs, capture a backward pass together with its forward pass, on leaf
 tensors that no live graph of eager calls holds: torch ties a leaf's gradient to

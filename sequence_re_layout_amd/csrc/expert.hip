@@ -219,8 +219,14 @@ struct SumDesc {
     int32_t streamed;               // store past the XCD's caches
 };
 
-// Sums of at least this many bytes are stored past the XCD's caches; small
-// calls end later that way (16 tokens x 4096, 8 choices: 5.4 against 4.5 us).
+// Sums of at least this many bytes are stored past the XCD's caches.  Weighted
+// sums in bf16 with such stores and without, us (2048 channels, 4 choices; 4096,
+// 2; 512, 8): 16 MiB 15.7 / 15.7, 10.0 / 9.8, 26.7 / 26.3; 32 MiB 29.2 / 28.8,
+// 18.3 / 18.2, 51.0 / 50.3; 64 MiB 57.0 / 57.3, 34.9 / 34.9, 100.7 / 100.2; 96
+// MiB 83.7 / 85.8, 49.4 / 49.8, 150.3 / 150.7; 128 MiB 111.4 / 113.6, 66.0 /
+// 67.1, 201.6 / 203.0.  They gain from about 64 MiB on and cost up to 2%
+// between 32 and 64; the smallest calls end later (16 tokens x 4096, 8 choices:
+// 5.4 against 4.5).
 constexpr int64_t kStreamBytes = int64_t{32} << 20;
 
 // expert -> seq and the gradient of seq -> expert: out[t] = sum over k of
@@ -334,9 +340,9 @@ __device__ inline float sum_over_lanes(float (&v)[KB], int lane, int span)
 // weighted dout.  The dot products are then summed over the lanes.
 // UNI: a token takes whole waves, so that its index and weights are scalars.
 // Bound by HBM where there are many tokens: 16384 x 2048, 8 slots, 1143 MB in
-// 206 us (5.5 TB/s; the bare reads and writes of this pattern 217 us with
-// non-temporal reads of dout, which here may come from the Infinity Cache); by
-// one work-group's chain of loads, sums and stores where there are few.
+// 206 us (5.5 TB/s).  The bare reads and writes of this pattern take 208 us, and
+// 217 with non-temporal reads of dout, which may come from the Infinity Cache.
+// By one work-group's chain of loads, sums and stores where there are few.
 template <typename E, int VW, int KB, bool UNI>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const GradDesc D)
 {

@@ -60,9 +60,16 @@ constexpr int kSortItems = kSortBlock * kSortSteps;
 constexpr int kMaxExperts = 1024;
 constexpr int kDigitBits = 10;              // of one pass of a sort by id
 // Tokens that are sorted by counting alone: with (id, token) pairs of 32 bits,
-// and of 64.  Whole gradients into 8191 x 128, this way and by digits: 4095
-// tokens 16.8 and 28.8 us, 8192 24.6 and 32.5, 12000 33.0 and 32.8, 14000 40.2
-// and 33.3.
+// and of 64, which fill 56 of the 64 KiB of LDS that a launch gets by default.
+// Whole gradients by counting and by digits, us:
+//   8191 x 128 (two digits)     4096 tokens 17.5 / 29.7, 8192 22.2 / 30.1, 11264
+//                               29.5 / 30.5, 13500 37.8 / 30.6
+//   2097152 x 8 (three)         4096 29.8 / 49.6, 7168 34.8 / 50.7
+//   1000 x 128 (one)            4096 16.9 / 22.9, 8192 22.1 / 24.3, 11264 29.8 / 25.2
+//   131072 x 2048 (two, beside  4096 96.5 / 97.7, 6000 101.2 / 98.5, 11264
+//   512 MiB of zeros)           113.7 / 103.1
+// The limit is that of the first kind: with one digit, or zeros that take as
+// long as the digits, digits are faster from about 9000 and 5000 tokens on.
 constexpr int kRankNarrow = 11264, kRankWide = 7168;
 
 // Pairs id * T + token, ids up to V, in 32 bits.
