@@ -31,7 +31,8 @@ their gradients in the same way:
 Tensors are contiguous and of the plan's dtype and element counts, as the
 binding checks; outputs are allocated with torch on the inputs' device.  Only
 buffers are marshalled here: every element is moved by the library's kernels.
-The gradients are not themselves differentiable.  An index, rows or ids that a
+The gradients of the index-driven re-layouts are not themselves differentiable:
+a loss with one of them in it is refused.  An index, rows or ids that a
 backward pass still needs must not be written again through the binding's calls
 before it: torch does not see these writes.
 
@@ -44,7 +45,6 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import binding as b
 
@@ -98,6 +98,20 @@ def head_to_seq_o(plan, o):
 
 # ------------------------------------------------ index-driven re-layouts --
 
+class _Gradient(torch.autograd.Function):
+    """compute(*tensors) of a backward pass.  With create_graph, autograd sees
+    that the gradient depends on these tensors, and differentiating it again
+    is an error wherever it stands in a loss."""
+
+    @staticmethod
+    def forward(ctx, compute, *tensors):
+        return compute(*tensors)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the gradients of the re-layouts are not themselves differentiable")
+
+
 class ExpertIndex(NamedTuple):
     """What basp_expert_sort returns: int32 tensors on the device."""
     pos: torch.Tensor
@@ -116,6 +130,14 @@ def _workspace(plan, device):
     return torch.empty(plan.info["workspace_bytes"], dtype=torch.uint8, device=device)
 
 
+def _tokens_grad(plan, shape, pos):
+    def compute(grad):
+        dx = torch.empty(shape, dtype=grad.dtype, device=grad.device)
+        b.basp_seq_to_expert_grad(plan, grad.contiguous(), pos, dx)
+        return dx
+    return compute
+
+
 class _RouteToExpert(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, x, ids):
@@ -129,12 +151,9 @@ class _RouteToExpert(torch.autograd.Function):
         return (rows, *index)
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad, *_):
         (pos,) = ctx.saved_tensors
-        dx = torch.empty(ctx.shape, dtype=grad.dtype, device=grad.device)
-        b.basp_seq_to_expert_grad(ctx.plan, grad.contiguous(), pos, dx)
-        return None, dx, None
+        return None, _Gradient.apply(_tokens_grad(ctx.plan, ctx.shape, pos), grad), None
 
 
 class _SeqToExpert(torch.autograd.Function):
@@ -148,12 +167,9 @@ class _SeqToExpert(torch.autograd.Function):
         return rows
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad):
         (pos,) = ctx.saved_tensors
-        dx = torch.empty(ctx.shape, dtype=grad.dtype, device=grad.device)
-        b.basp_seq_to_expert_grad(ctx.plan, grad.contiguous(), pos, dx)
-        return None, dx, None, None
+        return None, _Gradient.apply(_tokens_grad(ctx.plan, ctx.shape, pos), grad), None, None
 
 
 class _ExpertToSeq(torch.autograd.Function):
@@ -167,12 +183,15 @@ class _ExpertToSeq(torch.autograd.Function):
         return out
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad):
         rows, weights, pos, order = ctx.saved_tensors
-        drows, dweights = torch.empty_like(rows), torch.empty_like(weights)
-        b.basp_expert_to_seq_grad(ctx.plan, grad.contiguous(), rows, pos, order, weights, drows, dweights)
-        return None, drows, dweights, None, None
+
+        def compute(grad, rows, weights):
+            drows, dweights = torch.empty_like(rows), torch.empty_like(weights)
+            b.basp_expert_to_seq_grad(ctx.plan, grad.contiguous(), rows, pos, order, weights, drows, dweights)
+            return drows, dweights
+
+        return (None, *_Gradient.apply(compute, grad, rows, weights), None, None)
 
 
 class _EmbedToSeq(torch.autograd.Function):
@@ -186,14 +205,17 @@ class _EmbedToSeq(torch.autograd.Function):
         return out
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad):
         (ids,) = ctx.saved_tensors
         plan = ctx.plan
-        dtable = torch.empty(ctx.shape, dtype=plan.grad[0], device=grad.device)
-        b.basp_embed_to_seq_grad(plan, ids, grad.contiguous(), ctx.scale, False, dtable,
-                                 _workspace(plan, grad.device))
-        return None, None, dtable, None
+
+        def compute(grad):
+            dtable = torch.empty(ctx.shape, dtype=plan.grad[0], device=grad.device)
+            b.basp_embed_to_seq_grad(plan, ids, grad.contiguous(), ctx.scale, False, dtable,
+                                     _workspace(plan, grad.device))
+            return dtable
+
+        return None, None, _Gradient.apply(compute, grad), None
 
 
 def sort_by_expert(plan, ids):
