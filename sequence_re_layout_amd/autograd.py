@@ -31,8 +31,8 @@ their gradients in the same way:
 Tensors are contiguous and of the plan's dtype and element counts, as the
 binding checks; outputs are allocated with torch on the inputs' device.  Only
 buffers are marshalled here: every element is moved by the library's kernels.
-The gradients of the index-driven re-layouts are not themselves differentiable:
-a loss with one of them in it is refused.  An index, rows or ids that a
+The gradients are not themselves differentiable: a loss with one of them in it
+is refused.  An index, rows or ids that a
 backward pass still needs must not be written again through the binding's calls
 before it: torch does not see these writes.
 
@@ -49,6 +49,20 @@ import torch
 from . import binding as b
 
 
+class _Gradient(torch.autograd.Function):
+    """compute(*tensors) of a backward pass.  With create_graph, autograd sees
+    that the gradient depends on these tensors, and differentiating it again
+    is an error wherever it stands in a loss."""
+
+    @staticmethod
+    def forward(ctx, compute, *tensors):
+        return compute(*tensors)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the gradients of the re-layouts are not themselves differentiable")
+
+
 class _SeqToHeadQKV(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, q, k, v):
@@ -60,13 +74,16 @@ class _SeqToHeadQKV(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad):
-        i = ctx.plan.info
-        dev, dt = grad.device, grad.dtype
-        dq = torch.empty(i["q_elems"], dtype=dt, device=dev)
-        dk = torch.empty(i["kv_elems"], dtype=dt, device=dev)
-        dv = torch.empty(i["kv_elems"], dtype=dt, device=dev)
-        b.basp_head_to_seq_qkv(ctx.plan, grad.contiguous(), dq, dk, dv)
-        return None, dq, dk, dv
+        def compute(grad):
+            i = ctx.plan.info
+            dev, dt = grad.device, grad.dtype
+            dq = torch.empty(i["q_elems"], dtype=dt, device=dev)
+            dk = torch.empty(i["kv_elems"], dtype=dt, device=dev)
+            dv = torch.empty(i["kv_elems"], dtype=dt, device=dev)
+            b.basp_head_to_seq_qkv(ctx.plan, grad.contiguous(), dq, dk, dv)
+            return dq, dk, dv
+
+        return (None, *_Gradient.apply(compute, grad))
 
 
 class _HeadToSeqO(torch.autograd.Function):
@@ -79,9 +96,12 @@ class _HeadToSeqO(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad):
-        do = torch.empty(ctx.plan.info["q_elems"], dtype=grad.dtype, device=grad.device)
-        b.basp_seq_to_head_o(ctx.plan, grad.contiguous(), do)
-        return None, do
+        def compute(grad):
+            do = torch.empty(ctx.plan.info["q_elems"], dtype=grad.dtype, device=grad.device)
+            b.basp_seq_to_head_o(ctx.plan, grad.contiguous(), do)
+            return do
+
+        return None, _Gradient.apply(compute, grad)
 
 
 def seq_to_head_qkv(plan, q, k, v):
@@ -97,20 +117,6 @@ def head_to_seq_o(plan, o):
 
 
 # ------------------------------------------------ index-driven re-layouts --
-
-class _Gradient(torch.autograd.Function):
-    """compute(*tensors) of a backward pass.  With create_graph, autograd sees
-    that the gradient depends on these tensors, and differentiating it again
-    is an error wherever it stands in a loss."""
-
-    @staticmethod
-    def forward(ctx, compute, *tensors):
-        return compute(*tensors)
-
-    @staticmethod
-    def backward(ctx, *_):
-        raise RuntimeError("the gradients of the re-layouts are not themselves differentiable")
-
 
 class ExpertIndex(NamedTuple):
     """What basp_expert_sort returns: int32 tensors on the device."""

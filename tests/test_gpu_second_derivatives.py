@@ -53,3 +53,23 @@ def test_a_gradient_in_the_loss_of_the_experts(what):
         torch.autograd.grad(y.sum() + (grad * grad).sum(), leaves)
     # the loss without it is as it was
     assert torch.equal(torch.autograd.grad(f().sum(), of, create_graph=True)[0], want)
+
+
+@pytest.mark.parametrize("what", ["qkv, of q", "qkv, of k", "qkv, of v", "output"])
+def test_a_gradient_in_the_loss_of_the_boundary(what):
+    plan = b.basp_plan_create(2, 2, 8, 4, 2, 16, b.BASP_FP32, b.BASP_MODE_ULYSSES)
+    i = plan.info
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    q, k, v, o = (torch.randn(n, generator=g, device="cuda").requires_grad_()
+                  for n in (i["q_elems"], i["kv_elems"], i["kv_elems"], i["q_elems"]))
+    of = {"qkv, of q": q, "qkv, of k": k, "qkv, of v": v, "output": o}[what]
+    f = (lambda: ag.head_to_seq_o(plan, o) ** 3) if what == "output" else (lambda: ag.seq_to_head_qkv(plan, q, k, v) ** 3)
+    leaves = (o,) if what == "output" else (q, k, v)
+    want = torch.autograd.grad(f().sum(), of)[0]
+    assert torch.allclose(want, 3 * of.detach() ** 2, rtol=8 * 2.0 ** -24, atol=0)   # two roundings a side
+    y = f()
+    (grad,) = torch.autograd.grad(y.sum(), of, create_graph=True)
+    assert torch.equal(grad, want)
+    with pytest.raises(RuntimeError, match="differentia"):
+        torch.autograd.grad(y.sum() + (grad * grad).sum(), leaves)
