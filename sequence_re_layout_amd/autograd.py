@@ -32,9 +32,9 @@ Tensors are contiguous and of the plan's dtype and element counts, as the
 binding checks; outputs are allocated with torch on the inputs' device.  Only
 buffers are marshalled here: every element is moved by the library's kernels.
 The gradients are not themselves differentiable: a loss with one of them in it
-is refused.  An index, rows or ids that a
-backward pass still needs must not be written again through the binding's calls
-before it: torch does not see these writes.
+is refused.  An index, rows or ids that a backward pass still needs must not be
+written again through the binding's calls before it: torch does not see these
+writes.
 
 In HIP graphs, capture a backward pass together with its forward pass, on leaf
 tensors that no live graph of eager calls holds: torch ties a leaf's gradient to
