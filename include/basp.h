@@ -611,6 +611,164 @@ basp_status basp_embed_to_seq(const basp_embed_plan *plan, const void *ids, cons
 basp_status basp_embed_to_seq_grad(const basp_embed_plan *plan, const void *ids, const void *dout,
                                    float scale, int accumulate, void *dtable, void *ws, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The rest of a layer: attention, layer norm, balance loss
+ * ---------------------------------------------------------------------------
+ * What a layer computes between the re-layouts above, on their buffers as they
+ * lie: attention on the head shards that basp_seq_to_head writes and
+ * basp_head_to_seq takes, the norm of token rows, and the loss that keeps a
+ * router's choices balanced.  They are not part of the paper's method.
+ *
+ * Conventions as for the index-driven re-layouts: dense buffers of the plan's
+ * types at any element-aligned address, ws of the stated size and 16-byte
+ * aligned, one workspace for each call that may run at the same time, launches
+ * of kernels only (HIP graphs), the same inputs give the same bits.
+ * Products of matrices are taken of the inputs' type and added in fp32; all
+ * sums, statistics and softmaxes are fp32.
+ */
+
+/*
+ * Attention with a sliding window and sinks.
+ *
+ * Sequence b holds lengths[b] tokens in a cache of S (the layout's).  Its query
+ * i of `queries` stands at position p = starts[b] + i and sees the keys
+ *     j <= p   with   p - j < window   or   j < sinks,
+ * and none at all if p lies outside [0, lengths[b]).  Over the keys it sees
+ *     o = sum_j P_j v_j,  P = softmax(scale <q, k_j>),  lse = log sum_j exp(scale <q, k_j>).
+ * A row that sees nothing gets zeros and lse = -infinity, and has no part in any
+ * gradient.  Query head h reads the key and value head h / (Hq / Hkv).
+ *   training   queries = S, starts NULL (0); padded batches by lengths
+ *   serving    queries = the new tokens, starts[b] = lengths[b] - queries, their
+ *              keys and values already in the cache
+ * Keys and values at or after lengths[b] are not read.  Infinities and NaN in a
+ * key or value reach only the rows that see it, and in a row of q or dout only
+ * that row and the gradients of the keys that it sees.
+ *
+ * Buffers: the head-sharded layout (either order) of one shard for each rank and
+ * sequence, `shards` = N*Bl of them in the layout's order:
+ *   q, o, dout, dq  [shards][Hl_q][queries][d] or [shards][queries][Hl_q][d]
+ *   k, v, dk, dv    [shards][Hl_kv][S][d]      or [shards][S][Hl_kv][d]
+ *   lse             [shards][Hl_q][queries] fp32, in either order
+ *   starts, lengths [B] int32 per sequence, or NULL: starts 0 and lengths S, and
+ *                   with queries < S starts lengths - queries.  Values of lengths
+ *                   outside [0, S] count as the nearest of the two.
+ * With queries = S the parts of the fused buffer of basp_seq_to_head are q, k
+ * and v, and dq, dk and dv those of basp_head_to_seq_qkv's.
+ */
+typedef struct basp_attention_plan basp_attention_plan;
+
+typedef struct basp_attention_info {
+    int64_t S, queries, window;
+    int32_t sinks, shards, B, Hl_q, Hl_kv, d, layout, dtype;
+    int64_t q_elems, kv_elems, lse_elems;
+    int64_t workspace_bytes;         /* of basp_attention      */
+    int64_t grad_workspace_bytes;    /* of basp_attention_grad */
+} basp_attention_info;
+
+/*
+ * Create an attention plan.  Host only: no device call, no device memory; the
+ * layout is read and not kept.
+ *   layout   N, B, S, heads, d, dtype, groups and order of the head shards
+ *   queries  1 to S (0 if S is 0)     window  >= 1; S and above: all earlier keys
+ *   sinks    >= 0 first tokens that stay visible
+ * Errors (NULL returned, code in basp_last_error()):
+ *   BASP_ERR_INVALID       layout NULL, or an argument out of range
+ *   BASP_ERR_INDIVISIBLE   Hq no multiple of Hkv
+ *   BASP_ERR_UNSUPPORTED   dtype BASP_INT32, d above 128, S of 2^29 or more,
+ *                          (Hq / Hkv) * queries of 2^30 or more, or more
+ *                          than 2^24 - 1 work-groups in a launch
+ */
+basp_attention_plan *basp_attention_plan_create(const basp_plan *layout, int64_t queries, int64_t window, int64_t sinks);
+void basp_attention_plan_destroy(basp_attention_plan *plan); /* NULL is allowed */
+basp_status basp_attention_plan_query(const basp_attention_plan *plan, basp_attention_info *info);
+
+/*
+ * o and lse (NULL: not wanted).  scale must be finite and positive
+ * (BASP_ERR_INVALID).
+ */
+basp_status basp_attention(const basp_attention_plan *plan, const void *q, const void *k, const void *v,
+                           const int32_t *starts, const int32_t *lengths, float scale, void *o, float *lse, void *ws,
+                           void *stream);
+
+/*
+ * Gradients of basp_attention for a gradient dout of o, from o and lse as it
+ * wrote them:  with dP = <dout, v_j> and dS = P (dP - <dout, o>),
+ *   dq = scale sum_j dS_j k_j,   dk_j = scale sum dS_j q,   dv_j = sum P_j dout,
+ * the latter two over the rows of all query heads of the key head that see j.
+ * Every element is written; zeros for keys that no row sees.
+ */
+basp_status basp_attention_grad(const basp_attention_plan *plan, const void *q, const void *k, const void *v, const void *o,
+                                const float *lse, const void *dout, const int32_t *starts, const int32_t *lengths, float scale,
+                                void *dq, void *dk, void *dv, void *ws, void *stream);
+
+/*
+ * Layer norm of T rows of D channels:
+ *   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(variance + eps)
+ * with the row's mean and variance (of D, not D - 1).
+ */
+typedef struct basp_norm_plan basp_norm_plan;
+
+typedef struct basp_norm_info {
+    int64_t T, D;
+    int32_t dtype, weight_dtype;
+    int64_t workspace_bytes;         /* of basp_layer_norm_grad */
+} basp_norm_info;
+
+/*
+ * Create a norm plan.  Host only.  T rows (>= 0) of D channels (>= 1); dtype of
+ * x, y and their gradients, weight_dtype of weight, bias and theirs: BASP_BF16,
+ * BASP_FP16 or BASP_FP32, each on its own.
+ * Errors (NULL returned): BASP_ERR_INVALID; BASP_ERR_UNSUPPORTED (T of 2^31 - 1
+ * or more, D of 2^28 or more).
+ */
+basp_norm_plan *basp_norm_plan_create(int64_t T, int64_t D, basp_dtype dtype, basp_dtype weight_dtype);
+void basp_norm_plan_destroy(basp_norm_plan *plan); /* NULL is allowed */
+basp_status basp_norm_plan_query(const basp_norm_plan *plan, basp_norm_info *info);
+
+/*
+ * x, y [T][D]; weight, bias [D] (bias NULL: none); mean, rstd [T] fp32 (either
+ * may be NULL: not wanted).  eps finite and >= 0 (BASP_ERR_INVALID).
+ */
+basp_status basp_layer_norm(const basp_norm_plan *plan, const void *x, const void *weight, const void *bias, float eps,
+                            void *y, float *mean, float *rstd, void *stream);
+
+/*
+ * Gradients from mean and rstd as basp_layer_norm wrote them: dx [T][D],
+ * dweight [D] and dbias [D] (NULL: not wanted).  With T = 0 dweight and dbias
+ * are zeros.
+ */
+basp_status basp_layer_norm_grad(const basp_norm_plan *plan, const void *dy, const void *x, const void *weight,
+                                 const float *mean, const float *rstd, void *dx, void *dweight, void *dbias, void *ws,
+                                 void *stream);
+
+/*
+ * Balance loss and per-expert counts of an expert plan's router: T tokens with
+ * scores for E experts, of which each chose K.
+ *   p[t]      = softmax(logits[t])
+ *   L           live tokens: those with mask[t] != 0 (mask NULL: all)
+ *   counts[e] = kept choices of e (ids[t][k] = e) by live tokens
+ *   slope[e]  = coef * E * counts[e] / (K * L) / L        (0 if L is 0)
+ *   loss      = sum over e of slope[e] * sum over live t of p[t][e]
+ * The loss is coef where choices and probabilities are spread evenly.
+ *   logits [T][E] (weight_dtype), ids [T][K] as for basp_expert_sort, mask [T]
+ *   bytes, loss [1] fp32, counts [E] int32, slope [E] fp32, ws of
+ *   basp_balance_workspace_bytes(plan) bytes (0 for a NULL plan).
+ * Scores and choices of masked tokens take no part, whatever the scores are.
+ * coef finite (BASP_ERR_INVALID).
+ */
+size_t basp_balance_workspace_bytes(const basp_expert_plan *plan);
+basp_status basp_balance_loss(const basp_expert_plan *plan, const void *logits, const void *ids, const uint8_t *mask,
+                              float coef, float *loss, int32_t *counts, float *slope, void *ws, void *stream);
+
+/*
+ * Gradient of the loss for the scores, the counts being constants:
+ *   dlogits[t][j] = dloss * p[t][j] * (slope[j] - sum over e of slope[e] * p[t][e]),
+ * zeros for masked tokens.  slope as basp_balance_loss wrote it, dloss [1] fp32.
+ */
+basp_status basp_balance_loss_grad(const basp_expert_plan *plan, const void *logits, const uint8_t *mask,
+                                   const float *slope, const float *dloss, void *dlogits, void *stream);
+
 /* Status of the last call made by this thread, and a static description.
  * (Error reporting: not a step of the method.) */
 basp_status basp_last_error(void);

@@ -72,6 +72,23 @@ class basp_embed_info(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class basp_attention_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("S", "queries", "window")] + [
+        (n, ctypes.c_int32) for n in ("sinks", "shards", "B", "Hl_q", "Hl_kv", "d", "layout", "dtype")] + [
+        (n, ctypes.c_int64) for n in ("q_elems", "kv_elems", "lse_elems", "workspace_bytes", "grad_workspace_bytes")]
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class basp_norm_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "D")] + [
+        (n, ctypes.c_int32) for n in ("dtype", "weight_dtype")] + [("workspace_bytes", ctypes.c_int64)]
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
 class basp_tuning(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "vectors_per_thread", "tile_tokens", "tile_heads", "cache_policy", "max_grid",
@@ -162,6 +179,33 @@ _lib.basp_embed_to_seq.argtypes = [_plan_p, _vp, _vp, ctypes.c_float, _vp, _vp]
 _lib.basp_embed_to_seq.restype = _i32
 _lib.basp_embed_to_seq_grad.argtypes = [_plan_p, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp]
 _lib.basp_embed_to_seq_grad.restype = _i32
+_f32 = ctypes.c_float
+_lib.basp_attention_plan_create.argtypes = [_plan_p, _i64, _i64, _i64]
+_lib.basp_attention_plan_create.restype = _plan_p
+_lib.basp_attention_plan_destroy.argtypes = [_plan_p]
+_lib.basp_attention_plan_destroy.restype = None
+_lib.basp_attention_plan_query.argtypes = [_plan_p, ctypes.POINTER(basp_attention_info)]
+_lib.basp_attention_plan_query.restype = _i32
+_lib.basp_attention.argtypes = [_plan_p] + [_vp] * 5 + [_f32] + [_vp] * 4
+_lib.basp_attention.restype = _i32
+_lib.basp_attention_grad.argtypes = [_plan_p] + [_vp] * 8 + [_f32] + [_vp] * 5
+_lib.basp_attention_grad.restype = _i32
+_lib.basp_norm_plan_create.argtypes = [_i64, _i64, _i32, _i32]
+_lib.basp_norm_plan_create.restype = _plan_p
+_lib.basp_norm_plan_destroy.argtypes = [_plan_p]
+_lib.basp_norm_plan_destroy.restype = None
+_lib.basp_norm_plan_query.argtypes = [_plan_p, ctypes.POINTER(basp_norm_info)]
+_lib.basp_norm_plan_query.restype = _i32
+_lib.basp_layer_norm.argtypes = [_plan_p] + [_vp] * 3 + [_f32] + [_vp] * 4
+_lib.basp_layer_norm.restype = _i32
+_lib.basp_layer_norm_grad.argtypes = [_plan_p] + [_vp] * 10
+_lib.basp_layer_norm_grad.restype = _i32
+_lib.basp_balance_workspace_bytes.argtypes = [_plan_p]
+_lib.basp_balance_workspace_bytes.restype = ctypes.c_size_t
+_lib.basp_balance_loss.argtypes = [_plan_p] + [_vp] * 3 + [_f32] + [_vp] * 5
+_lib.basp_balance_loss.restype = _i32
+_lib.basp_balance_loss_grad.argtypes = [_plan_p] + [_vp] * 6
+_lib.basp_balance_loss_grad.restype = _i32
 _lib.basp_last_error.argtypes = []
 _lib.basp_last_error.restype = _i32
 _lib.basp_status_str.argtypes = [_i32]
@@ -445,6 +489,8 @@ class ExpertPlan:
         self.pos, self.order = (i32, i["slots"]), (i32, i["max_rows"])
         self.offsets, self.counts = (i32, i["E"] + 1), (i32, i["E"])
         self.tokens, self.rows, self.weights = (dt, tokens), (dt, rows), (wt, i["slots"])
+        self.logits, self.scalar, self.slope = (wt, i["T"] * i["E"]), (torch.float32, 1), (torch.float32, i["E"])
+        self.balance_bytes = basp_balance_workspace_bytes(self)
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -491,8 +537,8 @@ def _addr(x, of, name: str, device: int):
     raise ValueError("%s holds %d elements, the plan needs %d" % (name, x.numel(), of[1]))
 
 
-def _ws_addr(ws, plan, device: int):
-    need = plan.info["workspace_bytes"]
+def _ws_addr(ws, plan, device: int, need=None):
+    need = plan.info["workspace_bytes"] if need is None else need
     if ws is None or isinstance(ws, int):
         return ws
     if not ws.is_cuda or not ws.is_contiguous():
@@ -619,3 +665,149 @@ def basp_embed_to_seq_grad(plan: EmbedPlan, ids, dout, scale, accumulate, dtable
     _check(_lib.basp_embed_to_seq_grad(
         plan.handle, _addr(ids, plan.ids, "ids", d), _addr(dout, plan.tokens, "dout", d), scale, bool(accumulate),
         _addr(dtable, plan.grad, "dtable", d), _ws_addr(ws, plan, d), _stream_on(d, stream)), "basp_embed_to_seq_grad")
+
+
+# ------------------------------------- attention, layer norm, balance loss --
+
+class AttentionPlan:
+    """Owner of a ``basp_attention_plan*``; destroyed with the object.  ``info``
+    holds the ``basp_attention_plan_query`` result as a dict."""
+
+    def __init__(self, handle: int):
+        self.handle = handle
+        self.info = i = basp_attention_plan_query(self)
+        dt = _torch_dtype(i["dtype"])
+        self.q, self.kv, self.lse = (dt, i["q_elems"]), (dt, i["kv_elems"]), (torch.float32, i["lse_elems"])
+        self.per_sequence = (torch.int32, i["B"])
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _lib is not None:   # _lib is None during interpreter shutdown
+            _lib.basp_attention_plan_destroy(h)
+
+
+class NormPlan:
+    """Owner of a ``basp_norm_plan*``; destroyed with the object.  ``info`` holds
+    the ``basp_norm_plan_query`` result as a dict."""
+
+    def __init__(self, handle: int):
+        self.handle = handle
+        self.info = i = basp_norm_plan_query(self)
+        self.rows = (_torch_dtype(i["dtype"]), i["T"] * i["D"])
+        self.weight, self.stats = (_torch_dtype(i["weight_dtype"]), i["D"]), (torch.float32, i["T"])
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _lib is not None:   # _lib is None during interpreter shutdown
+            _lib.basp_norm_plan_destroy(h)
+
+
+def basp_attention_plan_create(layout: Plan, queries, window, sinks=0) -> AttentionPlan:
+    """``layout``: the Plan whose head shards hold the keys and values."""
+    if not isinstance(layout, Plan):
+        raise TypeError("layout must be a Plan")
+    _check_bits(64, queries=queries, window=window, sinks=sinks)
+    h = _lib.basp_attention_plan_create(layout.handle, queries, window, sinks)
+    if not h:
+        raise BaspError(_lib.basp_last_error(), "basp_attention_plan_create")
+    return AttentionPlan(h)
+
+
+def basp_attention_plan_destroy(plan: AttentionPlan) -> None:
+    h, plan.handle = plan.handle, None
+    _lib.basp_attention_plan_destroy(h)
+
+
+def basp_attention_plan_query(plan: AttentionPlan) -> dict:
+    info = basp_attention_info()
+    _check(_lib.basp_attention_plan_query(plan.handle, ctypes.byref(info)), "basp_attention_plan_query")
+    return info.as_dict()
+
+
+def basp_attention(plan: AttentionPlan, q, k, v, starts, lengths, scale, o, lse, ws, stream=None) -> None:
+    """starts, lengths and lse may be None."""
+    d = torch.cuda.current_device()
+    _check(_lib.basp_attention(
+        plan.handle, _addr(q, plan.q, "q", d), _addr(k, plan.kv, "k", d), _addr(v, plan.kv, "v", d),
+        _addr(starts, plan.per_sequence, "starts", d), _addr(lengths, plan.per_sequence, "lengths", d), scale,
+        _addr(o, plan.q, "o", d), _addr(lse, plan.lse, "lse", d), _ws_addr(ws, plan, d), _stream_on(d, stream)),
+        "basp_attention")
+
+
+def basp_attention_grad(plan: AttentionPlan, q, k, v, o, lse, dout, starts, lengths, scale, dq, dk, dv, ws,
+                        stream=None) -> None:
+    """starts and lengths as they were given to basp_attention."""
+    d = torch.cuda.current_device()
+    _check(_lib.basp_attention_grad(
+        plan.handle, _addr(q, plan.q, "q", d), _addr(k, plan.kv, "k", d), _addr(v, plan.kv, "v", d),
+        _addr(o, plan.q, "o", d), _addr(lse, plan.lse, "lse", d), _addr(dout, plan.q, "dout", d),
+        _addr(starts, plan.per_sequence, "starts", d), _addr(lengths, plan.per_sequence, "lengths", d), scale,
+        _addr(dq, plan.q, "dq", d), _addr(dk, plan.kv, "dk", d), _addr(dv, plan.kv, "dv", d),
+        _ws_addr(ws, plan, d, plan.info["grad_workspace_bytes"]), _stream_on(d, stream)), "basp_attention_grad")
+
+
+def basp_norm_plan_create(T, D, dtype=BASP_BF16, weight_dtype=BASP_FP32) -> NormPlan:
+    _check_bits(64, T=T, D=D)
+    _check_bits(32, dtype=dtype, weight_dtype=weight_dtype)
+    h = _lib.basp_norm_plan_create(T, D, dtype, weight_dtype)
+    if not h:
+        raise BaspError(_lib.basp_last_error(), "basp_norm_plan_create")
+    return NormPlan(h)
+
+
+def basp_norm_plan_destroy(plan: NormPlan) -> None:
+    h, plan.handle = plan.handle, None
+    _lib.basp_norm_plan_destroy(h)
+
+
+def basp_norm_plan_query(plan: NormPlan) -> dict:
+    info = basp_norm_info()
+    _check(_lib.basp_norm_plan_query(plan.handle, ctypes.byref(info)), "basp_norm_plan_query")
+    return info.as_dict()
+
+
+def basp_layer_norm(plan: NormPlan, x, weight, bias, eps, y, mean, rstd, stream=None) -> None:
+    """bias, mean and rstd may be None."""
+    d = torch.cuda.current_device()
+    _check(_lib.basp_layer_norm(
+        plan.handle, _addr(x, plan.rows, "x", d), _addr(weight, plan.weight, "weight", d),
+        _addr(bias, plan.weight, "bias", d), eps, _addr(y, plan.rows, "y", d), _addr(mean, plan.stats, "mean", d),
+        _addr(rstd, plan.stats, "rstd", d), _stream_on(d, stream)), "basp_layer_norm")
+
+
+def basp_layer_norm_grad(plan: NormPlan, dy, x, weight, mean, rstd, dx, dweight, dbias, ws, stream=None) -> None:
+    """dbias may be None."""
+    d = torch.cuda.current_device()
+    _check(_lib.basp_layer_norm_grad(
+        plan.handle, _addr(dy, plan.rows, "dy", d), _addr(x, plan.rows, "x", d), _addr(weight, plan.weight, "weight", d),
+        _addr(mean, plan.stats, "mean", d), _addr(rstd, plan.stats, "rstd", d), _addr(dx, plan.rows, "dx", d),
+        _addr(dweight, plan.weight, "dweight", d), _addr(dbias, plan.weight, "dbias", d), _ws_addr(ws, plan, d),
+        _stream_on(d, stream)), "basp_layer_norm_grad")
+
+
+def basp_balance_workspace_bytes(plan: ExpertPlan) -> int:
+    return int(_lib.basp_balance_workspace_bytes(plan.handle))
+
+
+def _mask_addr(mask, plan: ExpertPlan, device: int):
+    """Truth values or bytes, one a token."""
+    of = (getattr(mask, "dtype", None) if getattr(mask, "dtype", None) is torch.bool else torch.uint8, plan.info["T"])
+    return _addr(mask, of, "mask", device)
+
+
+def basp_balance_loss(plan: ExpertPlan, logits, ids, mask, coef, loss, counts, slope, ws, stream=None) -> None:
+    """mask (torch.bool or torch.uint8) may be None."""
+    d = torch.cuda.current_device()
+    _check(_lib.basp_balance_loss(
+        plan.handle, _addr(logits, plan.logits, "logits", d), _addr(ids, plan.ids, "ids", d), _mask_addr(mask, plan, d),
+        coef, _addr(loss, plan.scalar, "loss", d), _addr(counts, plan.counts, "counts", d),
+        _addr(slope, plan.slope, "slope", d), _ws_addr(ws, plan, d, plan.balance_bytes), _stream_on(d, stream)),
+        "basp_balance_loss")
+
+
+def basp_balance_loss_grad(plan: ExpertPlan, logits, mask, slope, dloss, dlogits, stream=None) -> None:
+    d = torch.cuda.current_device()
+    _check(_lib.basp_balance_loss_grad(
+        plan.handle, _addr(logits, plan.logits, "logits", d), _mask_addr(mask, plan, d), _addr(slope, plan.slope, "slope", d),
+        _addr(dloss, plan.scalar, "dloss", d), _addr(dlogits, plan.logits, "dlogits", d), _stream_on(d, stream)),
+        "basp_balance_loss_grad")

@@ -17,8 +17,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbasp.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("plan.cpp", "launch.cpp", "index_plan.cpp", "relayout.hip",
-                                           "expert.hip", "embed.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("plan.cpp", "launch.cpp", "index_plan.cpp", "layer_plan.cpp", "attention_plan.cpp",
+                                           "relayout.hip", "expert.hip", "embed.hip", "norm.hip", "balance.hip",
+                                           "attention.hip", "attention_grad.hip")]
 ARCH = "gfx950"
 
 

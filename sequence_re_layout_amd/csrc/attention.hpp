@@ -1,0 +1,453 @@
+// attention.hpp -- what the kernels of attention share: the matrix products of a
+// wave, tiles of rows in LDS, and which keys a query sees.
+//
+// All products are 32 x 32 results of one wave with v_mfma_f32_32x32x16 (bf16,
+// fp16) or eight v_mfma_f32_32x32x2 (fp32).  A lane's operands are eight
+// consecutive numbers of k of one row (A) or column (B) lane % 32, the upper 32
+// lanes those after the lower ones'; its results are 16 rows of column
+// lane % 32, register i being row 8*(i / 4) + 4*(lane / 32) + i % 4.
+//
+// The kernels keep one side of every product in registers, a column a lane
+// (queries in the forward pass and the gradient of q, keys in the gradients of k
+// and v), and stream rows of the other side through LDS.  With scores as results
+// (streamed row, own column), softmax statistics are a lane's own but for one
+// exchange between the halves of the wave, and the weights P are at once the B
+// operand of the product that follows: its k are the streamed rows, and any
+// order of them does as long as both operands have the same.  Slot i of a
+// 16-row step is row 8*(i / 4) + 4*(lane / 32) + i % 4 in both.  The A operand of
+// that product is the tile read along its rows, transposed on the way by
+// ds_read_b64_tr_b16.
+//
+// A tile's rows lie in LDS in chunks of 16 bytes that are exchanged within a row
+// (chunk c of row r at place c ^ swizzle(r)), so that eight rows read along a
+// column, and four rows read transposed, fall on all banks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#define BASP_HD __host__ __device__
+#include "attention_plan.hpp"
+#include "barrier.hpp"
+#include "rowvec.hpp"
+
+namespace basp {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <typename T> struct Of;
+template <> struct Of<__bf16> {
+    static constexpr uint32_t exponent = 0x7f807f80u, carry = 0x00800080u, top = 0x80008000u;
+    typedef __bf16 x8 __attribute__((ext_vector_type(8)));
+};
+template <> struct Of<_Float16> {
+    static constexpr uint32_t exponent = 0x7c007c00u, carry = 0x04000400u, top = 0x80008000u;
+    typedef _Float16 x8 __attribute__((ext_vector_type(8)));
+};
+template <> struct Of<float> {
+    static constexpr uint32_t exponent = 0x7f800000u, carry = 0x00800000u, top = 0x80000000u;
+    typedef float x8 __attribute__((ext_vector_type(8)));
+};
+template <typename T> using Vec8 = typename Of<T>::x8;
+
+// Whether one of the numbers is infinite or NaN (its exponent is all ones).
+template <typename T>
+__device__ inline bool wild(Vec8<T> x)
+{
+    typedef uint32_t words __attribute__((ext_vector_type(sizeof(T) * 2)));
+    const words w = __builtin_bit_cast(words, x);
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) * 2); ++i)
+        any |= (w[i] & Of<T>::exponent) + Of<T>::carry;
+    return any & Of<T>::top;
+}
+
+__device__ inline f32x16 product(Vec8<__bf16> a, Vec8<__bf16> b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ inline f32x16 product(Vec8<_Float16> a, Vec8<_Float16> b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+// Each of the eight takes one number of k from either half of the wave.
+__device__ inline f32x16 product(Vec8<float> a, Vec8<float> b, f32x16 c)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+}
+
+// Row of register i of a result, and of slot i of a 16-row step.
+__device__ inline int row_of(int i, int half) { return 8 * (i / 4) + 4 * half + i % 4; }
+
+// Registers 8*s to 8*s + 7 of a result as the B operand of the next product: the
+// one rounding of P (or dS) to the inputs' type, which the matrix instruction
+// takes.  The softmax's sum is taken of the unrounded values.
+template <typename T>
+__device__ inline Vec8<T> operand(const f32x16 &c, int s)
+{
+    Vec8<T> r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        r[i] = static_cast<T>(c[8 * s + i]);
+    return r;
+}
+
+__device__ inline float other_half(float x) { return __shfl_xor(x, 32); }
+
+// ------------------------------------------------------------------- tiles --
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+// ROWS rows of C channels in LDS.
+template <typename T, int C, int ROWS>
+struct Tile {
+    static constexpr int kRow = C * sizeof(T), kChunks = kRow / 16, kBytes = ROWS * kRow;
+    static constexpr int kPer = 16 / sizeof(T);        // numbers of a chunk
+
+    // Eight chunks a row: two rows span the banks, so that the row's lowest bit
+    // is left out.  Sixteen and more: the low bits of the row move chunks by
+    // four, the next ones by one.
+    static __device__ inline uint32_t swizzle(uint32_t r)
+    {
+        return kChunks == 8 ? ((r >> 1 & 1) << 2) | (r >> 2 & 3) : ((r & 3) << 2) | (r >> 2 & 3);
+    }
+
+    // The A operand of scores: row `row0` + lane % 32, channels 16*s on.
+    static __device__ inline Vec8<T> along_channels(const char *tile, int row0, int s)
+    {
+        const uint32_t lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
+        const char *const at = tile + (row0 + r) * kRow;
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t c = (2 * s) ^ (half ^ swizzle(r));
+            return *reinterpret_cast<const Vec8<T> *>(at + c * 16);
+        } else {
+            typedef float x4 __attribute__((ext_vector_type(4)));
+            const uint32_t c = (4 * s) ^ ((2 * half) ^ swizzle(r));
+            const x4 lo = *reinterpret_cast<const x4 *>(at + c * 16), hi = *reinterpret_cast<const x4 *>(at + (c ^ 1) * 16);
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    }
+
+    // The A operand of sums over rows: channel 32*block + lane % 32 of the slots
+    // of the 16 rows from row0 on.
+    static __device__ inline Vec8<T> along_rows(const char *tile, int row0, int block)
+    {
+        const uint32_t lane = threadIdx.x & 63, half = lane >> 5;
+        if constexpr (sizeof(T) == 2) {
+            // 16 lanes read four rows of 16 channels, four channels each, and
+            // receive a channel each of the four rows
+            const uint32_t l = lane & 15, r = 4 * half + (l >> 2), group = lane >> 4 & 1;
+            const uint32_t c = (2 * group + (l >> 1 & 1)) ^ swizzle(r);
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            s16x4 part[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // swizzle(r + 8 j) == swizzle(r) ^ 2 j
+                const uint32_t off = (row0 + 8 * j + r) * kRow + ((4 * block) ^ (2 * j) ^ c) * 16 + (l & 1) * 8;
+                part[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_char *)(tile + off));
+            }
+            typedef short s16x8 __attribute__((ext_vector_type(8)));
+            return __builtin_bit_cast(Vec8<T>, s16x8(__builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7)));
+        } else {
+            Vec8<T> v;
+            const uint32_t c = block * 8 + ((lane & 31) >> 2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t r = row0 + row_of(i, half);
+                v[i] = *reinterpret_cast<const float *>(tile + r * kRow + ((c ^ swizzle(r)) * 16) + (lane & 3) * 4);
+            }
+            return v;
+        }
+    }
+
+    // One number.
+    static __device__ inline float at(const char *tile, int row, int channel)
+    {
+        const uint32_t c = (uint32_t(channel) / kPer) ^ swizzle(row);
+        return static_cast<float>(*reinterpret_cast<const T *>(tile + row * kRow + c * 16 + (channel % kPer) * sizeof(T)));
+    }
+
+    // Rows of `d` channels, `token` bytes apart, into the tile by THREADS threads:
+    // zeros after row `rows` and channel d.  DIRECT: rows of whole 16-byte chunks
+    // at 16-byte addresses go from memory to LDS without passing registers; the
+    // loads are complete after wait_tiles and a barrier.
+    template <int THREADS, bool DIRECT>
+    static __device__ inline void load(char *__restrict__ tile, const char *from, uint32_t token, int rows, int d)
+    {
+        const uint32_t thread = threadIdx.x % THREADS;
+        constexpr int STEPS = kBytes / 16 / THREADS;
+        static_assert(kBytes % (16 * THREADS) == 0, "whole rounds of the threads");
+        if constexpr (DIRECT) {
+            const __amdgpu_buffer_rsrc_t from_rows =
+                __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(from), 0, 0x7ffffff0, 0x00020000);
+#pragma unroll
+            for (int p = 0; p < STEPS; ++p) {
+                const uint32_t i = p * THREADS + thread, r = i / kChunks, c = (i % kChunks) ^ swizzle(r);
+                // beyond the buffer: reads as zeros
+                const uint32_t off = int(r) < rows && int(c) * kPer < d ? r * token + c * 16 : 0x80000000u;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    from_rows, (lds_char *)(tile + (p * THREADS + (thread & ~63u)) * 16), 16, off, 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < STEPS; ++p) {
+                const uint32_t i = p * THREADS + thread, r = i / kChunks, c = (i % kChunks) ^ swizzle(r);
+                typedef T xn __attribute__((ext_vector_type(kPer)));
+                xn x = {};
+                if (int(r) < rows)
+                    x = chunk(from + uint64_t(r) * token, int(c) * kPer, d);
+                *reinterpret_cast<xn *>(tile + i * 16) = x;
+            }
+        }
+    }
+
+    // Channels c to c + kPer - 1 of a row of d, zeros after it.
+    static __device__ inline auto chunk(const char *row, int c, int d)
+    {
+        typedef T xn __attribute__((ext_vector_type(kPer)));
+        xn x = {};
+        if (c + kPer <= d)
+            return __builtin_bit_cast(xn, *reinterpret_cast<const u32x4m *>(row + c * sizeof(T)));
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (c + i < d)
+                x[i] = reinterpret_cast<const T *>(row)[c + i];
+        return x;
+    }
+};
+
+// Up to 64 floats straight to LDS by a wave, zeros after n.
+__device__ inline void load_floats(float *to, const float *from, int n)
+{
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(from), 0, n * 4, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_char *)to, 4, (threadIdx.x & 63) * 4, 0, 0, 0);
+}
+
+// The wave's loads to LDS have arrived.
+__device__ inline void wait_tiles() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Eight channels of the row that a lane keeps, zeros after d.
+template <typename T>
+__device__ inline Vec8<T> row_part(const char *row, int c, int d)
+{
+    typedef Tile<T, 64, 1> R;
+    if constexpr (sizeof(T) == 2)
+        return R::chunk(row, c, d);
+    else
+        return __builtin_shufflevector(R::chunk(row, c, d), R::chunk(row, c + 4, d), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// sums[b] += (32 channels of block b) x (N rows from row0 on of the tile),
+// weighted by p, which holds N / 32 results of 32 rows.  PART: some rows are hidden from some
+// columns, which then have the weight 0.  A product of 0 and an infinity or NaN
+// would be NaN, so a step with such numbers is added up without the zeros.
+template <typename T, int C, int ROWS, int N, bool PART, int BLOCKS>
+__device__ inline void add_rows(f32x16 (&sums)[BLOCKS], const char *tile, int row0, const f32x16 (&p)[N / 32])
+{
+    typedef Tile<T, C, ROWS> Rows;
+#pragma unroll
+    for (int s = 0; s < N / 16; ++s) {
+        const Vec8<T> weights = operand<T>(p[s / 2], s % 2);
+        Vec8<T> a[BLOCKS];
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+            a[b] = Rows::along_rows(tile, row0 + 16 * s, b);
+        if constexpr (PART) {
+            bool any = false;
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b)
+                any |= wild<T>(a[b]);
+            if (__ballot(any)) {
+                const int half = (threadIdx.x & 63) >> 5;
+                // a slot of either half at a time, its weight picked out of the operand
+#pragma clang loop unroll(disable)
+                for (int i = 0; i < 16; ++i) {
+                    float w = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        w = i % 8 == j ? static_cast<float>(weights[j]) : w;
+                    const float across = other_half(w);
+                    w = (i >> 3) == half ? w : across;
+                    const int row = row0 + 16 * s + row_of(i % 8, i >> 3);
+#pragma unroll
+                    for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const float x = Rows::at(tile, row, 32 * b + row_of(r, half));
+                            sums[b][r] = w != 0.f ? fmaf(w, x, sums[b][r]) : sums[b][r];
+                        }
+                }
+                continue;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+            sums[b] = product(a[b], weights, sums[b]);
+    }
+}
+
+// ---------------------------------------------------------- who sees what --
+
+// What a kernel needs of a call to find its rows and keys.
+struct AttendShape {
+    const int32_t *starts, *lengths;
+    int32_t S, queries, reach, firsts;          // as in the plan
+    int32_t Hl_q, Hl_kv, ratio, P, Bl, d, total;    // total: queries * ratio
+    uint32_t q_token, kv_token;
+    int64_t q_head, q_shard, kv_head, kv_shard;
+    FastDiv by_ratio, by_heads, by_Bl, by_P;
+    float scale, scale_log2;                    // log2(e) * scale: exponents are powers of two
+};
+
+// The sequence of a shard, its length and the position of its first query.
+struct Sequence {
+    int length, start;
+};
+
+__device__ inline Sequence sequence_of(const AttendShape &A, uint32_t shard)
+{
+    // shards are [groups][P][Bl]
+    const uint32_t rank = fastdiv(shard, A.by_Bl), b = fastdiv(rank, A.by_P) * A.Bl + (shard - rank * A.Bl);
+    Sequence s;
+    s.length = A.S;
+    if (A.lengths) {
+        const int n = scalar(A.lengths[b]);
+        s.length = n < 0 ? 0 : n > A.S ? A.S : n;
+    }
+    s.start = A.starts ? int(scalar(A.starts[b])) : A.queries < A.S ? s.length - A.queries : 0;
+    // farther out, no row has a position within the sequence either
+    s.start = s.start < -A.queries ? -A.queries : s.start > A.S ? A.S : s.start;
+    return s;
+}
+
+__device__ inline bool sees(const AttendShape &A, int position, int key)
+{
+    return key <= position && (position - key < A.reach || key < A.firsts);
+}
+
+// Tiles of keys that positions [low, high] see, KEYS each: first those of the
+// sinks before the window, then those of the window.
+template <int KEYS>
+struct KeyTiles {
+    int sinks_end, window, end, sink_tiles, tiles;
+
+    __device__ inline KeyTiles(const AttendShape &A, int low, int high)
+    {
+        window = low - A.reach + 1 > 0 ? low - A.reach + 1 : 0;
+        end = high + 1;
+        sinks_end = A.firsts < window ? A.firsts : window;
+        sink_tiles = (sinks_end + KEYS - 1) / KEYS;
+        tiles = high < low ? 0 : sink_tiles + (end - window + KEYS - 1) / KEYS;
+    }
+    __device__ inline int first(int i) const { return i < sink_tiles ? i * KEYS : window + (i - sink_tiles) * KEYS; }
+    __device__ inline int rows(int i) const
+    {
+        const int n = (i < sink_tiles ? sinks_end : end) - first(i);
+        return n < KEYS ? n : KEYS;
+    }
+};
+
+// How positions [low, high] of a wave see the keys [first, first + rows).
+enum class Seen { none, some, all };
+
+__device__ inline Seen how_seen(const AttendShape &A, int low, int high, int first, int rows)
+{
+    const int last = first + rows - 1;
+    if (low > high || first > high || (low - last >= A.reach && first >= A.firsts))
+        return Seen::none;
+    return last <= low && (high - first < A.reach || last < A.firsts) ? Seen::all : Seen::some;
+}
+
+__device__ inline int wave_min(int x)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_xor(x, d);
+        x = y < x ? y : x;
+    }
+    return scalar(x);
+}
+
+__device__ inline int wave_max(int x) { return -wave_min(-x); }
+
+// A lane's column: a query and a head of the key head's group.
+struct Column {
+    int position;
+    bool exists, live;
+    uint32_t query, head;
+
+    __device__ inline Column(const AttendShape &A, const Sequence &s, uint32_t column, uint32_t key_head)
+    {
+        exists = column < uint32_t(A.total);
+        query = fastdiv(column, A.by_ratio);
+        head = key_head * A.ratio + (column - query * A.ratio);
+        position = s.start + int(query);
+        live = exists && position >= 0 && position < s.length;
+    }
+    __device__ inline int64_t at(const AttendShape &A, uint32_t shard) const
+    {
+        return shard * A.q_shard + head * A.q_head + int64_t{query} * A.q_token;
+    }
+    __device__ inline int64_t row(const AttendShape &A, uint32_t shard) const
+    {
+        return (int64_t{shard} * A.Hl_q + head) * A.queries + query;
+    }
+};
+
+template <typename T, int C>
+__device__ inline void load_column(const AttendShape &A, const char *row, bool live, Vec8<T> (&x)[C / 16])
+{
+    const int half = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int c = 0; c < C / 16; ++c) {
+        x[c] = Vec8<T>{};
+        if (live)
+            x[c] = row_part<T>(row, 16 * c + 8 * half, A.d);
+    }
+}
+
+// Work-group number `id` of `all`, so that each of the eight XCDs takes
+// neighbours, which read the same keys: id % 8 is the XCD.
+__device__ inline uint32_t by_xcd(uint32_t id, uint32_t all)
+{
+    const uint32_t x = id & 7, each = all >> 3, more = all & 7;
+    return x * each + (x < more ? x : more) + (id >> 3);
+}
+
+// What the wave's lanes wrote to LDS or read from it is done before what follows.
+__device__ inline void wave_order()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// lse from a maximum in the scores' units and the sum relative to it.
+__device__ inline float log_sum(float m, float l, const AttendShape &A)
+{
+    return m == -INFINITY ? -INFINITY : (m * A.scale_log2 + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+}
+
+// Four channels of a result's rows as stored.
+template <typename T>
+__device__ inline void store_four(char *row, int c, int d, const float (&x)[4])
+{
+    if (c + 4 <= d) {
+        store_values<T, 4>(row + c * sizeof(T), x);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (c + i < d)
+            reinterpret_cast<T *>(row)[c + i] = static_cast<T>(x[i]);
+}
+
+}  // namespace basp

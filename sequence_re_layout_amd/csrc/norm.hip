@@ -1,0 +1,526 @@
+// norm.hip -- layer norm of token rows and its gradients: the kernels and entry
+// points of the norm plans (basp.h, "Layer norm").
+//
+// Bound by HBM: a row is read once into registers, its mean and the sum of
+// squares about that mean are taken there in fp32 (two passes over registers,
+// so that a mean far from zero costs no digits), and it is written once.  The
+// gradient reads the row and its gradient once; the weight's and the bias's
+// gradients ride along in registers over the rows of a work-group, which leaves
+// one partial sum of each, and a second launch adds these in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#define BASP_HD __host__ __device__
+#include "layer_plan.hpp"
+#include "plan_internal.hpp"
+#include "rowvec.hpp"
+#include "runtime.hpp"
+#include "teams.hpp"
+
+namespace basp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kLaunchGroups = int64_t{1} << 22;     // work-groups of one launch: 32-bit global size
+
+struct NormDesc {
+    const char *x;
+    const void *weight, *bias;
+    char *y;
+    float *mean, *rstd;
+    uint32_t rows, row, vecs, D;    // row: bytes
+    float eps, inv_D;
+    basp_dtype weight_dtype;
+};
+
+// Elements at the front of vector a that the vector before it holds too.
+template <typename E, int VW>
+__device__ inline uint32_t shared_front(uint32_t a, uint32_t off)
+{
+    return (a * VW - off) / sizeof(E);
+}
+
+template <typename E, int VW>
+__device__ inline void norm_vector(const NormDesc &D, typename MemVec<VW>::type x, uint32_t off, float mean, float rstd,
+                                   char *y)
+{
+    constexpr int N = VW / sizeof(E);
+    float f[N], w[N], o[N];
+    unpack<E, VW>(x, f);
+    load_any<N>(D.weight, off / sizeof(E), D.weight_dtype, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        o[i] = (f[i] - mean) * rstd * w[i];
+    if (D.bias) {
+        load_any<N>(D.bias, off / sizeof(E), D.weight_dtype, w);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            o[i] += w[i];
+    }
+    store_vec<VW>(y + off, pack<E, VW>(o));
+}
+
+// LANES lanes take a row, R vectors each.
+template <typename E, int VW, int LANES, int R>
+__global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void norm_kernel(const NormDesc D)
+{
+    constexpr int N = VW / sizeof(E), TEAMS = LANES > kThreads ? 1 : kThreads / LANES;
+    __shared__ float lds[2][LANES > 64 ? LANES / 64 : 1];
+    const uint32_t lane = threadIdx.x % LANES, t = blockIdx.x * TEAMS + threadIdx.x / LANES;
+    const bool live = t < D.rows;
+    const char *x = D.x + uint64_t(live ? t : 0) * D.row;
+    typename MemVec<VW>::type v[R];
+    float sum[1] = {0.f}, sq[1] = {0.f};
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (lane + r * LANES < D.vecs)
+            v[r] = load_vec<VW, false>(x + vec_offset<VW>(lane + r * LANES, D.row));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint32_t a = lane + r * LANES;
+        if (a < D.vecs) {
+            const uint32_t seen = shared_front<E, VW>(a, vec_offset<VW>(a, D.row));
+            float f[N];
+            unpack<E, VW>(v[r], f);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                sum[0] += uint32_t(i) < seen ? 0.f : f[i];
+        }
+    }
+    team_sum<LANES, 1>(sum, lds[0]);
+    const float mean = sum[0] * D.inv_D;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint32_t a = lane + r * LANES;
+        if (a < D.vecs) {
+            const uint32_t seen = shared_front<E, VW>(a, vec_offset<VW>(a, D.row));
+            float f[N];
+            unpack<E, VW>(v[r], f);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                sq[0] += uint32_t(i) < seen ? 0.f : (f[i] - mean) * (f[i] - mean);
+        }
+    }
+    team_sum<LANES, 1>(sq, lds[1]);
+    const float rstd = 1.f / sqrtf(sq[0] * D.inv_D + D.eps);
+    if (!live)
+        return;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (lane + r * LANES < D.vecs)
+            norm_vector<E, VW>(D, v[r], vec_offset<VW>(lane + r * LANES, D.row), mean, rstd, D.y + uint64_t(t) * D.row);
+    if (lane == 0) {
+        if (D.mean)
+            D.mean[t] = mean;
+        if (D.rstd)
+            D.rstd[t] = rstd;
+    }
+}
+
+// Rows of more vectors than the registers of a work-group hold: read three
+// times, the second and third time from the caches.
+template <typename E>
+__global__ __launch_bounds__(1024) void norm_long_kernel(const NormDesc D)
+{
+    constexpr int N = 16 / sizeof(E), LANES = 1024;
+    __shared__ float lds[2][LANES / 64];
+    const uint32_t t = blockIdx.x;
+    const char *x = D.x + uint64_t(t) * D.row;
+    float sum[1] = {0.f}, sq[1] = {0.f};
+    for (int pass = 0; pass < 2; ++pass) {
+        const float mean = sum[0] * D.inv_D;
+        float s = 0.f;
+        for (uint32_t a = threadIdx.x; a < D.vecs; a += LANES) {
+            const uint32_t off = vec_offset<16>(a, D.row), seen = shared_front<E, 16>(a, off);
+            float f[N];
+            unpack<E, 16>(load_vec<16, false>(x + off), f);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                s += uint32_t(i) < seen ? 0.f : pass ? (f[i] - mean) * (f[i] - mean) : f[i];
+        }
+        if (pass) {
+            sq[0] = s;
+            team_sum<LANES, 1>(sq, lds[1]);
+        } else {
+            sum[0] = s;
+            team_sum<LANES, 1>(sum, lds[0]);
+        }
+    }
+    const float mean = sum[0] * D.inv_D, rstd = 1.f / sqrtf(sq[0] * D.inv_D + D.eps);
+    for (uint32_t a = threadIdx.x; a < D.vecs; a += LANES) {
+        const uint32_t off = vec_offset<16>(a, D.row);
+        norm_vector<E, 16>(D, load_vec<16, false>(x + off), off, mean, rstd, D.y + uint64_t(t) * D.row);
+    }
+    if (threadIdx.x == 0) {
+        if (D.mean)
+            D.mean[t] = mean;
+        if (D.rstd)
+            D.rstd[t] = rstd;
+    }
+}
+
+// --------------------------------------------------------------- gradient --
+
+struct NormGradDesc {
+    const char *dy, *x;
+    const void *weight;
+    const float *mean, *rstd;
+    char *dx;
+    float *partial;                 // [groups][2][width], the weight's and the bias's
+    uint64_t rows;
+    uint32_t groups, row, vecs, D, width;
+    float inv_D;
+    basp_dtype weight_dtype;
+};
+
+// Columns of a work-group's partial sums from vectors of a row: those of a
+// vector that the one before holds too are left to it.
+template <typename E, int VW, int N>
+__device__ inline void store_columns(float *to, uint32_t a, uint32_t off, const float (&f)[N])
+{
+    const uint32_t seen = shared_front<E, VW>(a, off);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (uint32_t(i) >= seen)
+            to[off / sizeof(E) + i] = f[i];
+}
+
+// LANES lanes take a row, R vectors each; a work-group's teams take rows in
+// turn and keep the sums over them in registers.
+template <typename E, int VW, int LANES, int R>
+__global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void norm_grad_kernel(const NormGradDesc D)
+{
+    constexpr int N = VW / sizeof(E), TEAMS = LANES > kThreads ? 1 : kThreads / LANES;
+    __shared__ float lds[2][LANES > 64 ? LANES / 64 * 2 : 1];
+    __shared__ float joined[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? LANES * N * 2 : 1];
+    const uint32_t lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
+    float w[R][N], dw[R][N], db[R][N];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint32_t a = lane + r * LANES;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            w[r][i] = dw[r][i] = db[r][i] = 0.f;
+        if (a < D.vecs)
+            load_any<N>(D.weight, vec_offset<VW>(a, D.row) / sizeof(E), D.weight_dtype, w[r]);
+    }
+    int turn = 0;
+    for (uint64_t first = uint64_t(blockIdx.x) * TEAMS; first < D.rows; first += uint64_t(D.groups) * TEAMS, turn ^= 1) {
+        const uint64_t t = first + team;
+        const bool live = t < D.rows;
+        const uint64_t at = live ? t * D.row : 0;
+        typename MemVec<VW>::type xv[R], gv[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t a = lane + r * LANES;
+            if (live && a < D.vecs) {
+                gv[r] = load_vec<VW, false>(D.dy + at + vec_offset<VW>(a, D.row));
+                xv[r] = load_vec<VW, false>(D.x + at + vec_offset<VW>(a, D.row));
+            }
+        }
+        const float mean = live ? D.mean[t] : 0.f, rstd = live ? D.rstd[t] : 0.f;
+        float sums[2] = {0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t a = lane + r * LANES;
+            if (live && a < D.vecs) {
+                const uint32_t seen = shared_front<E, VW>(a, vec_offset<VW>(a, D.row));
+                float x[N], g[N];
+                unpack<E, VW>(xv[r], x);
+                unpack<E, VW>(gv[r], g);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float xhat = (x[i] - mean) * rstd, gw = g[i] * w[r][i];
+                    dw[r][i] = fmaf(g[i], xhat, dw[r][i]);
+                    db[r][i] += g[i];
+                    sums[0] += uint32_t(i) < seen ? 0.f : gw;
+                    sums[1] += uint32_t(i) < seen ? 0.f : gw * xhat;
+                }
+            }
+        }
+        team_sum<LANES, 2>(sums, lds[turn]);
+        const float c1 = sums[0] * D.inv_D, c2 = sums[1] * D.inv_D;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t a = lane + r * LANES;
+            if (live && a < D.vecs) {
+                float x[N], g[N];
+                unpack<E, VW>(xv[r], x);
+                unpack<E, VW>(gv[r], g);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    x[i] = rstd * (g[i] * w[r][i] - c1 - (x[i] - mean) * rstd * c2);
+                store_vec<VW>(D.dx + at + vec_offset<VW>(a, D.row), pack<E, VW>(x));
+            }
+        }
+    }
+    float *const mine = D.partial + uint64_t(blockIdx.x) * 2 * D.width;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint32_t a = lane + r * LANES;
+        if constexpr (TEAMS > 1) {          // the teams' sums, added by the first in their order
+            lds_barrier();
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                joined[team][i * LANES + lane] = dw[r][i];
+                joined[team][(N + i) * LANES + lane] = db[r][i];
+            }
+            lds_barrier();
+            if (team == 0)
+                for (int j = 1; j < TEAMS; ++j)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        dw[r][i] += joined[j][i * LANES + lane];
+                        db[r][i] += joined[j][(N + i) * LANES + lane];
+                    }
+        }
+        if (team == 0 && a < D.vecs) {
+            const uint32_t off = vec_offset<VW>(a, D.row);
+            store_columns<E, VW>(mine, a, off, dw[r]);
+            store_columns<E, VW>(mine + D.width, a, off, db[r]);
+        }
+    }
+}
+
+// Long rows: the gradient of x, a row a work-group, read twice.
+template <typename E>
+__global__ __launch_bounds__(1024) void norm_grad_long_kernel(const NormGradDesc D)
+{
+    constexpr int N = 16 / sizeof(E), LANES = 1024;
+    __shared__ float lds[LANES / 64 * 2];
+    const uint64_t t = blockIdx.x;
+    const float mean = D.mean[t], rstd = D.rstd[t];
+    float sums[2] = {0.f, 0.f};
+    for (int pass = 0; pass < 2; ++pass) {
+        for (uint32_t a = threadIdx.x; a < D.vecs; a += LANES) {
+            const uint32_t off = vec_offset<16>(a, D.row), seen = shared_front<E, 16>(a, off);
+            float x[N], g[N], w[N];
+            unpack<E, 16>(load_vec<16, false>(D.x + t * D.row + off), x);
+            unpack<E, 16>(load_vec<16, false>(D.dy + t * D.row + off), g);
+            load_any<N>(D.weight, off / sizeof(E), D.weight_dtype, w);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float xhat = (x[i] - mean) * rstd, gw = g[i] * w[i];
+                if (pass) {
+                    x[i] = rstd * (gw - sums[0] * D.inv_D - xhat * (sums[1] * D.inv_D));
+                } else {
+                    sums[0] += uint32_t(i) < seen ? 0.f : gw;
+                    sums[1] += uint32_t(i) < seen ? 0.f : gw * xhat;
+                }
+            }
+            if (pass)
+                store_vec<16>(D.dx + t * D.row + off, pack<E, 16>(x));
+        }
+        if (!pass)
+            team_sum<LANES, 2>(sums, lds);
+    }
+}
+
+// Long rows: the partial sums, a vector of columns a lane and every groups-th row.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void norm_columns_kernel(const NormGradDesc D)
+{
+    constexpr int N = 16 / sizeof(E);
+    const uint32_t a = blockIdx.x * kThreads + threadIdx.x;
+    if (a >= D.vecs)
+        return;
+    const uint32_t off = vec_offset<16>(a, D.row);
+    float dw[N] = {}, db[N] = {};
+    for (uint64_t t = blockIdx.y; t < D.rows; t += D.groups) {
+        const float mean = D.mean[t], rstd = D.rstd[t];
+        float x[N], g[N];
+        unpack<E, 16>(load_vec<16, false>(D.x + t * D.row + off), x);
+        unpack<E, 16>(load_vec<16, false>(D.dy + t * D.row + off), g);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            dw[i] = fmaf(g[i], (x[i] - mean) * rstd, dw[i]);
+            db[i] += g[i];
+        }
+    }
+    float *const mine = D.partial + uint64_t(blockIdx.y) * 2 * D.width;
+    store_columns<E, 16>(mine, a, off, dw);
+    store_columns<E, 16>(mine + D.width, a, off, db);
+}
+
+struct NormJoinDesc {
+    const float *partial;
+    void *dweight, *dbias;
+    uint32_t groups, D, width;
+    basp_dtype weight_dtype;
+};
+
+// Sums of the work-groups' partial sums: 16 lanes side by side take four
+// columns each, and 16 of them every sixteenth work-group.  blockIdx.y: the
+// weight's or the bias's.
+__global__ __launch_bounds__(kThreads) void norm_join_kernel(const NormJoinDesc D)
+{
+    typedef float f4 __attribute__((ext_vector_type(4)));
+    __shared__ f4 part[16][16];
+    const uint32_t c = threadIdx.x & 15, s = threadIdx.x >> 4, col = (blockIdx.x * 16 + c) * 4;
+    f4 sum = {0.f, 0.f, 0.f, 0.f};
+    if (col < D.width)
+        for (uint32_t g = s; g < D.groups; g += 16)
+            sum += *reinterpret_cast<const f4 *>(D.partial + (uint64_t(g) * 2 + blockIdx.y) * D.width + col);
+    part[s][c] = sum;
+    lds_barrier();
+    void *const to = blockIdx.y ? D.dbias : D.dweight;
+    if (s == 0 && to) {
+        for (int j = 1; j < 16; ++j)
+            sum += part[j][c];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (col + i < D.D)
+                store_number(to, col + i, D.weight_dtype, sum[i]);
+    }
+}
+
+// --------------------------------------------------------------- launches --
+
+// fn for a row of `vecs` vectors: f(lanes of a row, function).  Lanes and
+// vectors a lane so that a row is in registers at once: short rows share a
+// wave, up to 512 vectors a wave takes a row and needs no barrier.
+struct NormShape {
+    const void *fn;
+    int lanes;
+};
+
+template <typename E, int VW>
+NormShape norm_shape(int64_t vecs)
+{
+    const auto of = [](auto fn, int lanes) { return NormShape{reinterpret_cast<const void *>(fn), lanes}; };
+    if (vecs <= 16)
+        return of(norm_kernel<E, VW, 16, 1>, 16);
+    if constexpr (VW == 16) {
+        if (vecs <= 64)
+            return of(norm_kernel<E, VW, 64, 1>, 64);
+        if (vecs <= 128)
+            return of(norm_kernel<E, VW, 64, 2>, 64);
+        if (vecs <= 256)
+            return of(norm_kernel<E, VW, 64, 4>, 64);
+        if (vecs <= 512)
+            return of(norm_kernel<E, VW, 64, 8>, 64);
+        if (vecs <= 1024)
+            return of(norm_kernel<E, VW, 256, 4>, 256);
+        if (vecs <= 2048)
+            return of(norm_kernel<E, VW, 256, 8>, 256);
+    }
+    return of(norm_long_kernel<E>, 1024);
+}
+
+template <typename E, int VW>
+NormShape norm_grad_shape(int64_t vecs)
+{
+    const auto of = [](auto fn, int lanes) { return NormShape{reinterpret_cast<const void *>(fn), lanes}; };
+    if (vecs <= 16)
+        return of(norm_grad_kernel<E, VW, 16, 1>, 16);
+    if constexpr (VW == 16) {
+        if (vecs <= 64)
+            return of(norm_grad_kernel<E, VW, 64, 1>, 64);
+        if (vecs <= 128)
+            return of(norm_grad_kernel<E, VW, 64, 2>, 64);
+        if (vecs <= 256)
+            return of(norm_grad_kernel<E, VW, 64, 4>, 64);
+        if (vecs <= 512)
+            return of(norm_grad_kernel<E, VW, 256, 2>, 256);
+        if (vecs <= 1024)
+            return of(norm_grad_kernel<E, VW, 256, 4>, 256);
+        if (vecs <= kNormGradVecs)
+            return of(norm_grad_kernel<E, VW, 1024, 2>, 1024);
+    }
+    return of(norm_grad_long_kernel<E>, 1024);
+}
+
+template <typename E>
+const void *columns_fn()
+{
+    return reinterpret_cast<const void *>(norm_columns_kernel<E>);
+}
+
+basp_status launch_norm(const basp_norm_plan &p, const void *x, const void *weight, const void *bias, float eps, void *y,
+                        float *mean, float *rstd, void *stream)
+{
+    const int64_t row = p.D * p.es;
+    const NormShape s = BASP_BY_ROW(norm_shape, p.dtype, p.vw, p.vecs);
+    const int64_t teams = s.lanes < kThreads ? kThreads / s.lanes : 1, step = kLaunchGroups / (s.lanes > kThreads ? 4 : 1) * teams;
+    basp_status st = BASP_OK;
+    for (int64_t t0 = 0; t0 < p.T && st == BASP_OK; t0 += step) {
+        const int64_t n = std::min(step, p.T - t0);
+        const NormDesc D = {static_cast<const char *>(x) + t0 * row, weight, bias, static_cast<char *>(y) + t0 * row,
+                            mean ? mean + t0 : nullptr, rstd ? rstd + t0 : nullptr, uint32_t(n), uint32_t(row),
+                            uint32_t(p.vecs), uint32_t(p.D), eps, 1.f / float(p.D), p.weight_dtype};
+        st = launch_kernel(s.fn, dim3(uint32_t((n + teams - 1) / teams)), std::max(kThreads, s.lanes), D, stream, t0 == 0,
+                           t0 + n == p.T);
+    }
+    return st;
+}
+
+basp_status launch_norm_grad(const basp_norm_plan &p, const void *dy, const void *x, const void *weight, const float *mean,
+                             const float *rstd, void *dx, void *dweight, void *dbias, void *ws, void *stream)
+{
+    const int64_t row = p.D * p.es;
+    const NormShape s = BASP_BY_ROW(norm_grad_shape, p.dtype, p.vw, p.vecs);
+    NormGradDesc D = {static_cast<const char *>(dy), static_cast<const char *>(x), weight, mean, rstd, static_cast<char *>(dx),
+                      static_cast<float *>(ws), uint64_t(p.T), uint32_t(p.grad_groups), uint32_t(row), uint32_t(p.vecs),
+                      uint32_t(p.D), uint32_t(p.width), 1.f / float(p.D), p.weight_dtype};
+    basp_status st = BASP_OK;
+    if (p.T && (p.vecs <= kNormGradVecs || p.vw < 16)) {
+        st = launch_kernel(s.fn, dim3(D.groups), std::max(kThreads, s.lanes), D, stream, true, false);
+    } else if (p.T) {
+        const int64_t step = kLaunchGroups / 4;
+        for (int64_t t0 = 0; t0 < p.T && st == BASP_OK; t0 += step) {
+            NormGradDesc part = D;
+            part.dy += t0 * row;
+            part.x += t0 * row;
+            part.dx += t0 * row;
+            part.mean += t0;
+            part.rstd += t0;
+            st = launch_kernel(s.fn, dim3(uint32_t(std::min(step, p.T - t0))), s.lanes, part, stream, t0 == 0, false);
+        }
+        const void *fn = p.dtype == BASP_FP32 ? columns_fn<float>() : p.dtype == BASP_BF16 ? columns_fn<__bf16>() : columns_fn<_Float16>();
+        if (st == BASP_OK)
+            st = launch_kernel(fn, dim3(uint32_t((p.vecs + kThreads - 1) / kThreads), D.groups), kThreads, D, stream, false, false);
+    }
+    const NormJoinDesc J = {D.partial, dweight, dbias, D.groups, D.D, D.width, p.weight_dtype};
+    if (st == BASP_OK)
+        st = launch_kernel(reinterpret_cast<const void *>(norm_join_kernel), dim3(uint32_t((p.width + 63) / 64), dbias ? 2 : 1),
+                           kThreads, J, stream, p.T == 0, true);
+    return st;
+}
+
+}  // namespace
+}  // namespace basp
+
+using basp::CallBuf;
+
+extern "C" basp_status basp_layer_norm(const basp_norm_plan *p, const void *x, const void *weight, const void *bias,
+                                       float eps, void *y, float *mean, float *rstd, void *stream)
+{
+    return basp::timed_call([&]() -> basp_status {
+        if (!p || !(eps >= 0.f) || std::isinf(eps))
+            return BASP_ERR_INVALID;
+        const int64_t rows = p->T * p->D * p->es, cols = p->D * p->ws_es, stats = p->T * 4;
+        const CallBuf in[] = {{x, rows, p->es}, {weight, cols, p->ws_es}, {bias, bias ? cols : 0, p->ws_es}};
+        const CallBuf out[] = {{y, rows, p->es}, {mean, mean ? stats : 0, 4}, {rstd, rstd ? stats : 0, 4}};
+        const basp_status s = basp::check_call(in, 3, out, 3);
+        return s != BASP_OK ? s : basp::launch_norm(*p, x, weight, bias, eps, y, mean, rstd, stream);
+    });
+}
+
+extern "C" basp_status basp_layer_norm_grad(const basp_norm_plan *p, const void *dy, const void *x, const void *weight,
+                                            const float *mean, const float *rstd, void *dx, void *dweight, void *dbias,
+                                            void *ws, void *stream)
+{
+    return basp::timed_call([&]() -> basp_status {
+        if (!p)
+            return BASP_ERR_INVALID;
+        const int64_t rows = p->T * p->D * p->es, cols = p->D * p->ws_es, stats = p->T * 4;
+        const CallBuf in[] = {{dy, rows, p->es}, {x, rows, p->es}, {weight, cols, p->ws_es}, {mean, stats, 4}, {rstd, stats, 4}};
+        const CallBuf out[] = {{dx, rows, p->es}, {dweight, cols, p->ws_es}, {dbias, dbias ? cols : 0, p->ws_es},
+                               {ws, p->workspace_bytes, 16}};
+        const basp_status s = basp::check_call(in, 5, out, 4);
+        return s != BASP_OK ? s : basp::launch_norm_grad(*p, dy, x, weight, mean, rstd, dx, dweight, dbias, ws, stream);
+    });
+}

@@ -17,19 +17,10 @@
 
 #include <cstdint>
 
+#include "barrier.hpp"
 #include "index_plan.hpp"
 
 namespace basp {
-
-// A barrier for what the work-group has in LDS alone.  __syncthreads() also
-// waits until every store to memory has arrived, which takes microseconds and
-// which nobody here reads.
-__device__ inline void lds_barrier()
-{
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
 
 // LDS of one work-group: counters [waves][bins], the bins' totals, starts
 // (bins + 1) and a scratch word per wave.
