@@ -48,71 +48,92 @@ struct Running {
                 o[b][i] = 0.f;
     }
 
-    // Scores to weights, with m, l and o brought up to date.
-    template <int TILES>
-    __device__ inline void weigh(f32x16 (&s)[TILES], float scale_log2)
+    // Relative to a new maximum.
+    __device__ inline void rescale(float most, float scale_log2)
     {
-        float most = s[0][0];
+        const float now = fmaxf(m, most), factor = now == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - now) * scale_log2);
+        m = now;
+        l *= factor;
 #pragma unroll
-        for (int t = 0; t < TILES; ++t)
+        for (int b = 0; b < BLOCKS; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                most = fmaxf(most, s[t][i]);
-        most = fmaxf(most, other_half(most));
-        // rescaling is left out while no column's maximum grows
-        if (__ballot(most > m)) {
-            const float now = fmaxf(m, most), factor = now == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - now) * scale_log2);
-            m = now;
-            l *= factor;
-#pragma unroll
-            for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    o[b][i] *= factor;
-        }
-        const float base = m == -INFINITY ? 0.f : m * scale_log2;
-#pragma unroll
-        for (int t = 0; t < TILES; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], scale_log2, -base));
-                l += s[t][i];
-            }
+                o[b][i] *= factor;
     }
 };
 
-// One tile of ROWS keys from `first` on for a wave: scores, weights and sums.
-template <typename T, int C, int ROWS>
-__device__ inline void attend_tile(const AttendShape &A, const char *__restrict__ keys, const char *__restrict__ values,
-                                   const Vec8<T> (&q)[C / 16], Running<C / 32> &run, Seen seen, int first, int rows, int position)
+// A wave's way through tiles of ROWS keys: next() goes on to the next tile that
+// some of its columns see and says whether there is one, and tile() has it.  m is
+// left behind a column's maximum by up to 8 in the exponent of two, which keeps
+// weights below 2^8 (in range of fp16 too) and their relative precision: after
+// the first tile it hardly ever moves.  Where it does, the loop is left, the sums
+// are rescaled and the tile begun again (a branch in the loop would copy them in
+// every tile, see wild_rows).
+template <typename T, int C, int ROWS, typename Next, typename At>
+__device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C / 16], int position, Running<C / 32> &run, Next next,
+                                    At tile)
 {
-    typedef Tile<T, C, ROWS> Keys;
-    f32x16 s[ROWS / 32];
+    const int half = (threadIdx.x & 63) >> 5;
+    bool more = next();
+    while (more) {
+        f32x16 s[ROWS / 32];
+        float most;
+        bool behind;
+        for (;;) {
+            const auto at = tile();
 #pragma unroll
-    for (int t = 0; t < ROWS / 32; ++t) {
+            for (int t = 0; t < ROWS / 32; ++t)
+                s[t] = rows_times<T, C, ROWS>(at.keys, 32 * t, q);
+            if (at.part) {
+                const Sight sees(A, position, at.first + at.rows);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            s[t][i] = 0.f;
+                for (int t = 0; t < ROWS / 32; ++t)
 #pragma unroll
-        for (int c = 0; c < C / 16; ++c)
-            s[t] = product(Keys::along_channels(keys, 32 * t, c), q[c], s[t]);
-    }
-    if (seen == Seen::some || rows < ROWS) {
-        const int half = (threadIdx.x & 63) >> 5;
-#pragma unroll
-        for (int t = 0; t < ROWS / 32; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int row = 32 * t + row_of(i, half);
-                s[t][i] = row < rows && sees(A, position, first + row) ? s[t][i] : -INFINITY;
+                    for (int i = 0; i < 16; ++i)
+                        s[t][i] = sees(at.first + 32 * t + row_of(i, half)) ? s[t][i] : -INFINITY;
             }
-        run.weigh(s, A.scale_log2);
-        add_rows<T, C, ROWS, ROWS, true>(run.o, values, 0, s);
-    } else {
-        run.weigh(s, A.scale_log2);
-        add_rows<T, C, ROWS, ROWS, false>(run.o, values, 0, s);
+            most = s[0][0];
+#pragma unroll
+            for (int t = 0; t < ROWS / 32; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    most = fmaxf(most, s[t][i]);
+            most = fmaxf(most, other_half(most));
+            behind = __ballot(most > run.m + A.slack);
+            if (behind)
+                break;
+            const float base = run.m == -INFINITY ? 0.f : run.m * A.scale_log2;
+#pragma unroll
+            for (int t = 0; t < ROWS / 32; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], A.scale_log2, -base));
+                    run.l += s[t][i];
+                }
+            if (at.part && wild_rows<T, C, ROWS, ROWS>(at.values, 0))
+                break;
+            add_rows<T, C, ROWS, ROWS>(run.o, at.values, 0, s);
+            more = next();
+            if (!more)
+                return;
+        }
+        if (behind) {
+            run.rescale(most, A.scale_log2);
+        } else {
+            add_wild_rows<T, C, ROWS, ROWS>(run.o, tile().values, 0, s);
+            more = next();
+        }
     }
 }
+
+// A tile as a wave sees it: part of the keys hidden from part of its columns, or
+// not.
+struct TileView {
+    const char *__restrict__ keys;
+    const char *__restrict__ values;
+    int first, rows;
+    bool part;
+};
 
 // SHARE registers, from number `from` on, of the finished sums of 32 columns.
 template <typename T, int SHARE>
@@ -172,15 +193,23 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_tile_
     Running<C / 32> run;
     if (tiles.tiles)
         fetch(0, lds[0][0]);
-    for (int i = 0; i < tiles.tiles; ++i) {
-        wait_tiles();
-        lds_barrier();              // the tile is there, and the one before is no longer read
-        if (i + 1 < tiles.tiles)
-            fetch(i + 1, lds[~i & 1][0]);
-        const Seen seen = how_seen(A, wave_low, wave_high, tiles.first(i), tiles.rows(i));
-        if (seen != Seen::none)
-            attend_tile<T, C, KEYS>(A, lds[i & 1][0], lds[i & 1][1], q, run, seen, tiles.first(i), tiles.rows(i), col.position);
-    }
+    int i = -1;
+    Seen seen;
+    const auto next = [&]() {
+        for (++i; i < tiles.tiles; ++i) {
+            wait_tiles();
+            lds_barrier();          // the tile is there, and the one before is no longer read
+            if (i + 1 < tiles.tiles)
+                fetch(i + 1, lds[~i & 1][0]);
+            seen = how_seen(A, wave_low, wave_high, tiles.first(i), tiles.rows(i));
+            if (seen != Seen::none)
+                return true;
+        }
+        return false;
+    };
+    attend_tiles<T, C, KEYS>(A, q, col.position, run, next, [&]() {
+        return TileView{lds[i & 1][0], lds[i & 1][1], tiles.first(i), tiles.rows(i), seen == Seen::some || tiles.rows(i) < KEYS};
+    });
     if (!col.exists)
         return;
     const float l = run.l + other_half(run.l), inv = col.live ? 1.f / l : 0.f;
@@ -230,23 +259,29 @@ __global__ __launch_bounds__(kThreads, 1) void attend_step_kernel(const AttendDe
         Keys::template load<64, DIRECT>(to + Keys::kBytes, v + at, A.kv_token, tiles.rows(i), A.d);
     };
     Running<C / 32> run;
-    const int mine = int(split) * WAVES + int(wave), step = D.splits * WAVES;
-    int buffer = 0;
-    if (mine < tiles.tiles)
-        fetch(mine, lds[wave][0][0]);
-    for (int i = mine; i < tiles.tiles; i += step) {
+    const int step = D.splits * WAVES;
+    int i = int(split) * WAVES + int(wave) - step, buffer = BUFFERS - 1;
+    if (i + step < tiles.tiles)
+        fetch(i + step, lds[wave][0][0]);
+    const auto next = [&]() {
+        wave_order();
+        if (BUFFERS == 1 && i >= 0 && i + step < tiles.tiles)
+            fetch(i + step, lds[wave][0][0]);
+        i += step;
+        if (i >= tiles.tiles)
+            return false;
         wait_tiles();
         wave_order();
+        buffer = (buffer + 1) % BUFFERS;
         if (BUFFERS == 2 && i + step < tiles.tiles)
             fetch(i + step, lds[wave][(buffer + 1) % BUFFERS][0]);
-        const Seen seen = how_seen(A, low, high, tiles.first(i), tiles.rows(i));
-        attend_tile<T, C, KEYS>(A, lds[wave][buffer][0], lds[wave][buffer][1], q, run, seen, tiles.first(i), tiles.rows(i),
-                                col.position);
-        wave_order();
-        if (BUFFERS == 1 && i + step < tiles.tiles)
-            fetch(i + step, lds[wave][0][0]);
-        buffer = (buffer + 1) % BUFFERS;
-    }
+        return true;
+    };
+    attend_tiles<T, C, KEYS>(A, q, col.position, run, next, [&]() {
+        const int first = tiles.first(i), rows = tiles.rows(i);
+        return TileView{lds[wave][buffer][0], lds[wave][buffer][1], first, rows,
+                        rows < KEYS || how_seen(A, low, high, first, rows) != Seen::all};
+    });
 
     // the waves' sums relative to the largest of their maxima
     const int half = lane >> 5, c = lane & 31;

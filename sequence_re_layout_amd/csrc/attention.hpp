@@ -245,52 +245,70 @@ __device__ inline Vec8<T> row_part(const char *row, int c, int d)
         return __builtin_shufflevector(R::chunk(row, c, d), R::chunk(row, c + 4, d), 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// sums[b] += (32 channels of block b) x (N rows from row0 on of the tile),
-// weighted by p, which holds N / 32 results of 32 rows.  PART: some rows are hidden from some
-// columns, which then have the weight 0.  A product of 0 and an infinity or NaN
-// would be NaN, so a step with such numbers is added up without the zeros.
-template <typename T, int C, int ROWS, int N, bool PART, int BLOCKS>
-__device__ inline void add_rows(f32x16 (&sums)[BLOCKS], const char *tile, int row0, const f32x16 (&p)[N / 32])
+// The products of a wave's columns with 32 rows of a tile: C / 16 steps.
+template <typename T, int C, int ROWS>
+__device__ inline f32x16 rows_times(const char *tile, int row0, const Vec8<T> (&columns)[C / 16])
 {
     typedef Tile<T, C, ROWS> Rows;
+    f32x16 r = product(Rows::along_channels(tile, row0, 0), columns[0], f32x16{});
+#pragma unroll
+    for (int c = 1; c < C / 16; ++c)
+        r = product(Rows::along_channels(tile, row0, c), columns[c], r);
+    return r;
+}
+
+// sums[b] += (32 channels of block b) x (N rows from row0 on of the tile),
+// weighted by p, which holds N / 32 results of 32 rows.
+template <typename T, int C, int ROWS, int N, int BLOCKS>
+__device__ inline void add_rows(f32x16 (&sums)[BLOCKS], const char *tile, int row0, const f32x16 (&p)[N / 32])
+{
 #pragma unroll
     for (int s = 0; s < N / 16; ++s) {
         const Vec8<T> weights = operand<T>(p[s / 2], s % 2);
-        Vec8<T> a[BLOCKS];
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b)
-            a[b] = Rows::along_rows(tile, row0 + 16 * s, b);
-        if constexpr (PART) {
-            bool any = false;
+            sums[b] = product(Tile<T, C, ROWS>::along_rows(tile, row0 + 16 * s, b), weights, sums[b]);
+    }
+}
+
+// Where some rows are hidden from some columns, their weight is 0, and a product
+// of 0 and an infinity or NaN would be NaN.  So rows with such numbers
+// (wild_rows) are added up one by one and without the zeros.  The kernels leave
+// their loop for that and come back: a branch inside it would cost a copy of all
+// sums in every step.
+template <typename T, int C, int ROWS, int N>
+__device__ inline bool wild_rows(const char *tile, int row0)
+{
+    bool any = false;
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b)
-                any |= wild<T>(a[b]);
-            if (__ballot(any)) {
-                const int half = (threadIdx.x & 63) >> 5;
-                // a slot of either half at a time, its weight picked out of the operand
+    for (uint32_t i = 0; i < N * Tile<T, C, ROWS>::kRow / 1024; i += sizeof(T) / 2)
+        any |= wild<T>(*reinterpret_cast<const Vec8<T> *>(tile + row0 * Tile<T, C, ROWS>::kRow + i * 1024 +
+                                                          (threadIdx.x & 63) * 8 * sizeof(T)));
+    return __ballot(any);
+}
+
+template <typename T, int C, int ROWS, int N, int BLOCKS>
+__device__ inline void add_wild_rows(f32x16 (&sums)[BLOCKS], const char *tile, int row0, const f32x16 (&p)[N / 32])
+{
+    const int half = (threadIdx.x & 63) >> 5;
 #pragma clang loop unroll(disable)
-                for (int i = 0; i < 16; ++i) {
-                    float w = 0.f;
+    for (int r = 0; r < N; ++r) {
+        const int at = r / 32 * 16 + (r >> 3 & 3) * 4 + (r & 3), of = r >> 2 & 1;    // register, and half of the wave
+        float w = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        w = i % 8 == j ? static_cast<float>(weights[j]) : w;
-                    const float across = other_half(w);
-                    w = (i >> 3) == half ? w : across;
-                    const int row = row0 + 16 * s + row_of(i % 8, i >> 3);
-#pragma unroll
-                    for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const float x = Rows::at(tile, row, 32 * b + row_of(r, half));
-                            sums[b][r] = w != 0.f ? fmaf(w, x, sums[b][r]) : sums[b][r];
-                        }
-                }
-                continue;
-            }
-        }
+        for (int j = 0; j < N / 2; ++j)
+            w = at == j ? p[j / 16][j % 16] : w;
+        const float across = other_half(w);
+        w = of == half ? w : across;
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b)
-            sums[b] = product(a[b], weights, sums[b]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = Tile<T, C, ROWS>::at(tile, row0 + r, 32 * b + row_of(i, half));
+                sums[b][i] = w != 0.f ? fmaf(w, x, sums[b][i]) : sums[b][i];
+                if (i % 4 == 3)         // few of these in registers at a time
+                    __builtin_amdgcn_sched_barrier(0);
+            }
     }
 }
 
@@ -305,6 +323,7 @@ struct AttendShape {
     int64_t q_head, q_shard, kv_head, kv_shard;
     FastDiv by_ratio, by_heads, by_Bl, by_P;
     float scale, scale_log2;                    // log2(e) * scale: exponents are powers of two
+    float slack;                                // scores above the maximum that are not worth a rescaling
 };
 
 // The sequence of a shard, its length and the position of its first query.
@@ -328,10 +347,18 @@ __device__ inline Sequence sequence_of(const AttendShape &A, uint32_t shard)
     return s;
 }
 
-__device__ inline bool sees(const AttendShape &A, int position, int key)
-{
-    return key <= position && (position - key < A.reach || key < A.firsts);
-}
+// The keys that a position sees are those up to `last` which come after
+// `before` or are among the first ones.
+struct Sight {
+    int last, before, firsts;
+
+    // Of the keys below `end`.
+    __device__ inline Sight(const AttendShape &A, int position, int end)
+        : last(position < end ? position : end - 1), before(position - A.reach), firsts(A.firsts)
+    {
+    }
+    __device__ inline bool operator()(int key) const { return (key <= last) & ((key > before) | (key < firsts)); }
+};
 
 // Tiles of keys that positions [low, high] see, KEYS each: first those of the
 // sinks before the window, then those of the window.

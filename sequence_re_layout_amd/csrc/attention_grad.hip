@@ -27,6 +27,8 @@ namespace basp {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFewTiles = 3;        // tiles of keys up to which <dO, O> is summed again from P and dP
 
 struct AttendGradDesc {
     AttendShape shape;
@@ -44,7 +46,7 @@ struct AttendGradDesc {
 template <typename T, int C, bool DIRECT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_kernel(const AttendGradDesc D)
 {
-    constexpr int KEYS = sizeof(T) == 2 ? 64 : 32;
+    constexpr int KEYS = sizeof(T) == 2 ? 64 : 32, PARTS = KEYS / 32;
     typedef Tile<T, C, KEYS> Keys;
     __shared__ __attribute__((aligned(16))) char lds[2][2][Keys::kBytes];
     const AttendShape &A = D.shape;
@@ -58,23 +60,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
     Vec8<T> q[C / 16], g[C / 16];
     load_column<T, C>(A, D.q + col.at(A, shard), col.live, q);
     load_column<T, C>(A, D.dout + col.at(A, shard), col.live, g);
-    float delta = 0.f, lse = 0.f;
-    if (col.live) {
-        const char *const o = D.o + col.at(A, shard);
-#pragma unroll
-        for (int c = 0; c < C / 16; ++c) {
-            const Vec8<T> x = row_part<T>(o, 16 * c + 8 * half, A.d);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                delta = fmaf(static_cast<float>(x[i]), static_cast<float>(g[c][i]), delta);
-        }
-        lse = D.lse[col.row(A, shard)] * 1.4426950408889634f;
-    }
-    delta += other_half(delta);
-    if (col.live && half == 0) {
-        D.rows[col.row(A, shard)] = lse;
-        D.rows[D.lse_elems + col.row(A, shard)] = delta;
-    }
+    const float lse = col.live ? D.lse[col.row(A, shard)] * kLog2e : 0.f;
 
     const uint32_t last = (first + kTileColumns < uint32_t(A.total) ? first + kTileColumns : uint32_t(A.total)) - 1;
     int low = seq.start + int(fastdiv(first, A.by_ratio)), high = seq.start + int(fastdiv(last, A.by_ratio));
@@ -90,6 +76,76 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
         Keys::template load<kThreads, DIRECT>(to, k + at, A.kv_token, tiles.rows(i), A.d);
         Keys::template load<kThreads, DIRECT>(to + Keys::kBytes, v + at, A.kv_token, tiles.rows(i), A.d);
     };
+    // on to the next 32 keys that some column of the wave sees
+    int u = -1;
+    Seen seen;
+    const auto next = [&]() {
+        for (++u; u < tiles.tiles * PARTS; ++u) {
+            const int j = u / PARTS, t = u % PARTS, rows = tiles.rows(j) - 32 * t;
+            if (t == 0) {
+                wait_tiles();
+                lds_barrier();
+                if (j + 1 < tiles.tiles)
+                    fetch(j + 1, lds[~j & 1][0]);
+            }
+            seen = rows > 0 ? how_seen(A, wave_low, wave_high, tiles.first(j) + 32 * t, rows < 32 ? rows : 32) : Seen::none;
+            if (seen != Seen::none)
+                return true;
+        }
+        return false;
+    };
+    // P and dP of these keys; P is 0 where a key is hidden
+    const auto weigh = [&](f32x16 &p, f32x16 &dp) {
+        const int j = u / PARTS, t = u % PARTS, from = tiles.first(j) + 32 * t, rows = tiles.rows(j) - 32 * t;
+        p = rows_times<T, C, KEYS>(lds[j & 1][0], 32 * t, q);
+        dp = rows_times<T, C, KEYS>(lds[j & 1][1], 32 * t, g);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], A.scale_log2, -lse));
+        const bool part = seen == Seen::some || rows < 32;
+        if (part) {
+            const Sight sees(A, col.position, from + rows);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const bool is = sees(from + row_of(i, half));
+                p[i] = is ? p[i] : 0.f;
+                dp[i] = is ? dp[i] : 0.f;
+            }
+        }
+        return part;
+    };
+
+    // delta = <dO, O> = sum P dP.  O has been rounded to its type, which shows
+    // where a row sees few keys: there delta is summed first, in fp32.
+    float delta = 0.f;
+    if (tiles.tiles <= kFewTiles) {
+        if (tiles.tiles)
+            fetch(0, lds[0][0]);
+        while (next()) {
+            f32x16 p, dp;
+            weigh(p, dp);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                delta = fmaf(p[i], dp[i], delta);
+        }
+        u = -1;
+        lds_barrier();
+    } else if (col.live) {
+        const char *const o = D.o + col.at(A, shard);
+#pragma unroll
+        for (int c = 0; c < C / 16; ++c) {
+            const Vec8<T> x = row_part<T>(o, 16 * c + 8 * half, A.d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                delta = fmaf(static_cast<float>(x[i]), static_cast<float>(g[c][i]), delta);
+        }
+    }
+    delta += other_half(delta);
+    if (col.live && half == 0) {
+        D.rows[col.row(A, shard)] = lse;
+        D.rows[D.lse_elems + col.row(A, shard)] = delta;
+    }
+
     f32x16 sums[C / 32];
 #pragma unroll
     for (int b = 0; b < C / 32; ++b)
@@ -98,42 +154,26 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
             sums[b][i] = 0.f;
     if (tiles.tiles)
         fetch(0, lds[0][0]);
-    for (int j = 0; j < tiles.tiles; ++j) {
-        wait_tiles();
-        lds_barrier();
-        if (j + 1 < tiles.tiles)
-            fetch(j + 1, lds[~j & 1][0]);
-        const char *const keys = lds[j & 1][0], *const values = lds[j & 1][1];
-#pragma unroll 1
-        for (int t = 0; t < KEYS / 32; ++t) {
-            const int first_key = tiles.first(j) + 32 * t, rows = tiles.rows(j) - 32 * t;
-            if (rows <= 0)
+    bool more = next();
+    while (more) {
+        f32x16 ds[1];
+        for (;;) {
+            f32x16 dp;
+            const bool part = weigh(ds[0], dp);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                ds[0][i] *= dp[i] - delta;
+            const char *const keys = lds[u / PARTS & 1][0];
+            if (part && wild_rows<T, C, KEYS, 32>(keys, u % PARTS * 32))
                 break;
-            const Seen seen = how_seen(A, wave_low, wave_high, first_key, rows < 32 ? rows : 32);
-            if (seen == Seen::none)
-                continue;
-            f32x16 s[1], dp;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[0][i] = dp[i] = 0.f;
-#pragma unroll
-            for (int c = 0; c < C / 16; ++c) {
-                s[0] = product(Keys::along_channels(keys, 32 * t, c), q[c], s[0]);
-                dp = product(Keys::along_channels(values, 32 * t, c), g[c], dp);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[0][i] = __builtin_amdgcn_exp2f(fmaf(s[0][i], A.scale_log2, -lse)) * (dp[i] - delta);
-            if (seen == Seen::some || rows < 32) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int row = row_of(i, half);
-                    s[0][i] = row < rows && sees(A, col.position, first_key + row) ? s[0][i] : 0.f;
-                }
-                add_rows<T, C, KEYS, 32, true>(sums, keys, 32 * t, s);
-            } else {
-                add_rows<T, C, KEYS, 32, false>(sums, keys, 32 * t, s);
-            }
+            add_rows<T, C, KEYS, 32>(sums, keys, u % PARTS * 32, ds);
+            more = next();
+            if (!more)
+                break;
+        }
+        if (more) {
+            add_wild_rows<T, C, KEYS, 32>(sums, lds[u / PARTS & 1][0], u % PARTS * 32, ds);
+            more = next();
         }
     }
     if (!col.exists)
@@ -175,7 +215,7 @@ __device__ inline void store_key(const AttendShape &A, char *to, uint32_t shard,
 template <typename T, int C, bool DIRECT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && C <= 64 ? 2 : 1) void attend_dkv_kernel(const AttendGradDesc D)
 {
-    constexpr int ROWS = sizeof(T) == 2 ? 64 : 32;
+    constexpr int ROWS = sizeof(T) == 2 ? 64 : 32, PARTS = ROWS / 32;
     typedef Tile<T, C, ROWS> Rows;
     __shared__ __attribute__((aligned(16))) char lds[2][2][Rows::kBytes];
     __shared__ __attribute__((aligned(16))) float lds_rows[2][2][64];
@@ -226,54 +266,66 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && C <= 64 ? 2 : 1) void a
     };
     if (all)
         fetch(0, 0, 0);
-    int tile = 0, head = 0;
-    for (int j = 0; j < all; ++j) {
-        wait_tiles();
-        lds_barrier();
-        const int from = begin + tile * ROWS;
-        tile = tile + 1 < tiles ? tile + 1 : 0;
-        head += tile == 0;
-        if (j + 1 < all)
-            fetch(head, tile, ~j & 1);
-        const char *const queries = lds[j & 1][0], *const grads = lds[j & 1][1];
-#pragma unroll 1
-        for (int t = 0; t < ROWS / 32; ++t) {
-            const int at = from + 32 * t, rows = end - at < 32 ? end - at : 32;
-            if (rows <= 0)
-                break;
-            const int low = seq.start + at, high = low + rows - 1;
-            const Seen seen = how_seen(A, low, high, wave_key, 32);
-            if (seen == Seen::none)
-                continue;
-            f32x16 p[1], ds[1];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                p[0][i] = ds[0][i] = 0.f;
-#pragma unroll
-            for (int c = 0; c < C / 16; ++c) {
-                p[0] = product(Rows::along_channels(queries, 32 * t, c), k[c], p[0]);
-                ds[0] = product(Rows::along_channels(grads, 32 * t, c), v[c], ds[0]);
+    // on to the next 32 queries that see some key of the wave
+    int u = -1, at = 0, tile = 0, head = 0;
+    Seen seen;
+    const auto next = [&]() {
+        for (++u; u < all * PARTS; ++u) {
+            const int j = u / PARTS, t = u % PARTS;
+            if (t == 0) {
+                wait_tiles();
+                lds_barrier();
+                at = begin + tile * ROWS;
+                tile = tile + 1 < tiles ? tile + 1 : 0;
+                head += tile == 0;
+                if (j + 1 < all)
+                    fetch(head, tile, ~j & 1);
+            } else {
+                at += 32;
             }
+            const int low = seq.start + at, high = seq.start + (at + 32 < end ? at + 32 : end) - 1;
+            seen = how_seen(A, low, high, wave_key, 32);
+            if (seen != Seen::none)
+                return true;
+        }
+        return false;
+    };
+    bool more = next();
+    while (more) {
+        f32x16 p[1], ds[1];
+        for (;;) {
+            const int buffer = u / PARTS & 1, row0 = u % PARTS * 32, rows = end - at;
+            const char *const queries = lds[buffer][0], *const grads = lds[buffer][1];
+            p[0] = rows_times<T, C, ROWS>(queries, row0, k);
+            ds[0] = rows_times<T, C, ROWS>(grads, row0, v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int row = 32 * t + row_of(i, half);
-                p[0][i] = __builtin_amdgcn_exp2f(fmaf(p[0][i], A.scale_log2, -lds_rows[j & 1][0][row]));
-                ds[0][i] = p[0][i] * (ds[0][i] - lds_rows[j & 1][1][row]);
+                const int row = row0 + row_of(i, half);
+                p[0][i] = __builtin_amdgcn_exp2f(fmaf(p[0][i], A.scale_log2, -lds_rows[buffer][0][row]));
+                ds[0][i] = p[0][i] * (ds[0][i] - lds_rows[buffer][1][row]);
             }
-            if (seen == Seen::some || rows < 32) {
+            const bool part = seen == Seen::some || rows < 32;
+            if (part) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int row = row_of(i, half);
-                    const bool is = row < rows && sees(A, low + row, key);
+                    const bool is = (row < rows) & Sight(A, seq.start + at + row, A.S)(key);
                     p[0][i] = is ? p[0][i] : 0.f;
                     ds[0][i] = is ? ds[0][i] : 0.f;
                 }
-                add_rows<T, C, ROWS, 32, true>(dv, grads, 32 * t, p);
-                add_rows<T, C, ROWS, 32, true>(dk, queries, 32 * t, ds);
-            } else {
-                add_rows<T, C, ROWS, 32, false>(dv, grads, 32 * t, p);
-                add_rows<T, C, ROWS, 32, false>(dk, queries, 32 * t, ds);
+                if (wild_rows<T, C, ROWS, 32>(queries, row0) || wild_rows<T, C, ROWS, 32>(grads, row0))
+                    break;
             }
+            add_rows<T, C, ROWS, 32>(dv, grads, row0, p);
+            add_rows<T, C, ROWS, 32>(dk, queries, row0, ds);
+            more = next();
+            if (!more)
+                break;
+        }
+        if (more) {
+            add_wild_rows<T, C, ROWS, 32>(dv, lds[u / PARTS & 1][1], u % PARTS * 32, p);
+            add_wild_rows<T, C, ROWS, 32>(dk, lds[u / PARTS & 1][0], u % PARTS * 32, ds);
+            more = next();
         }
     }
     if ((sinks ? D.sink_chunks : D.chunks) == 1) {

@@ -36,6 +36,7 @@ inline AttendShape attend_shape(const basp_attention_plan &p, const int32_t *sta
     A.by_P = make_fastdiv(uint32_t(p.P));
     A.scale = scale;
     A.scale_log2 = float(double(scale) * 1.4426950408889634);
+    A.slack = float(8.0 / (double(scale) * 1.4426950408889634));
     return A;
 }
 
