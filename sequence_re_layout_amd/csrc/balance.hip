@@ -36,6 +36,7 @@ struct BalanceDesc {
     int64_t T, per_group;           // tokens, and of a work-group
     uint32_t row, vecs;
     int32_t K, E, wide_ids;
+    FastDiv by_K;
 };
 
 // Scores of one token in a team's registers, -inf where a lane has no column
@@ -58,6 +59,15 @@ struct Scores {
         }
     }
 
+    __device__ inline void clear()
+    {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                f[r][i] = 0.f;
+    }
+
     __device__ inline void softmax()
     {
         float most = -INFINITY;
@@ -72,7 +82,7 @@ struct Scores {
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                f[r][i] = expf(f[r][i] - most);
+                f[r][i] = __builtin_amdgcn_exp2f((f[r][i] - most) * 1.4426950408889634f);
                 total[0] += f[r][i];
             }
         team_sum<LANES, 1>(total, nullptr);
@@ -95,11 +105,6 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const BalanceD
     for (int e = threadIdx.x; e <= D.E; e += kBalanceThreads)
         hist[e] = 0;
     lds_barrier();
-    for (int64_t s = begin * D.K + threadIdx.x; s < end * D.K; s += kBalanceThreads) {
-        const int64_t id = D.wide_ids ? static_cast<const int64_t *>(D.ids)[s] : static_cast<const int32_t *>(D.ids)[s];
-        if (id >= 0 && id < D.E && (!D.mask || D.mask[s / D.K]))
-            atomicAdd(&hist[id], 1);
-    }
     const uint32_t lane = threadIdx.x % LANES;
     float acc[R][N];
 #pragma unroll
@@ -108,21 +113,39 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const BalanceD
         for (int i = 0; i < N; ++i)
             acc[r][i] = 0.f;
     int live = 0;
-    for (int64_t t = begin + threadIdx.x / LANES; t < end; t += TEAMS) {
-        if (D.mask && !D.mask[t])
-            continue;
-        ++live;
-        Scores<E, VW, LANES, R> s;
-        s.load(D.logits + t * D.row, lane, D.row, D.vecs);
-        s.softmax();
+    // four tokens at a time: the sums over lanes of one are as long a chain as a
+    // load from memory
+    constexpr int U = 4;
+    for (int64_t t = begin + threadIdx.x / LANES; t < end; t += TEAMS * U) {
+        Scores<E, VW, LANES, R> s[U];
+        bool is[U];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int u = 0; u < U; ++u) {
+            const int64_t at = t + u * TEAMS;
+            if (at < end)               // a masked token's scores are loaded too, and then ignored
+                s[u].load(D.logits + at * D.row, lane, D.row, D.vecs);
+            else
+                s[u].clear();
+            is[u] = at < end && (!D.mask || D.mask[at]);
+        }
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                acc[r][i] += s.f[r][i];
+        for (int u = 0; u < U; ++u) {
+            s[u].softmax();
+            live += is[u];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    acc[r][i] += is[u] ? s[u].f[r][i] : 0.f;
+        }
     }
     if (lane == 0 && live)
         atomicAdd(&hist[D.E], live);
+    for (int64_t s = begin * D.K + threadIdx.x; s < end * D.K; s += kBalanceThreads) {
+        const int64_t id = D.wide_ids ? static_cast<const int64_t *>(D.ids)[s] : static_cast<const int32_t *>(D.ids)[s];
+        if (id >= 0 && id < D.E && (!D.mask || D.mask[begin + fastdiv(uint32_t(s - begin * D.K), D.by_K)]))
+            atomicAdd(&hist[id], 1);
+    }
     // the teams' sums: those of a wave first, then the waves in their order
     const uint32_t wave = threadIdx.x >> 6, in_wave = threadIdx.x & 63;
 #pragma unroll
@@ -177,6 +200,7 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_join_kernel(const Bal
     float P = 0.f;
     int n = 0;
     if (e < D.E)
+#pragma unroll 8
         for (int g = s; g < D.groups; g += slices) {
             P += D.sums[int64_t(g) * D.E + e];
             n += D.group_counts[int64_t(g) * (D.E + 1) + e];
@@ -230,27 +254,27 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const Balanc
     if (t >= D.tokens)
         return;
     char *const out = D.dlogits + uint64_t(t) * D.row;
-    const bool live = !D.mask || D.mask[t];
-    Scores<E, VW, LANES, R> s;
+    Scores<E, VW, LANES, R> s;      // all loads first; a masked token's scores are then ignored
     float slope[R][N], dot[1] = {0.f};
-    if (live) {
-        s.load(D.logits + uint64_t(t) * D.row, lane, D.row, D.vecs);
-        s.softmax();
+    s.load(D.logits + uint64_t(t) * D.row, lane, D.row, D.vecs);
+    const bool live = !D.mask || D.mask[t];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const uint32_t a = lane + r * LANES;
+    for (int r = 0; r < R; ++r) {
+        const uint32_t a = lane + r * LANES;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                slope[r][i] = 0.f;
-            if (a < D.vecs)
-                load_values<float, N>(reinterpret_cast<const char *>(D.slope) + vec_offset<VW>(a, D.row) / sizeof(E) * 4, slope[r]);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                dot[0] += s.f[r][i] * slope[r][i];
-        }
-        team_sum<LANES, 1>(dot, nullptr);
+        for (int i = 0; i < N; ++i)
+            slope[r][i] = 0.f;
+        if (a < D.vecs)
+            load_values<float, N>(reinterpret_cast<const char *>(D.slope) + vec_offset<VW>(a, D.row) / sizeof(E) * 4, slope[r]);
     }
     const float g = *D.dloss;
+    s.softmax();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            dot[0] += s.f[r][i] * slope[r][i];
+    team_sum<LANES, 1>(dot, nullptr);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const uint32_t a = lane + r * LANES, off = vec_offset<VW>(a, D.row), seen = (a * VW - off) / sizeof(E);
@@ -328,7 +352,7 @@ basp_status launch_balance(const basp_expert_plan &p, const void *logits, const 
     int32_t *const group_counts = reinterpret_cast<int32_t *>(sums + int64_t{groups} * p.E);
     const BalanceDesc D = {static_cast<const char *>(logits), ids, mask, sums, group_counts, p.T,
                            groups ? (p.T + groups - 1) / groups : 0, uint32_t(r.row), uint32_t(r.vecs), p.K, p.E,
-                           p.id_bytes == 8};
+                           p.id_bytes == 8, make_fastdiv(uint32_t(p.K))};
     basp_status s = BASP_OK;
     if (groups)
         s = launch_kernel(shape.sum, dim3(groups), kBalanceThreads, D, stream, true, false);

@@ -41,8 +41,8 @@ extern "C" basp_norm_plan *basp_norm_plan_create(int64_t T, int64_t D, basp_dtyp
     p->ws_es = wes;
     p->vw = basp::row_vector(D, es);
     p->vecs = (D * es + p->vw - 1) / p->vw;
-    // rows of a work-group in one go: one, or more of short rows
-    const int64_t at_once = p->vecs <= 16 ? 16 : p->vecs <= 256 ? 4 : 1;
+    // rows of a work-group in one go: a share of its threads for each
+    const int64_t at_once = p->vecs <= 16 ? 16 : p->vecs <= 128 ? 4 : p->vecs <= 256 ? 2 : 1;
     p->grad_groups = int32_t(std::min<int64_t>(basp::kNormGradGroups, (T + at_once - 1) / at_once));
     p->width = (D + 3) / 4 * 4;
     p->workspace_bytes = int64_t{8} * p->grad_groups * p->width;

@@ -32,15 +32,15 @@ constexpr int kNormGradGroups = 512;
 // again by columns.
 constexpr int64_t kNormGradVecs = 2048;
 
-// The balance loss: tokens are summed in up to kBalanceGroups work-groups of
-// kBalanceThreads, one partial sum and one count of every expert each; one more
-// work-group joins them.
-constexpr int kBalanceGroups = 128, kBalanceThreads = 1024;
+// The balance loss: tokens are summed in up to 256 work-groups of
+// kBalanceThreads, one partial sum and one count of every expert each, and one
+// more work-group joins them, which reads about 130 GB/s: at most 2^17 of each.
+constexpr int kBalanceThreads = 1024;
 
 inline int balance_groups(const basp_expert_plan &p)
 {
-    const int64_t most = (p.T + 15) / 16;       // at least 16 tokens each
-    return int(most < 1 ? 1 : most > kBalanceGroups ? kBalanceGroups : most);
+    const int64_t wanted = (p.T + 15) / 16, most = p.E <= 512 ? 256 : (int64_t{1} << 17) / p.E;
+    return int(wanted < 1 ? 1 : wanted > most ? most : wanted);
 }
 
 }  // namespace basp

@@ -44,79 +44,97 @@ __device__ inline uint32_t shared_front(uint32_t a, uint32_t off)
 }
 
 template <typename E, int VW>
-__device__ inline void norm_vector(const NormDesc &D, typename MemVec<VW>::type x, uint32_t off, float mean, float rstd,
-                                   char *y)
+__device__ inline void norm_vector(typename MemVec<VW>::type x, float mean, float rstd, const float (&w)[VW / sizeof(E)],
+                                   const float (&b)[VW / sizeof(E)], char *y)
 {
     constexpr int N = VW / sizeof(E);
-    float f[N], w[N], o[N];
+    float f[N];
     unpack<E, VW>(x, f);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        f[i] = fmaf((f[i] - mean) * rstd, w[i], b[i]);
+    store_vec<VW>(y, pack<E, VW>(f));
+}
+
+// The weight and the bias of a vector's channels.
+template <typename E, int VW>
+__device__ inline void load_weights(const NormDesc &D, uint32_t off, float (&w)[VW / sizeof(E)], float (&b)[VW / sizeof(E)])
+{
+    constexpr int N = VW / sizeof(E);
     load_any<N>(D.weight, off / sizeof(E), D.weight_dtype, w);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        o[i] = (f[i] - mean) * rstd * w[i];
-    if (D.bias) {
-        load_any<N>(D.bias, off / sizeof(E), D.weight_dtype, w);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            o[i] += w[i];
-    }
-    store_vec<VW>(y + off, pack<E, VW>(o));
+        b[i] = 0.f;
+    if (D.bias)
+        load_any<N>(D.bias, off / sizeof(E), D.weight_dtype, b);
 }
 
-// LANES lanes take a row, R vectors each.
+// LANES lanes take a row, R vectors each, and keep the weights of their channels
+// in registers over the rows that they take in turn; the next row is on its way
+// while one is normed.
 template <typename E, int VW, int LANES, int R>
-__global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void norm_kernel(const NormDesc D)
+__global__ __launch_bounds__(kThreads) void norm_kernel(const NormDesc D)
 {
-    constexpr int N = VW / sizeof(E), TEAMS = LANES > kThreads ? 1 : kThreads / LANES;
+    constexpr int N = VW / sizeof(E), TEAMS = kThreads / LANES;
     __shared__ float lds[2][LANES > 64 ? LANES / 64 : 1];
-    const uint32_t lane = threadIdx.x % LANES, t = blockIdx.x * TEAMS + threadIdx.x / LANES;
-    const bool live = t < D.rows;
-    const char *x = D.x + uint64_t(live ? t : 0) * D.row;
+    const uint32_t lane = threadIdx.x % LANES, team = threadIdx.x / LANES, step = gridDim.x * TEAMS;
+    uint32_t off[R], seen[R];
+    float w[R][N], b[R][N];
     typename MemVec<VW>::type v[R];
-    float sum[1] = {0.f}, sq[1] = {0.f};
+    const auto fetch = [&](uint32_t t) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (t < D.rows && lane + r * LANES < D.vecs)
+                v[r] = load_vec<VW, true>(D.x + uint64_t(t) * D.row + off[r]);
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        off[r] = vec_offset<VW>(lane + r * LANES, D.row);
+        seen[r] = lane + r * LANES < D.vecs ? shared_front<E, VW>(lane + r * LANES, off[r]) : N;
+    }
+    fetch(blockIdx.x * TEAMS + team);
 #pragma unroll
     for (int r = 0; r < R; ++r)
         if (lane + r * LANES < D.vecs)
-            v[r] = load_vec<VW, false>(x + vec_offset<VW>(lane + r * LANES, D.row));
+            load_weights<E, VW>(D, off[r], w[r], b[r]);
+    for (uint32_t first = blockIdx.x * TEAMS; first < D.rows; first += step) {
+        const uint32_t t = first + team;
+        typename MemVec<VW>::type x[R];
+        float sum[1] = {0.f}, sq[1] = {0.f};
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const uint32_t a = lane + r * LANES;
-        if (a < D.vecs) {
-            const uint32_t seen = shared_front<E, VW>(a, vec_offset<VW>(a, D.row));
+        for (int r = 0; r < R; ++r) {
+            x[r] = v[r];
             float f[N];
-            unpack<E, VW>(v[r], f);
+            unpack<E, VW>(x[r], f);
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                sum[0] += uint32_t(i) < seen ? 0.f : f[i];
+                sum[0] += uint32_t(i) < seen[r] ? 0.f : f[i];
         }
-    }
-    team_sum<LANES, 1>(sum, lds[0]);
-    const float mean = sum[0] * D.inv_D;
+        fetch(t + step);
+        team_sum<LANES, 1>(sum, lds[0]);
+        const float mean = sum[0] * D.inv_D;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const uint32_t a = lane + r * LANES;
-        if (a < D.vecs) {
-            const uint32_t seen = shared_front<E, VW>(a, vec_offset<VW>(a, D.row));
+        for (int r = 0; r < R; ++r) {
             float f[N];
-            unpack<E, VW>(v[r], f);
+            unpack<E, VW>(x[r], f);
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                sq[0] += uint32_t(i) < seen ? 0.f : (f[i] - mean) * (f[i] - mean);
+                sq[0] += uint32_t(i) < seen[r] ? 0.f : (f[i] - mean) * (f[i] - mean);
         }
-    }
-    team_sum<LANES, 1>(sq, lds[1]);
-    const float rstd = 1.f / sqrtf(sq[0] * D.inv_D + D.eps);
-    if (!live)
-        return;
+        team_sum<LANES, 1>(sq, lds[1]);
+        const float rstd = 1.f / sqrtf(sq[0] * D.inv_D + D.eps);
+        if (t >= D.rows)
+            continue;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (lane + r * LANES < D.vecs)
-            norm_vector<E, VW>(D, v[r], vec_offset<VW>(lane + r * LANES, D.row), mean, rstd, D.y + uint64_t(t) * D.row);
-    if (lane == 0) {
-        if (D.mean)
-            D.mean[t] = mean;
-        if (D.rstd)
-            D.rstd[t] = rstd;
+        for (int r = 0; r < R; ++r)
+            if (lane + r * LANES < D.vecs)
+                norm_vector<E, VW>(x[r], mean, rstd, w[r], b[r], D.y + uint64_t(t) * D.row + off[r]);
+        if (lane == 0) {
+            if (D.mean)
+                D.mean[t] = mean;
+            if (D.rstd)
+                D.rstd[t] = rstd;
+        }
     }
 }
 
@@ -152,7 +170,9 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormDesc D)
     const float mean = sum[0] * D.inv_D, rstd = 1.f / sqrtf(sq[0] * D.inv_D + D.eps);
     for (uint32_t a = threadIdx.x; a < D.vecs; a += LANES) {
         const uint32_t off = vec_offset<16>(a, D.row);
-        norm_vector<E, 16>(D, load_vec<16, false>(x + off), off, mean, rstd, D.y + uint64_t(t) * D.row);
+        float w[N], b[N];
+        load_weights<E, 16>(D, off, w, b);
+        norm_vector<E, 16>(load_vec<16, false>(x + off), mean, rstd, w, b, D.y + uint64_t(t) * D.row + off);
     }
     if (threadIdx.x == 0) {
         if (D.mean)
@@ -189,98 +209,116 @@ __device__ inline void store_columns(float *to, uint32_t a, uint32_t off, const 
 }
 
 // LANES lanes take a row, R vectors each; a work-group's teams take rows in
-// turn and keep the sums over them in registers.
-template <typename E, int VW, int LANES, int R>
-__global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void norm_grad_kernel(const NormGradDesc D)
+// turn and keep the sums over them in registers; the next rows are on their way
+// while some are summed.
+template <typename E, int VW, int LANES, int R, int THREADS>
+__global__ __launch_bounds__(THREADS, 2) void norm_grad_kernel(const NormGradDesc D)
 {
-    constexpr int N = VW / sizeof(E), TEAMS = LANES > kThreads ? 1 : kThreads / LANES;
-    __shared__ float lds[2][LANES > 64 ? LANES / 64 * 2 : 1];
-    __shared__ float joined[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? LANES * N * 2 : 1];
+    constexpr int N = VW / sizeof(E), TEAMS = THREADS / LANES, COLUMNS = LANES * N;
+    constexpr bool AHEAD = R <= 2;              // more would not fit in registers
+    __shared__ float lds[2][LANES > 64 ? THREADS / 64 * 2 : 1];
+    __shared__ float joined[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? COLUMNS * 2 : 1];
     const uint32_t lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
+    uint32_t off[R], seen[R];
     float w[R][N], dw[R][N], db[R][N];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const uint32_t a = lane + r * LANES;
+        off[r] = vec_offset<VW>(a, D.row);
+        seen[r] = a < D.vecs ? shared_front<E, VW>(a, off[r]) : N;
 #pragma unroll
         for (int i = 0; i < N; ++i)
             w[r][i] = dw[r][i] = db[r][i] = 0.f;
         if (a < D.vecs)
-            load_any<N>(D.weight, vec_offset<VW>(a, D.row) / sizeof(E), D.weight_dtype, w[r]);
+            load_any<N>(D.weight, off[r] / sizeof(E), D.weight_dtype, w[r]);
     }
+    typename MemVec<VW>::type xv[R] = {}, gv[R] = {}, next_x[R] = {}, next_g[R] = {};
+    float next_mean = 0.f, next_rstd = 0.f;
+    const auto fetch = [&](uint64_t t) {
+        if (t >= D.rows)
+            return;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (lane + r * LANES < D.vecs) {
+                next_g[r] = load_vec<VW, true>(D.dy + t * D.row + off[r]);
+                next_x[r] = load_vec<VW, true>(D.x + t * D.row + off[r]);
+            }
+        next_mean = D.mean[t];
+        next_rstd = D.rstd[t];
+    };
+    const uint64_t step = uint64_t(D.groups) * TEAMS;
+    if constexpr (AHEAD)
+        fetch(uint64_t(blockIdx.x) * TEAMS + team);
     int turn = 0;
-    for (uint64_t first = uint64_t(blockIdx.x) * TEAMS; first < D.rows; first += uint64_t(D.groups) * TEAMS, turn ^= 1) {
+    for (uint64_t first = uint64_t(blockIdx.x) * TEAMS; first < D.rows; first += step, turn ^= 1) {
         const uint64_t t = first + team;
         const bool live = t < D.rows;
-        const uint64_t at = live ? t * D.row : 0;
-        typename MemVec<VW>::type xv[R], gv[R];
+        const uint64_t at = t * D.row;
+        if constexpr (!AHEAD)
+            fetch(t);
+        const float mean = next_mean, rstd = live ? next_rstd : 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint32_t a = lane + r * LANES;
-            if (live && a < D.vecs) {
-                gv[r] = load_vec<VW, false>(D.dy + at + vec_offset<VW>(a, D.row));
-                xv[r] = load_vec<VW, false>(D.x + at + vec_offset<VW>(a, D.row));
-            }
+            xv[r] = next_x[r];
+            gv[r] = next_g[r];
+            if (!live)
+                gv[r] = {};
         }
-        const float mean = live ? D.mean[t] : 0.f, rstd = live ? D.rstd[t] : 0.f;
+        if constexpr (AHEAD)
+            fetch(t + step);
         float sums[2] = {0.f, 0.f};
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint32_t a = lane + r * LANES;
-            if (live && a < D.vecs) {
-                const uint32_t seen = shared_front<E, VW>(a, vec_offset<VW>(a, D.row));
-                float x[N], g[N];
-                unpack<E, VW>(xv[r], x);
-                unpack<E, VW>(gv[r], g);
+            float x[N], g[N];
+            unpack<E, VW>(xv[r], x);
+            unpack<E, VW>(gv[r], g);
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float xhat = (x[i] - mean) * rstd, gw = g[i] * w[r][i];
-                    dw[r][i] = fmaf(g[i], xhat, dw[r][i]);
-                    db[r][i] += g[i];
-                    sums[0] += uint32_t(i) < seen ? 0.f : gw;
-                    sums[1] += uint32_t(i) < seen ? 0.f : gw * xhat;
-                }
+            for (int i = 0; i < N; ++i) {
+                const float xhat = (x[i] - mean) * rstd, gw = g[i] * w[r][i];
+                dw[r][i] = fmaf(g[i], xhat, dw[r][i]);
+                db[r][i] += g[i];
+                sums[0] += uint32_t(i) < seen[r] ? 0.f : gw;
+                sums[1] += uint32_t(i) < seen[r] ? 0.f : gw * xhat;
             }
         }
         team_sum<LANES, 2>(sums, lds[turn]);
         const float c1 = sums[0] * D.inv_D, c2 = sums[1] * D.inv_D;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const uint32_t a = lane + r * LANES;
-            if (live && a < D.vecs) {
+        for (int r = 0; r < R; ++r)
+            if (live && lane + r * LANES < D.vecs) {
                 float x[N], g[N];
                 unpack<E, VW>(xv[r], x);
                 unpack<E, VW>(gv[r], g);
 #pragma unroll
                 for (int i = 0; i < N; ++i)
                     x[i] = rstd * (g[i] * w[r][i] - c1 - (x[i] - mean) * rstd * c2);
-                store_vec<VW>(D.dx + at + vec_offset<VW>(a, D.row), pack<E, VW>(x));
+                store_vec<VW>(D.dx + at + off[r], pack<E, VW>(x));
             }
-        }
     }
     float *const mine = D.partial + uint64_t(blockIdx.x) * 2 * D.width;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const uint32_t a = lane + r * LANES;
-        if constexpr (TEAMS > 1) {          // the teams' sums, added by the first in their order
+        if constexpr (TEAMS == 1) {
+            if (lane + r * LANES < D.vecs) {
+                store_columns<E, VW>(mine, lane + r * LANES, off[r], dw[r]);
+                store_columns<E, VW>(mine + D.width, lane + r * LANES, off[r], db[r]);
+            }
+        } else {                    // the teams' sums, added in their order
             lds_barrier();
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 joined[team][i * LANES + lane] = dw[r][i];
-                joined[team][(N + i) * LANES + lane] = db[r][i];
+                joined[team][COLUMNS + i * LANES + lane] = db[r][i];
             }
             lds_barrier();
-            if (team == 0)
+            for (uint32_t c = threadIdx.x; c < COLUMNS * 2; c += THREADS) {
+                float sum = joined[0][c];
                 for (int j = 1; j < TEAMS; ++j)
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        dw[r][i] += joined[j][i * LANES + lane];
-                        db[r][i] += joined[j][(N + i) * LANES + lane];
-                    }
-        }
-        if (team == 0 && a < D.vecs) {
-            const uint32_t off = vec_offset<VW>(a, D.row);
-            store_columns<E, VW>(mine, a, off, dw[r]);
-            store_columns<E, VW>(mine + D.width, a, off, db[r]);
+                    sum += joined[j][c];
+                const uint32_t a = c % LANES + r * LANES, i = c / LANES % N, at = vec_offset<VW>(a, D.row);
+                if (a < D.vecs && i >= shared_front<E, VW>(a, at))
+                    mine[(c >= COLUMNS ? D.width : 0) + at / sizeof(E) + i] = sum;
+            }
         }
     }
 }
@@ -362,6 +400,7 @@ __global__ __launch_bounds__(kThreads) void norm_join_kernel(const NormJoinDesc 
     const uint32_t c = threadIdx.x & 15, s = threadIdx.x >> 4, col = (blockIdx.x * 16 + c) * 4;
     f4 sum = {0.f, 0.f, 0.f, 0.f};
     if (col < D.width)
+#pragma unroll 8
         for (uint32_t g = s; g < D.groups; g += 16)
             sum += *reinterpret_cast<const f4 *>(D.partial + (uint64_t(g) * 2 + blockIdx.y) * D.width + col);
     part[s][c] = sum;
@@ -380,55 +419,53 @@ __global__ __launch_bounds__(kThreads) void norm_join_kernel(const NormJoinDesc 
 // --------------------------------------------------------------- launches --
 
 // fn for a row of `vecs` vectors: f(lanes of a row, function).  Lanes and
-// vectors a lane so that a row is in registers at once: short rows share a
-// wave, up to 512 vectors a wave takes a row and needs no barrier.
+// vectors a lane so that a row is in registers at once.
 struct NormShape {
     const void *fn;
-    int lanes;
+    int lanes;                      // or threads, of a gradient
+    int groups;                     // that take rows in turn: as many as the device holds at once
 };
 
 template <typename E, int VW>
 NormShape norm_shape(int64_t vecs)
 {
-    const auto of = [](auto fn, int lanes) { return NormShape{reinterpret_cast<const void *>(fn), lanes}; };
+    const auto of = [](auto fn, int lanes, int groups) { return NormShape{reinterpret_cast<const void *>(fn), lanes, groups}; };
     if (vecs <= 16)
-        return of(norm_kernel<E, VW, 16, 1>, 16);
+        return of(norm_kernel<E, VW, 16, 1>, 16, 2048);
     if constexpr (VW == 16) {
         if (vecs <= 64)
-            return of(norm_kernel<E, VW, 64, 1>, 64);
+            return of(norm_kernel<E, VW, 64, 1>, 64, 2048);
         if (vecs <= 128)
-            return of(norm_kernel<E, VW, 64, 2>, 64);
+            return of(norm_kernel<E, VW, 64, 2>, 64, 1024);
         if (vecs <= 256)
-            return of(norm_kernel<E, VW, 64, 4>, 64);
+            return of(norm_kernel<E, VW, 256, 1>, 256, 2048);
         if (vecs <= 512)
-            return of(norm_kernel<E, VW, 64, 8>, 64);
+            return of(norm_kernel<E, VW, 256, 2>, 256, 1024);
         if (vecs <= 1024)
-            return of(norm_kernel<E, VW, 256, 4>, 256);
-        if (vecs <= 2048)
-            return of(norm_kernel<E, VW, 256, 8>, 256);
+            return of(norm_kernel<E, VW, 256, 4>, 256, 512);
     }
-    return of(norm_long_kernel<E>, 1024);
+    return of(norm_long_kernel<E>, 1024, 0);
 }
 
 template <typename E, int VW>
 NormShape norm_grad_shape(int64_t vecs)
 {
-    const auto of = [](auto fn, int lanes) { return NormShape{reinterpret_cast<const void *>(fn), lanes}; };
+    const auto of = [](auto fn, int threads) { return NormShape{reinterpret_cast<const void *>(fn), threads, 0}; };
     if (vecs <= 16)
-        return of(norm_grad_kernel<E, VW, 16, 1>, 16);
+        return of(norm_grad_kernel<E, VW, 16, 1, 256>, 256);
     if constexpr (VW == 16) {
         if (vecs <= 64)
-            return of(norm_grad_kernel<E, VW, 64, 1>, 64);
+            return of(norm_grad_kernel<E, VW, 64, 1, 256>, 256);
         if (vecs <= 128)
-            return of(norm_grad_kernel<E, VW, 64, 2>, 64);
+            return of(norm_grad_kernel<E, VW, 64, 2, 256>, 256);
         if (vecs <= 256)
-            return of(norm_grad_kernel<E, VW, 64, 4>, 64);
+            return of(norm_grad_kernel<E, VW, 128, 2, 256>, 256);
         if (vecs <= 512)
-            return of(norm_grad_kernel<E, VW, 256, 2>, 256);
+            return of(norm_grad_kernel<E, VW, 256, 2, 256>, 256);
         if (vecs <= 1024)
-            return of(norm_grad_kernel<E, VW, 256, 4>, 256);
+            return of(norm_grad_kernel<E, VW, 256, 4, 256>, 256);
         if (vecs <= kNormGradVecs)
-            return of(norm_grad_kernel<E, VW, 1024, 2>, 1024);
+            return of(norm_grad_kernel<E, VW, 512, 4, 512>, 512);
     }
     return of(norm_grad_long_kernel<E>, 1024);
 }
@@ -444,15 +481,16 @@ basp_status launch_norm(const basp_norm_plan &p, const void *x, const void *weig
 {
     const int64_t row = p.D * p.es;
     const NormShape s = BASP_BY_ROW(norm_shape, p.dtype, p.vw, p.vecs);
-    const int64_t teams = s.lanes < kThreads ? kThreads / s.lanes : 1, step = kLaunchGroups / (s.lanes > kThreads ? 4 : 1) * teams;
+    const bool in_turn = s.lanes <= kThreads;           // or a row a work-group
+    const int64_t teams = in_turn ? kThreads / s.lanes : 1, step = in_turn ? p.T : kLaunchGroups / 4;
     basp_status st = BASP_OK;
     for (int64_t t0 = 0; t0 < p.T && st == BASP_OK; t0 += step) {
-        const int64_t n = std::min(step, p.T - t0);
+        const int64_t n = std::min(step, p.T - t0), groups = (n + teams - 1) / teams;
         const NormDesc D = {static_cast<const char *>(x) + t0 * row, weight, bias, static_cast<char *>(y) + t0 * row,
                             mean ? mean + t0 : nullptr, rstd ? rstd + t0 : nullptr, uint32_t(n), uint32_t(row),
                             uint32_t(p.vecs), uint32_t(p.D), eps, 1.f / float(p.D), p.weight_dtype};
-        st = launch_kernel(s.fn, dim3(uint32_t((n + teams - 1) / teams)), std::max(kThreads, s.lanes), D, stream, t0 == 0,
-                           t0 + n == p.T);
+        st = launch_kernel(s.fn, dim3(uint32_t(in_turn ? std::min<int64_t>(groups, s.groups) : groups)),
+                           std::max(kThreads, s.lanes), D, stream, t0 == 0, t0 + n == p.T);
     }
     return st;
 }
@@ -467,7 +505,7 @@ basp_status launch_norm_grad(const basp_norm_plan &p, const void *dy, const void
                       uint32_t(p.D), uint32_t(p.width), 1.f / float(p.D), p.weight_dtype};
     basp_status st = BASP_OK;
     if (p.T && (p.vecs <= kNormGradVecs || p.vw < 16)) {
-        st = launch_kernel(s.fn, dim3(D.groups), std::max(kThreads, s.lanes), D, stream, true, false);
+        st = launch_kernel(s.fn, dim3(D.groups), s.lanes, D, stream, true, false);
     } else if (p.T) {
         const int64_t step = kLaunchGroups / 4;
         for (int64_t t0 = 0; t0 < p.T && st == BASP_OK; t0 += step) {

@@ -22,6 +22,7 @@ __device__ inline void team_sum(float (&x)[M], float *lds)
             x[m] += __shfl_xor(x[m], d);
     if constexpr (LANES > 64) {
         constexpr int WAVES = LANES / 64;
+        const float *const team = lds + threadIdx.x / LANES * WAVES * M;
         if ((threadIdx.x & 63) == 0)
 #pragma unroll
             for (int m = 0; m < M; ++m)
@@ -29,10 +30,10 @@ __device__ inline void team_sum(float (&x)[M], float *lds)
         lds_barrier();
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            float s = lds[m];
+            float s = team[m];
 #pragma unroll
             for (int w = 1; w < WAVES; ++w)
-                s += lds[w * M + m];
+                s += team[w * M + m];
             x[m] = s;
         }
     }
