@@ -74,11 +74,19 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
                                     At tile)
 {
     const int half = (threadIdx.x & 63) >> 5;
+    // half a result's scores as weights, and their sum
+    const auto weigh = [&](f32x16 &s, int part, float base) {
+#pragma unroll
+        for (int i = 8 * part; i < 8 * part + 8; ++i) {
+            s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], A.scale_log2, -base));
+            run.l += s[i];
+        }
+    };
     bool more = next();
     while (more) {
         f32x16 s[ROWS / 32];
         float most;
-        bool behind;
+        bool behind, wild;
         for (;;) {
             const auto at = tile();
 #pragma unroll
@@ -102,17 +110,20 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
             behind = __ballot(most > run.m + A.slack);
             if (behind)
                 break;
+            wild = at.part && wild_rows<T, C, ROWS, ROWS>(at.values, 0);
+            if (wild)
+                break;
+            // weights and their products in steps of 16 keys: exponentials are
+            // taken while the matrix unit is at the step before
             const float base = run.m == -INFINITY ? 0.f : run.m * A.scale_log2;
 #pragma unroll
-            for (int t = 0; t < ROWS / 32; ++t)
+            for (int j = 0; j < ROWS / 16; ++j) {
+                weigh(s[j / 2], j % 2, base);
+                const Vec8<T> weights = operand<T>(s[j / 2], j % 2);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], A.scale_log2, -base));
-                    run.l += s[t][i];
-                }
-            if (at.part && wild_rows<T, C, ROWS, ROWS>(at.values, 0))
-                break;
-            add_rows<T, C, ROWS, ROWS>(run.o, at.values, 0, s);
+                for (int b = 0; b < C / 32; ++b)
+                    run.o[b] = product(Tile<T, C, ROWS>::along_rows(at.values, 16 * j, b), weights, run.o[b]);
+            }
             more = next();
             if (!more)
                 return;
@@ -120,6 +131,10 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
         if (behind) {
             run.rescale(most, A.scale_log2);
         } else {
+            const float base = run.m == -INFINITY ? 0.f : run.m * A.scale_log2;
+#pragma unroll
+            for (int j = 0; j < ROWS / 16; ++j)
+                weigh(s[j / 2], j % 2, base);
             add_wild_rows<T, C, ROWS, ROWS>(run.o, tile().values, 0, s);
             more = next();
         }
@@ -174,21 +189,19 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_tile_
     const uint32_t wave = scalar(threadIdx.x >> 6), lane = threadIdx.x & 63, first = block * kTileColumns;
     const Column col(A, seq, first + wave * 32 + (lane & 31), key_head);
     Vec8<T> q[C / 16];
-    load_column<T, C>(A, D.q + col.at(A, shard), col.live, q);
+    load_column<T, C, DIRECT>(A, D.q + col.at(A, shard), col.live, q);
 
-    const uint32_t last = (first + kTileColumns < uint32_t(A.total) ? first + kTileColumns : uint32_t(A.total)) - 1;
-    int low = seq.start + int(fastdiv(first, A.by_ratio)), high = seq.start + int(fastdiv(last, A.by_ratio));
-    low = low < 0 ? 0 : low;
-    high = high < seq.length ? high : seq.length - 1;
-    const KeyTiles<KEYS> tiles(A, low, high);
-    const int wave_low = wave_min(col.live ? col.position : 0x7fffffff), wave_high = wave_max(col.live ? col.position : -1);
+    const Span all(A, seq, first, kTileColumns), mine(A, seq, first + wave * 32, 32);
+    const KeyTiles<KEYS> tiles(A, all.low, all.high);
 
     const char *const k = D.k + shard * A.kv_shard + key_head * A.kv_head;
     const char *const v = D.v + shard * A.kv_shard + key_head * A.kv_head;
+    uint32_t off[Keys::kBytes / 16 / kThreads];
+    Keys::template load_offsets<kThreads>(off, A.kv_token, A.d);
     const auto fetch = [&](int i, char *to) {
         const int64_t at = int64_t{tiles.first(i)} * A.kv_token;
-        Keys::template load<kThreads, DIRECT>(to, k + at, A.kv_token, tiles.rows(i), A.d);
-        Keys::template load<kThreads, DIRECT>(to + Keys::kBytes, v + at, A.kv_token, tiles.rows(i), A.d);
+        Keys::template load<kThreads, DIRECT>(to, off, k + at, A.kv_token, tiles.rows(i), A.d);
+        Keys::template load<kThreads, DIRECT>(to + Keys::kBytes, off, v + at, A.kv_token, tiles.rows(i), A.d);
     };
     Running<C / 32> run;
     if (tiles.tiles)
@@ -201,7 +214,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_tile_
             lds_barrier();          // the tile is there, and the one before is no longer read
             if (i + 1 < tiles.tiles)
                 fetch(i + 1, lds[~i & 1][0]);
-            seen = how_seen(A, wave_low, wave_high, tiles.first(i), tiles.rows(i));
+            seen = how_seen(A, mine.low, mine.high, tiles.first(i), tiles.rows(i));
             if (seen != Seen::none)
                 return true;
         }
@@ -247,16 +260,18 @@ __global__ __launch_bounds__(kThreads, 1) void attend_step_kernel(const AttendDe
     const uint32_t wave = scalar(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const Column col(A, seq, block * kStepColumns + (lane & 31), key_head);
     Vec8<T> q[C / 16];
-    load_column<T, C>(A, D.q + col.at(A, shard), col.live, q);
-    const int low = wave_min(col.live ? col.position : 0x7fffffff), high = wave_max(col.live ? col.position : -1);
-    const KeyTiles<KEYS> tiles(A, low, high);
+    load_column<T, C, DIRECT>(A, D.q + col.at(A, shard), col.live, q);
+    const Span mine(A, seq, block * kStepColumns, 32);
+    const KeyTiles<KEYS> tiles(A, mine.low, mine.high);
 
     const char *const k = D.k + shard * A.kv_shard + key_head * A.kv_head;
     const char *const v = D.v + shard * A.kv_shard + key_head * A.kv_head;
+    uint32_t off[Keys::kBytes / 16 / 64];
+    Keys::template load_offsets<64>(off, A.kv_token, A.d);
     const auto fetch = [&](int i, char *to) {
         const int64_t at = int64_t{tiles.first(i)} * A.kv_token;
-        Keys::template load<64, DIRECT>(to, k + at, A.kv_token, tiles.rows(i), A.d);
-        Keys::template load<64, DIRECT>(to + Keys::kBytes, v + at, A.kv_token, tiles.rows(i), A.d);
+        Keys::template load<64, DIRECT>(to, off, k + at, A.kv_token, tiles.rows(i), A.d);
+        Keys::template load<64, DIRECT>(to + Keys::kBytes, off, v + at, A.kv_token, tiles.rows(i), A.d);
     };
     Running<C / 32> run;
     const int step = D.splits * WAVES;
@@ -280,7 +295,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_step_kernel(const AttendDe
     attend_tiles<T, C, KEYS>(A, q, col.position, run, next, [&]() {
         const int first = tiles.first(i), rows = tiles.rows(i);
         return TileView{lds[wave][buffer][0], lds[wave][buffer][1], first, rows,
-                        rows < KEYS || how_seen(A, low, high, first, rows) != Seen::all};
+                        rows < KEYS || how_seen(A, mine.low, mine.high, first, rows) != Seen::all};
     });
 
     // the waves' sums relative to the largest of their maxima
@@ -410,7 +425,7 @@ extern "C" basp_status basp_attention(const basp_attention_plan *p, const void *
         D.splits = p->splits;
         D.by_blocks = basp::make_fastdiv(uint32_t(p->blocks));
         D.by_splits = basp::make_fastdiv(uint32_t(p->splits));
-        const bool direct = basp::whole_chunks(*p, {k, v});
+        const bool direct = basp::whole_chunks(*p, {q, k, v});
         return BASP_BY_HEAD(basp::launch_attention, p, *p, D, direct, stream);
     });
 }

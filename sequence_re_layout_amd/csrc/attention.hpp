@@ -100,11 +100,44 @@ __device__ inline Vec8<T> operand(const f32x16 &c, int s)
     return r;
 }
 
-__device__ inline float other_half(float x) { return __shfl_xor(x, 32); }
+// The value of the lane across the wave.
+__device__ inline float other_half(float x)
+{
+    const uint32_t w = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    return __builtin_bit_cast(float, (threadIdx.x & 32) ? uint32_t(r[0]) : uint32_t(r[1]));
+}
 
 // ------------------------------------------------------------------- tiles --
 
 typedef __attribute__((address_space(3))) char lds_char;
+
+// `bytes` bytes of memory from an address that is the same for the wave: reads
+// beyond them give zeros.
+__device__ inline u32x4 memory_rows(const void *from, uint32_t bytes)
+{
+    const uint64_t at = reinterpret_cast<uint64_t>(from);
+    return u32x4{scalar(uint32_t(at)), scalar(uint32_t(at >> 32)) & 0xffffu, scalar(bytes), 0x00020000u};
+}
+
+// BYTES bytes of each lane, `off` bytes into memory, straight to LDS, lane after
+// lane from `to` on.  Written as an instruction, since the compiler would wait
+// for it before the next transposed read of any part of LDS; it is complete after
+// wait_tiles.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"         // m0 is named so that the compiler sets it anew for itself
+template <int BYTES>
+__device__ inline void copy_to_lds(char *to, u32x4 from, uint32_t off)
+{
+    const uint32_t at = scalar(uint32_t(reinterpret_cast<uintptr_t>((lds_char *)to)));
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                     :: "s"(at), "v"(off), "s"(from) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                     :: "s"(at), "v"(off), "s"(from) : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 // ROWS rows of C channels in LDS.
 template <typename T, int C, int ROWS>
@@ -175,31 +208,39 @@ struct Tile {
         return static_cast<float>(*reinterpret_cast<const T *>(tile + row * kRow + c * 16 + (channel % kPer) * sizeof(T)));
     }
 
-    // Rows of `d` channels, `token` bytes apart, into the tile by THREADS threads:
-    // zeros after row `rows` and channel d.  DIRECT: rows of whole 16-byte chunks
-    // at 16-byte addresses go from memory to LDS without passing registers; the
-    // loads are complete after wait_tiles and a barrier.
-    template <int THREADS, bool DIRECT>
-    static __device__ inline void load(char *__restrict__ tile, const char *from, uint32_t token, int rows, int d)
+    // Brings rows of `d` channels, `token` bytes apart, into a tile by THREADS
+    // threads, with zeros after the last row and channel d.  DIRECT: rows of whole
+    // 16-byte chunks at 16-byte addresses go from memory to LDS without passing
+    // registers; the loads are complete after wait_tiles and a barrier.
+    //
+    // off: the places of a thread's chunks from the first row, the same for every
+    // tile (load_offsets).
+    template <int THREADS, int STEPS>
+    static __device__ inline void load_offsets(uint32_t (&off)[STEPS], uint32_t token, int d)
     {
-        const uint32_t thread = threadIdx.x % THREADS;
-        constexpr int STEPS = kBytes / 16 / THREADS;
-        static_assert(kBytes % (16 * THREADS) == 0, "whole rounds of the threads");
-        if constexpr (DIRECT) {
-            const __amdgpu_buffer_rsrc_t from_rows =
-                __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(from), 0, 0x7ffffff0, 0x00020000);
 #pragma unroll
-            for (int p = 0; p < STEPS; ++p) {
-                const uint32_t i = p * THREADS + thread, r = i / kChunks, c = (i % kChunks) ^ swizzle(r);
-                // beyond the buffer: reads as zeros
-                const uint32_t off = int(r) < rows && int(c) * kPer < d ? r * token + c * 16 : 0x80000000u;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    from_rows, (lds_char *)(tile + (p * THREADS + (thread & ~63u)) * 16), 16, off, 0, 0, 0);
-            }
+        for (int p = 0; p < STEPS; ++p) {
+            const uint32_t i = p * THREADS + threadIdx.x % THREADS, r = i / kChunks, c = (i % kChunks) ^ swizzle(r);
+            // beyond any buffer: reads as zeros
+            off[p] = int(c) * kPer < d ? r * token + c * 16 : 0x80000000u;
+        }
+    }
+
+    template <int THREADS, bool DIRECT, int STEPS>
+    static __device__ inline void load(char *__restrict__ tile, const uint32_t (&off)[STEPS], const char *from, uint32_t token,
+                                       int rows, int d)
+    {
+        static_assert(kBytes == 16 * THREADS * STEPS, "whole rounds of the threads");
+        if constexpr (DIRECT) {
+            const uint32_t wave = scalar(threadIdx.x % THREADS >> 6);
+            const u32x4 rows_of = memory_rows(from, rows * token);
+#pragma unroll
+            for (int p = 0; p < STEPS; ++p)
+                copy_to_lds<16>(tile + (p * THREADS + wave * 64) * 16, rows_of, off[p]);
         } else {
 #pragma unroll
             for (int p = 0; p < STEPS; ++p) {
-                const uint32_t i = p * THREADS + thread, r = i / kChunks, c = (i % kChunks) ^ swizzle(r);
+                const uint32_t i = p * THREADS + threadIdx.x % THREADS, r = i / kChunks, c = (i % kChunks) ^ swizzle(r);
                 typedef T xn __attribute__((ext_vector_type(kPer)));
                 xn x = {};
                 if (int(r) < rows)
@@ -227,8 +268,7 @@ struct Tile {
 // Up to 64 floats straight to LDS by a wave, zeros after n.
 __device__ inline void load_floats(float *to, const float *from, int n)
 {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(from), 0, n * 4, 0x00020000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_char *)to, 4, (threadIdx.x & 63) * 4, 0, 0, 0);
+    copy_to_lds<4>(reinterpret_cast<char *>(to), memory_rows(from, n * 4), (threadIdx.x & 63) * 4);
 }
 
 // The wave's loads to LDS have arrived.
@@ -393,17 +433,20 @@ __device__ inline Seen how_seen(const AttendShape &A, int low, int high, int fir
     return last <= low && (high - first < A.reach || last < A.firsts) ? Seen::all : Seen::some;
 }
 
-__device__ inline int wave_min(int x)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_xor(x, d);
-        x = y < x ? y : x;
-    }
-    return scalar(x);
-}
+// The positions of columns [first, first + n) that are within the sequence: their
+// first and last, or last < first.
+struct Span {
+    int low, high;
 
-__device__ inline int wave_max(int x) { return -wave_min(-x); }
+    __device__ inline Span(const AttendShape &A, const Sequence &s, uint32_t first, uint32_t n)
+    {
+        const uint32_t last = first + n <= uint32_t(A.total) ? first + n - 1 : uint32_t(A.total) - 1;
+        low = s.start + int(fastdiv(first, A.by_ratio));
+        high = first < uint32_t(A.total) ? s.start + int(fastdiv(last, A.by_ratio)) : -1;
+        low = low < 0 ? 0 : low;
+        high = high < s.length ? high : s.length - 1;
+    }
+};
 
 // A lane's column: a query and a head of the key head's group.
 struct Column {
@@ -429,15 +472,23 @@ struct Column {
     }
 };
 
-template <typename T, int C>
+// A row's channels as a column's operands, zeros where it is not live.
+template <typename T, int C, bool DIRECT>
 __device__ inline void load_column(const AttendShape &A, const char *row, bool live, Vec8<T> (&x)[C / 16])
 {
     const int half = (threadIdx.x & 63) >> 5;
 #pragma unroll
     for (int c = 0; c < C / 16; ++c) {
         x[c] = Vec8<T>{};
-        if (live)
-            x[c] = row_part<T>(row, 16 * c + 8 * half, A.d);
+        if constexpr (DIRECT) {         // d is a multiple of a chunk, which is 8 or 4 channels
+            if (sizeof(T) == 2 ? live && 16 * c + 8 * half < A.d : live && 16 * c + 8 * half + 4 < A.d)
+                x[c] = *reinterpret_cast<const Vec8<T> *>(row + (16 * c + 8 * half) * sizeof(T));
+            else if (sizeof(T) == 4 && live && 16 * c + 8 * half < A.d)
+                x[c] = row_part<T>(row, 16 * c + 8 * half, A.d);
+        } else {
+            if (live)
+                x[c] = row_part<T>(row, 16 * c + 8 * half, A.d);
+        }
     }
 }
 

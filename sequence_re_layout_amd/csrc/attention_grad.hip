@@ -58,23 +58,21 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
     const int half = lane >> 5;
     const Column col(A, seq, first + wave * 32 + (lane & 31), key_head);
     Vec8<T> q[C / 16], g[C / 16];
-    load_column<T, C>(A, D.q + col.at(A, shard), col.live, q);
-    load_column<T, C>(A, D.dout + col.at(A, shard), col.live, g);
+    load_column<T, C, DIRECT>(A, D.q + col.at(A, shard), col.live, q);
+    load_column<T, C, DIRECT>(A, D.dout + col.at(A, shard), col.live, g);
     const float lse = col.live ? D.lse[col.row(A, shard)] * kLog2e : 0.f;
 
-    const uint32_t last = (first + kTileColumns < uint32_t(A.total) ? first + kTileColumns : uint32_t(A.total)) - 1;
-    int low = seq.start + int(fastdiv(first, A.by_ratio)), high = seq.start + int(fastdiv(last, A.by_ratio));
-    low = low < 0 ? 0 : low;
-    high = high < seq.length ? high : seq.length - 1;
-    const KeyTiles<KEYS> tiles(A, low, high);
-    const int wave_low = wave_min(col.live ? col.position : 0x7fffffff), wave_high = wave_max(col.live ? col.position : -1);
+    const Span all(A, seq, first, kTileColumns), mine(A, seq, first + wave * 32, 32);
+    const KeyTiles<KEYS> tiles(A, all.low, all.high);
 
     const char *const k = D.k + shard * A.kv_shard + key_head * A.kv_head;
     const char *const v = D.v + shard * A.kv_shard + key_head * A.kv_head;
+    uint32_t off[Keys::kBytes / 16 / kThreads];
+    Keys::template load_offsets<kThreads>(off, A.kv_token, A.d);
     const auto fetch = [&](int i, char *to) {
         const int64_t at = int64_t{tiles.first(i)} * A.kv_token;
-        Keys::template load<kThreads, DIRECT>(to, k + at, A.kv_token, tiles.rows(i), A.d);
-        Keys::template load<kThreads, DIRECT>(to + Keys::kBytes, v + at, A.kv_token, tiles.rows(i), A.d);
+        Keys::template load<kThreads, DIRECT>(to, off, k + at, A.kv_token, tiles.rows(i), A.d);
+        Keys::template load<kThreads, DIRECT>(to + Keys::kBytes, off, v + at, A.kv_token, tiles.rows(i), A.d);
     };
     // on to the next 32 keys that some column of the wave sees
     int u = -1;
@@ -88,7 +86,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
                 if (j + 1 < tiles.tiles)
                     fetch(j + 1, lds[~j & 1][0]);
             }
-            seen = rows > 0 ? how_seen(A, wave_low, wave_high, tiles.first(j) + 32 * t, rows < 32 ? rows : 32) : Seen::none;
+            seen = rows > 0 ? how_seen(A, mine.low, mine.high, tiles.first(j) + 32 * t, rows < 32 ? rows : 32) : Seen::none;
             if (seen != Seen::none)
                 return true;
         }
@@ -233,8 +231,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && C <= 64 ? 2 : 1) void a
 
     Vec8<T> k[C / 16], v[C / 16];
     const int64_t at_key = shard * A.kv_shard + key_head * A.kv_head + int64_t{exists ? key : 0} * A.kv_token;
-    load_column<T, C>(A, D.k + at_key, exists, k);
-    load_column<T, C>(A, D.v + at_key, exists, v);
+    load_column<T, C, DIRECT>(A, D.k + at_key, exists, k);
+    load_column<T, C, DIRECT>(A, D.v + at_key, exists, v);
     f32x16 dk[C / 32], dv[C / 32];
 #pragma unroll
     for (int b = 0; b < C / 32; ++b)
@@ -254,12 +252,15 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && C <= 64 ? 2 : 1) void a
     end = end < begin + length ? end : begin + length;
     const int tiles = end > begin ? (end - begin + ROWS - 1) / ROWS : 0, all = tiles * A.ratio;
 
+    uint32_t off[Rows::kBytes / 16 / kThreads];
+    Rows::template load_offsets<kThreads>(off, A.q_token, A.d);
     const auto fetch = [&](int head, int tile, int buffer) {
+        char *const to = lds[buffer][0];
         const int from = begin + tile * ROWS, rows = end - from < ROWS ? end - from : ROWS;
         const uint32_t q_head = key_head * A.ratio + head;
         const int64_t at = shard * A.q_shard + q_head * A.q_head + int64_t{from} * A.q_token;
-        Rows::template load<kThreads, DIRECT>(lds[buffer][0], D.q + at, A.q_token, rows, A.d);
-        Rows::template load<kThreads, DIRECT>(lds[buffer][1], D.dout + at, A.q_token, rows, A.d);
+        Rows::template load<kThreads, DIRECT>(to, off, D.q + at, A.q_token, rows, A.d);
+        Rows::template load<kThreads, DIRECT>(to + Rows::kBytes, off, D.dout + at, A.q_token, rows, A.d);
         if (wave < 2)
             load_floats(lds_rows[buffer][wave], D.rows + wave * D.lse_elems + (int64_t{shard} * A.Hl_q + q_head) * A.queries + from,
                         rows);
