@@ -62,17 +62,16 @@ struct Running {
     }
 };
 
-// A wave's way through tiles of ROWS keys: next() goes on to the next tile that
-// some of its columns see and says whether there is one, and tile() has it.  m is
-// left behind a column's maximum by up to 8 in the exponent of two, which keeps
-// weights below 2^8 (in range of fp16 too) and their relative precision: after
-// the first tile it hardly ever moves.  Where it does, the loop is left, the sums
-// are rescaled and the tile begun again (a branch in the loop would copy them in
-// every tile, see wild_rows).
-template <typename T, int C, int ROWS, typename Next, typename At>
-__device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C / 16], int position, Running<C / 32> &run, Next next,
-                                    At tile)
+// The columns of a wave along its way through tiles of ROWS keys.  m is left
+// behind a column's maximum by up to 8 in the exponent of two, which keeps weights
+// below 2^8 (in range of fp16 too) and their relative precision: after the first
+// tile it hardly ever moves.  Where it does, the loop is left, the sums are
+// rescaled and the tile begun again (a branch in the loop would copy them in every
+// tile, see wild_rows).
+template <typename T, int C, int ROWS, typename Walk>
+__device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C / 16], int position, Running<C / 32> &run, Walk &walk)
 {
+    constexpr int TILES = ROWS / 32;
     const int half = (threadIdx.x & 63) >> 5;
     // half a result's scores as weights, and their sum
     const auto weigh = [&](f32x16 &s, int part, float base) {
@@ -82,27 +81,39 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
             run.l += s[i];
         }
     };
-    bool more = next();
+    wait_tiles();                   // for the columns, too, and on every way into the loop
+    bool more = walk.next();
     while (more) {
-        f32x16 s[ROWS / 32];
+        f32x16 s[TILES];
         float most;
         bool behind, wild;
         for (;;) {
-            const auto at = tile();
+            const char *const keys = walk.keys(), *const values = walk.values();
+            const bool hides = walk.hides();
+            RowOperands<T, C, ROWS> rows[TILES];
+            SumOperands<T, C, ROWS> sums[TILES];
+            rows[0].read(keys, 0);
+            pin_reads();
 #pragma unroll
-            for (int t = 0; t < ROWS / 32; ++t)
-                s[t] = rows_times<T, C, ROWS>(at.keys, 32 * t, q);
-            if (at.part) {
-                const Sight sees(A, position, at.first + at.rows);
+            for (int t = 0; t < TILES; ++t) {
+                if (t + 1 < TILES)
+                    rows[t + 1].read(keys, 32 * (t + 1));
+                else
+                    sums[0].read(values, 0);
+                s[t] = rows[t].times(q);
+                pin_reads();
+            }
+            if (hides) {
+                const Sight sees(A, position, walk.key() + 4 * half, walk.key_end());
 #pragma unroll
-                for (int t = 0; t < ROWS / 32; ++t)
+                for (int t = 0; t < TILES; ++t)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        s[t][i] = sees(at.first + 32 * t + row_of(i, half)) ? s[t][i] : -INFINITY;
+                        s[t][i] = sees(32 * t + row_of(i, 0)) ? s[t][i] : -INFINITY;
             }
             most = s[0][0];
 #pragma unroll
-            for (int t = 0; t < ROWS / 32; ++t)
+            for (int t = 0; t < TILES; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     most = fmaxf(most, s[t][i]);
@@ -110,21 +121,24 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
             behind = __ballot(most > run.m + A.slack);
             if (behind)
                 break;
-            wild = at.part && wild_rows<T, C, ROWS, ROWS>(at.values, 0);
+            wild = hides && wild_rows<T, C, ROWS, ROWS>(values, 0);
             if (wild)
                 break;
             // weights and their products in steps of 16 keys: exponentials are
             // taken while the matrix unit is at the step before
             const float base = run.m == -INFINITY ? 0.f : run.m * A.scale_log2;
 #pragma unroll
-            for (int j = 0; j < ROWS / 16; ++j) {
-                weigh(s[j / 2], j % 2, base);
-                const Vec8<T> weights = operand<T>(s[j / 2], j % 2);
+            for (int t = 0; t < TILES; ++t) {
+                if (t + 1 < TILES)
+                    sums[t + 1].read(values, 32 * (t + 1));
+                pin_reads();
 #pragma unroll
-                for (int b = 0; b < C / 32; ++b)
-                    run.o[b] = product(Tile<T, C, ROWS>::along_rows(at.values, 16 * j, b), weights, run.o[b]);
+                for (int j = 0; j < 2; ++j) {
+                    weigh(s[t], j, base);
+                    sums[t].add(run.o, j, s[t]);
+                }
             }
-            more = next();
+            more = walk.next();
             if (!more)
                 return;
         }
@@ -135,20 +149,11 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
 #pragma unroll
             for (int j = 0; j < ROWS / 16; ++j)
                 weigh(s[j / 2], j % 2, base);
-            add_wild_rows<T, C, ROWS, ROWS>(run.o, tile().values, 0, s);
-            more = next();
+            add_wild_rows<T, C, ROWS, ROWS>(run.o, walk.values(), 0, s);
+            more = walk.next();
         }
     }
 }
-
-// A tile as a wave sees it: part of the keys hidden from part of its columns, or
-// not.
-struct TileView {
-    const char *__restrict__ keys;
-    const char *__restrict__ values;
-    int first, rows;
-    bool part;
-};
 
 // SHARE registers, from number `from` on, of the finished sums of 32 columns.
 template <typename T, int SHARE>
@@ -180,7 +185,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_tile_
 {
     constexpr int KEYS = sizeof(T) == 2 ? 64 : 32;
     typedef Tile<T, C, KEYS> Keys;
-    __shared__ __attribute__((aligned(16))) char lds[2][2][Keys::kBytes];
+    __shared__ __attribute__((aligned(16))) char lds[4 * Keys::kBytes];
     const AttendShape &A = D.shape;
     const uint32_t group = by_xcd(blockIdx.x, gridDim.x), pair = fastdiv(group, D.by_blocks);
     const uint32_t block = D.blocks - 1 - (group - pair * D.blocks);       // long rows first
@@ -192,37 +197,11 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_tile_
     load_column<T, C, DIRECT>(A, D.q + col.at(A, shard), col.live, q);
 
     const Span all(A, seq, first, kTileColumns), mine(A, seq, first + wave * 32, 32);
-    const KeyTiles<KEYS> tiles(A, all.low, all.high);
-
-    const char *const k = D.k + shard * A.kv_shard + key_head * A.kv_head;
-    const char *const v = D.v + shard * A.kv_shard + key_head * A.kv_head;
-    uint32_t off[Keys::kBytes / 16 / kThreads];
-    Keys::template load_offsets<kThreads>(off, A.kv_token, A.d);
-    const auto fetch = [&](int i, char *to) {
-        const int64_t at = int64_t{tiles.first(i)} * A.kv_token;
-        Keys::template load<kThreads, DIRECT>(to, off, k + at, A.kv_token, tiles.rows(i), A.d);
-        Keys::template load<kThreads, DIRECT>(to + Keys::kBytes, off, v + at, A.kv_token, tiles.rows(i), A.d);
-    };
+    const int64_t at = shard * A.kv_shard + key_head * A.kv_head;
+    KeyWalk<T, C, KEYS, KEYS, kThreads, DIRECT> walk(A, lds, D.k + at, D.v + at, all, mine);
     Running<C / 32> run;
-    if (tiles.tiles)
-        fetch(0, lds[0][0]);
-    int i = -1;
-    Seen seen;
-    const auto next = [&]() {
-        for (++i; i < tiles.tiles; ++i) {
-            wait_tiles();
-            lds_barrier();          // the tile is there, and the one before is no longer read
-            if (i + 1 < tiles.tiles)
-                fetch(i + 1, lds[~i & 1][0]);
-            seen = how_seen(A, mine.low, mine.high, tiles.first(i), tiles.rows(i));
-            if (seen != Seen::none)
-                return true;
-        }
-        return false;
-    };
-    attend_tiles<T, C, KEYS>(A, q, col.position, run, next, [&]() {
-        return TileView{lds[i & 1][0], lds[i & 1][1], tiles.first(i), tiles.rows(i), seen == Seen::some || tiles.rows(i) < KEYS};
-    });
+    walk.begin();
+    attend_tiles<T, C, KEYS>(A, q, col.position, run, walk);
     if (!col.exists)
         return;
     const float l = run.l + other_half(run.l), inv = col.live ? 1.f / l : 0.f;
@@ -241,6 +220,63 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_tile_
     if (D.lse && half == 0)
         D.lse[col.row(A, shard)] = col.live ? log_sum(run.m, l, A) : -INFINITY;
 }
+
+// A wave's way of its own: every step-th tile of 32 keys from number `from` on.
+template <typename T, int C, int BUFFERS, bool DIRECT>
+struct StepWalk {
+    static constexpr int KEYS = 32;
+    typedef Tile<T, C, KEYS> Keys;
+    const AttendShape &A;
+    const Span &mine;
+    const KeyTiles<KEYS> tiles;
+    char *lds;                      // [BUFFERS][2][Keys::kBytes]
+    uint32_t place, off[Keys::kBytes / 16 / 64];
+    const char *k, *v;
+    int i, step, buffer;
+
+    __device__ inline StepWalk(const AttendShape &shape, char *lds_, const char *keys, const char *values, const Span &span, int from,
+                               int step_)
+        : A(shape), mine(span), tiles(shape, span.low, span.high), lds(lds_), place(lds_place(lds_)), k(keys), v(values),
+          i(from - step_), step(step_), buffer(BUFFERS - 1)
+    {
+        Keys::template load_offsets<64>(off, A.kv_token, A.d);
+    }
+    __device__ inline void fetch(int tile, int to)
+    {
+        const int64_t at = int64_t{tiles.first(tile)} * A.kv_token;
+        const int rows = tiles.rows(tile), here = to * 2 * Keys::kBytes;
+        Keys::template load<64, DIRECT>(lds + here, place + here, off, k + at, A.kv_token, rows, A.d);
+        Keys::template load<64, DIRECT>(lds + here + Keys::kBytes, place + here + Keys::kBytes, off, v + at, A.kv_token, rows, A.d);
+    }
+    __device__ inline void begin()
+    {
+        if (i + step < tiles.tiles)
+            fetch(i + step, 0);
+    }
+    __device__ inline bool next()
+    {
+        wave_order();
+        if (BUFFERS == 1 && i >= 0 && i + step < tiles.tiles)
+            fetch(i + step, 0);
+        i += step;
+        if (i >= tiles.tiles)
+            return false;
+        wait_tiles();
+        wave_order();
+        buffer = (buffer + 1) % BUFFERS;
+        if (BUFFERS == 2 && i + step < tiles.tiles)
+            fetch(i + step, (buffer + 1) % BUFFERS);
+        return true;
+    }
+    __device__ inline const char *keys() const { return lds + buffer * 2 * Keys::kBytes; }
+    __device__ inline const char *values() const { return keys() + Keys::kBytes; }
+    __device__ inline int key() const { return tiles.first(i); }
+    __device__ inline int key_end() const { return tiles.first(i) + tiles.rows(i); }
+    __device__ inline bool hides() const
+    {
+        return tiles.rows(i) < KEYS || how_seen(A, mine.low, mine.high, tiles.first(i), tiles.rows(i)) != Seen::all;
+    }
+};
 
 // 32 columns a work-group; its four waves, and the work-groups of a block, take
 // tiles of 32 keys in turn, each wave through LDS of its own, and join their
@@ -262,41 +298,12 @@ __global__ __launch_bounds__(kThreads, 1) void attend_step_kernel(const AttendDe
     Vec8<T> q[C / 16];
     load_column<T, C, DIRECT>(A, D.q + col.at(A, shard), col.live, q);
     const Span mine(A, seq, block * kStepColumns, 32);
-    const KeyTiles<KEYS> tiles(A, mine.low, mine.high);
-
-    const char *const k = D.k + shard * A.kv_shard + key_head * A.kv_head;
-    const char *const v = D.v + shard * A.kv_shard + key_head * A.kv_head;
-    uint32_t off[Keys::kBytes / 16 / 64];
-    Keys::template load_offsets<64>(off, A.kv_token, A.d);
-    const auto fetch = [&](int i, char *to) {
-        const int64_t at = int64_t{tiles.first(i)} * A.kv_token;
-        Keys::template load<64, DIRECT>(to, off, k + at, A.kv_token, tiles.rows(i), A.d);
-        Keys::template load<64, DIRECT>(to + Keys::kBytes, off, v + at, A.kv_token, tiles.rows(i), A.d);
-    };
+    const int64_t at = shard * A.kv_shard + key_head * A.kv_head;
+    StepWalk<T, C, BUFFERS, DIRECT> walk(A, lds[wave][0][0], D.k + at, D.v + at, mine, int(split) * WAVES + int(wave),
+                                         D.splits * WAVES);
     Running<C / 32> run;
-    const int step = D.splits * WAVES;
-    int i = int(split) * WAVES + int(wave) - step, buffer = BUFFERS - 1;
-    if (i + step < tiles.tiles)
-        fetch(i + step, lds[wave][0][0]);
-    const auto next = [&]() {
-        wave_order();
-        if (BUFFERS == 1 && i >= 0 && i + step < tiles.tiles)
-            fetch(i + step, lds[wave][0][0]);
-        i += step;
-        if (i >= tiles.tiles)
-            return false;
-        wait_tiles();
-        wave_order();
-        buffer = (buffer + 1) % BUFFERS;
-        if (BUFFERS == 2 && i + step < tiles.tiles)
-            fetch(i + step, lds[wave][(buffer + 1) % BUFFERS][0]);
-        return true;
-    };
-    attend_tiles<T, C, KEYS>(A, q, col.position, run, next, [&]() {
-        const int first = tiles.first(i), rows = tiles.rows(i);
-        return TileView{lds[wave][buffer][0], lds[wave][buffer][1], first, rows,
-                        rows < KEYS || how_seen(A, mine.low, mine.high, first, rows) != Seen::all};
-    });
+    walk.begin();
+    attend_tiles<T, C, KEYS>(A, q, col.position, run, walk);
 
     // the waves' sums relative to the largest of their maxima
     const int half = lane >> 5, c = lane & 31;

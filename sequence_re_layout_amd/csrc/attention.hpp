@@ -41,31 +41,15 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 template <typename T> struct Of;
 template <> struct Of<__bf16> {
-    static constexpr uint32_t exponent = 0x7f807f80u, carry = 0x00800080u, top = 0x80008000u;
     typedef __bf16 x8 __attribute__((ext_vector_type(8)));
 };
 template <> struct Of<_Float16> {
-    static constexpr uint32_t exponent = 0x7c007c00u, carry = 0x04000400u, top = 0x80008000u;
     typedef _Float16 x8 __attribute__((ext_vector_type(8)));
 };
 template <> struct Of<float> {
-    static constexpr uint32_t exponent = 0x7f800000u, carry = 0x00800000u, top = 0x80000000u;
     typedef float x8 __attribute__((ext_vector_type(8)));
 };
 template <typename T> using Vec8 = typename Of<T>::x8;
-
-// Whether one of the numbers is infinite or NaN (its exponent is all ones).
-template <typename T>
-__device__ inline bool wild(Vec8<T> x)
-{
-    typedef uint32_t words __attribute__((ext_vector_type(sizeof(T) * 2)));
-    const words w = __builtin_bit_cast(words, x);
-    uint32_t any = 0;
-#pragma unroll
-    for (int i = 0; i < int(sizeof(T) * 2); ++i)
-        any |= (w[i] & Of<T>::exponent) + Of<T>::carry;
-    return any & Of<T>::top;
-}
 
 __device__ inline f32x16 product(Vec8<__bf16> a, Vec8<__bf16> b, f32x16 c)
 {
@@ -100,6 +84,33 @@ __device__ inline Vec8<T> operand(const f32x16 &c, int s)
     return r;
 }
 
+// sum + 0 * (the numbers): NaN if one of them is infinite or NaN.
+__device__ inline float zeros_of(Vec8<__bf16> x, float sum)
+{
+    typedef __bf16 x2 __attribute__((ext_vector_type(2)));
+    const x2 zero = {};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+        sum = __builtin_amdgcn_fdot2_f32_bf16(x2{x[i], x[i + 1]}, zero, sum, false);
+    return sum;
+}
+__device__ inline float zeros_of(Vec8<_Float16> x, float sum)
+{
+    typedef _Float16 x2 __attribute__((ext_vector_type(2)));
+    const x2 zero = {};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+        sum = __builtin_amdgcn_fdot2(x2{x[i], x[i + 1]}, zero, sum, false);
+    return sum;
+}
+__device__ inline float zeros_of(Vec8<float> x, float sum)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        sum = fmaf(x[i], 0.f, sum);
+    return sum;
+}
+
 // The value of the lane across the wave.
 __device__ inline float other_half(float x)
 {
@@ -112,6 +123,12 @@ __device__ inline float other_half(float x)
 
 typedef __attribute__((address_space(3))) char lds_char;
 
+// The place of an LDS address in the work-group's share.
+__device__ inline uint32_t lds_place(const void *p)
+{
+    return uint32_t(reinterpret_cast<uintptr_t>((lds_char *)const_cast<char *>(static_cast<const char *>(p))));
+}
+
 // `bytes` bytes of memory from an address that is the same for the wave: reads
 // beyond them give zeros.
 __device__ inline u32x4 memory_rows(const void *from, uint32_t bytes)
@@ -121,15 +138,15 @@ __device__ inline u32x4 memory_rows(const void *from, uint32_t bytes)
 }
 
 // BYTES bytes of each lane, `off` bytes into memory, straight to LDS, lane after
-// lane from `to` on.  Written as an instruction, since the compiler would wait
+// lane from place `to` on (lds_place).  Written as an instruction, since the compiler would wait
 // for it before the next transposed read of any part of LDS; it is complete after
 // wait_tiles.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"         // m0 is named so that the compiler sets it anew for itself
 template <int BYTES>
-__device__ inline void copy_to_lds(char *to, u32x4 from, uint32_t off)
+__device__ inline void copy_to_lds(uint32_t to, u32x4 from, uint32_t off)
 {
-    const uint32_t at = scalar(uint32_t(reinterpret_cast<uintptr_t>((lds_char *)to)));
+    const uint32_t at = scalar(to);
     if constexpr (BYTES == 16)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                      :: "s"(at), "v"(off), "s"(from) : "memory", "m0");
@@ -213,8 +230,8 @@ struct Tile {
     // 16-byte chunks at 16-byte addresses go from memory to LDS without passing
     // registers; the loads are complete after wait_tiles and a barrier.
     //
-    // off: the places of a thread's chunks from the first row, the same for every
-    // tile (load_offsets).
+    // place: lds_place(tile).  off: the places of a thread's chunks from the first
+    // row, the same for every tile (load_offsets).
     template <int THREADS, int STEPS>
     static __device__ inline void load_offsets(uint32_t (&off)[STEPS], uint32_t token, int d)
     {
@@ -227,8 +244,8 @@ struct Tile {
     }
 
     template <int THREADS, bool DIRECT, int STEPS>
-    static __device__ inline void load(char *__restrict__ tile, const uint32_t (&off)[STEPS], const char *from, uint32_t token,
-                                       int rows, int d)
+    static __device__ inline void load(char *__restrict__ tile, uint32_t place, const uint32_t (&off)[STEPS], const char *from,
+                                       uint32_t token, int rows, int d)
     {
         static_assert(kBytes == 16 * THREADS * STEPS, "whole rounds of the threads");
         if constexpr (DIRECT) {
@@ -236,7 +253,7 @@ struct Tile {
             const u32x4 rows_of = memory_rows(from, rows * token);
 #pragma unroll
             for (int p = 0; p < STEPS; ++p)
-                copy_to_lds<16>(tile + (p * THREADS + wave * 64) * 16, rows_of, off[p]);
+                copy_to_lds<16>(place + (p * THREADS + wave * 64) * 16, rows_of, off[p]);
         } else {
 #pragma unroll
             for (int p = 0; p < STEPS; ++p) {
@@ -268,11 +285,17 @@ struct Tile {
 // Up to 64 floats straight to LDS by a wave, zeros after n.
 __device__ inline void load_floats(float *to, const float *from, int n)
 {
-    copy_to_lds<4>(reinterpret_cast<char *>(to), memory_rows(from, n * 4), (threadIdx.x & 63) * 4);
+    copy_to_lds<4>(lds_place(to), memory_rows(from, n * 4), (threadIdx.x & 63) * 4);
 }
 
-// The wave's loads to LDS have arrived.
-__device__ inline void wait_tiles() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// The wave's loads to LDS have arrived (vmcnt(0)).  As a builtin, so that the
+// compiler knows that its own loads have, too, and waits for none of them later,
+// when the next tile's are on their way.
+__device__ inline void wait_tiles()
+{
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+    asm volatile("" ::: "memory");
+}
 
 // Eight channels of the row that a lane keeps, zeros after d.
 template <typename T>
@@ -285,31 +308,55 @@ __device__ inline Vec8<T> row_part(const char *row, int c, int d)
         return __builtin_shufflevector(R::chunk(row, c, d), R::chunk(row, c + 4, d), 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// The products of a wave's columns with 32 rows of a tile: C / 16 steps.
-template <typename T, int C, int ROWS>
-__device__ inline f32x16 rows_times(const char *tile, int row0, const Vec8<T> (&columns)[C / 16])
-{
-    typedef Tile<T, C, ROWS> Rows;
-    f32x16 r = product(Rows::along_channels(tile, row0, 0), columns[0], f32x16{});
-#pragma unroll
-    for (int c = 1; c < C / 16; ++c)
-        r = product(Rows::along_channels(tile, row0, c), columns[c], r);
-    return r;
-}
+// A operands of a tile's rows are read a good while before they are used: all of
+// a product's at once, and pinned there (the compiler would read each just before
+// its use and wait for it, 100 cycles and more a time).
+__device__ inline void pin_reads() { __builtin_amdgcn_sched_barrier(0); }
 
-// sums[b] += (32 channels of block b) x (N rows from row0 on of the tile),
-// weighted by p, which holds N / 32 results of 32 rows.
-template <typename T, int C, int ROWS, int N, int BLOCKS>
-__device__ inline void add_rows(f32x16 (&sums)[BLOCKS], const char *tile, int row0, const f32x16 (&p)[N / 32])
-{
+// Operands of the scores of 32 rows from row0 on, and the scores: the products of
+// a wave's columns with these rows.
+template <typename T, int C, int ROWS>
+struct RowOperands {
+    Vec8<T> a[C / 16];
+
+    __device__ inline void read(const char *tile, int row0)
+    {
 #pragma unroll
-    for (int s = 0; s < N / 16; ++s) {
-        const Vec8<T> weights = operand<T>(p[s / 2], s % 2);
-#pragma unroll
-        for (int b = 0; b < BLOCKS; ++b)
-            sums[b] = product(Tile<T, C, ROWS>::along_rows(tile, row0 + 16 * s, b), weights, sums[b]);
+        for (int c = 0; c < C / 16; ++c)
+            a[c] = Tile<T, C, ROWS>::along_channels(tile, row0, c);
     }
-}
+    __device__ inline f32x16 times(const Vec8<T> (&columns)[C / 16]) const
+    {
+        f32x16 r = product(a[0], columns[0], f32x16{});
+#pragma unroll
+        for (int c = 1; c < C / 16; ++c)
+            r = product(a[c], columns[c], r);
+        return r;
+    }
+};
+
+// Operands of the sums over 32 rows from row0 on, and the sums: sums[b] += (32
+// channels of block b) x (rows), weighted by p, in two steps of 16 rows.
+template <typename T, int C, int ROWS>
+struct SumOperands {
+    Vec8<T> a[2][C / 32];
+
+    __device__ inline void read(const char *tile, int row0)
+    {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int b = 0; b < C / 32; ++b)
+                a[s][b] = Tile<T, C, ROWS>::along_rows(tile, row0 + 16 * s, b);
+    }
+    __device__ inline void add(f32x16 (&sums)[C / 32], int s, const f32x16 &p) const
+    {
+        const Vec8<T> weights = operand<T>(p, s);
+#pragma unroll
+        for (int b = 0; b < C / 32; ++b)
+            sums[b] = product(a[s][b], weights, sums[b]);
+    }
+};
 
 // Where some rows are hidden from some columns, their weight is 0, and a product
 // of 0 and an infinity or NaN would be NaN.  So rows with such numbers
@@ -319,12 +366,12 @@ __device__ inline void add_rows(f32x16 (&sums)[BLOCKS], const char *tile, int ro
 template <typename T, int C, int ROWS, int N>
 __device__ inline bool wild_rows(const char *tile, int row0)
 {
-    bool any = false;
+    float sum = 0.f;
 #pragma unroll
     for (uint32_t i = 0; i < N * Tile<T, C, ROWS>::kRow / 1024; i += sizeof(T) / 2)
-        any |= wild<T>(*reinterpret_cast<const Vec8<T> *>(tile + row0 * Tile<T, C, ROWS>::kRow + i * 1024 +
-                                                          (threadIdx.x & 63) * 8 * sizeof(T)));
-    return __ballot(any);
+        sum = zeros_of(*reinterpret_cast<const Vec8<T> *>(tile + row0 * Tile<T, C, ROWS>::kRow + i * 1024 +
+                                                          (threadIdx.x & 63) * 8 * sizeof(T)), sum);
+    return __ballot(sum != 0.f);
 }
 
 template <typename T, int C, int ROWS, int N, int BLOCKS>
@@ -387,17 +434,25 @@ __device__ inline Sequence sequence_of(const AttendShape &A, uint32_t shard)
     return s;
 }
 
-// The keys that a position sees are those up to `last` which come after
-// `before` or are among the first ones.
+// The keys from `first` on that a position sees, of those below `end`: offsets up
+// to `last`, which come after `before` or are below `firsts`.
 struct Sight {
     int last, before, firsts;
 
-    // Of the keys below `end`.
-    __device__ inline Sight(const AttendShape &A, int position, int end)
-        : last(position < end ? position : end - 1), before(position - A.reach), firsts(A.firsts)
+    __device__ inline Sight(const AttendShape &A, int position, int first, int end)
+        : last((position < end ? position : end - 1) - first), before(position - A.reach - first), firsts(A.firsts - first)
     {
     }
-    __device__ inline bool operator()(int key) const { return (key <= last) & ((key > before) | (key < firsts)); }
+    __device__ inline bool operator()(int at) const { return (at <= last) & ((at > before) | (at < firsts)); }
+    // Moved on by n keys.
+    __device__ inline Sight at(int n) const
+    {
+        Sight s = *this;
+        s.last -= n;
+        s.before -= n;
+        s.firsts -= n;
+        return s;
+    }
 };
 
 // Tiles of keys that positions [low, high] see, KEYS each: first those of the
@@ -446,6 +501,105 @@ struct Span {
         low = low < 0 ? 0 : low;
         high = high < s.length ? high : s.length - 1;
     }
+};
+
+// A work-group's way through its tiles of keys and values: two of them in LDS, of
+// which the next one is on its way while one is used.  What a wave does with a
+// tile follows from the tile's number, and addresses go on by additions: few
+// scalar instructions a tile, since a wave runs them one after another and none
+// beside its vector ones.  A tile is used in parts of PART keys.
+template <typename T, int C, int KEYS, int PART, int THREADS, bool DIRECT>
+struct KeyWalk {
+    typedef Tile<T, C, KEYS> Keys;
+    char *lds;                                  // [2][2][Keys::kBytes]
+    uint32_t place, token, off[Keys::kBytes / 16 / THREADS];
+    int d, sinks, tiles, window, end;           // sinks: tiles of them
+    int use_from, use_to, all_from, all_to;     // tiles of the window of which the wave sees some keys, and all
+    bool idle;                                  // the wave sees none at all
+    const char *k, *v;                          // of the next tile to fetch
+    int64_t back, step;                         // from the sinks' last tile to the window's first; from tile to tile
+    int fetched, fetch_left;                    // its number, and keys from it on in the sinks or the window
+    int i, first, left, part;                   // of the tile in use
+
+    __device__ inline KeyWalk(const AttendShape &A, char *lds_, const char *keys, const char *values, const Span &all,
+                              const Span &mine)
+        : lds(lds_), place(lds_place(lds_)), token(A.kv_token), d(A.d), k(keys), v(values)
+    {
+        Keys::template load_offsets<THREADS>(off, token, d);
+        const KeyTiles<KEYS> t(A, all.low, all.high);
+        sinks = t.sink_tiles;
+        tiles = t.tiles;
+        window = t.window;
+        end = t.end;
+        idle = mine.low > mine.high;
+        // tile n of the window begins at key window + n * KEYS; where it begins
+        // before the last sink, a wave sees keys before its own window
+        const int behind = window < A.firsts ? 0 : mine.low - A.reach + 1 - window;
+        const int ahead = mine.high - A.reach + 1 - window;
+        use_from = sinks + (behind > 0 ? behind / KEYS : 0);
+        use_to = sinks + (mine.high - window) / KEYS;
+        all_from = sinks + (ahead > 0 ? (ahead + KEYS - 1) / KEYS : 0);
+        all_to = sinks + (mine.low + 1 - window) / KEYS - 1;
+        step = int64_t{KEYS} * token;
+        back = (int64_t{window} - int64_t{sinks - 1} * KEYS) * token;
+        first = sinks ? 0 : window;
+        left = sinks ? t.sinks_end : end - window;
+        k += int64_t{first} * token;
+        v += int64_t{first} * token;
+    }
+
+    // The first tile on its way.
+    __device__ inline void begin()
+    {
+        fetched = 0;
+        fetch_left = left;
+        i = -1;
+        part = KEYS / PART;
+        if (tiles)
+            fetch();
+    }
+
+    __device__ inline void fetch()
+    {
+        const int rows = fetch_left < KEYS ? fetch_left : KEYS, buffer = (fetched & 1) * 2 * Keys::kBytes;
+        Keys::template load<THREADS, DIRECT>(lds + buffer, place + buffer, off, k, token, rows, d);
+        Keys::template load<THREADS, DIRECT>(lds + buffer + Keys::kBytes, place + buffer + Keys::kBytes, off, v, token, rows, d);
+        ++fetched;
+        const bool turn = fetched == sinks;
+        k += turn ? back : step;
+        v += turn ? back : step;
+        fetch_left = turn ? end - window : fetch_left - KEYS;
+    }
+
+    // On to the next keys that some column of the wave sees.
+    __device__ inline bool next()
+    {
+        if (KEYS > PART && ++part < KEYS / PART && left > part * PART)
+            return true;
+        part = 0;
+        for (;;) {
+            if (++i >= tiles)
+                return false;
+            if (i) {
+                first = i == sinks ? window : first + KEYS;
+                left = i == sinks ? end - window : left - KEYS;
+            }
+            wait_tiles();
+            lds_barrier();          // the tile is there, and the one before is no longer read
+            if (fetched < tiles)
+                fetch();
+            if (!idle & ((i < sinks) | ((i >= use_from) & (i <= use_to))))
+                return true;
+        }
+    }
+    __device__ inline const char *keys() const { return lds + (i & 1) * 2 * Keys::kBytes; }
+    __device__ inline const char *values() const { return keys() + Keys::kBytes; }
+    __device__ inline int row0() const { return KEYS > PART ? part * PART : 0; }
+    __device__ inline int key() const { return first + row0(); }
+    // One after the last key of the tile.
+    __device__ inline int key_end() const { return first + (left < KEYS ? left : KEYS); }
+    // Whether some of the tile's keys are hidden from some columns.
+    __device__ inline bool hides() const { return i < sinks ? left < KEYS : (i < all_from) | (i > all_to); }
 };
 
 // A lane's column: a query and a head of the key head's group.

@@ -46,9 +46,9 @@ struct AttendGradDesc {
 template <typename T, int C, bool DIRECT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_kernel(const AttendGradDesc D)
 {
-    constexpr int KEYS = sizeof(T) == 2 ? 64 : 32, PARTS = KEYS / 32;
+    constexpr int KEYS = sizeof(T) == 2 ? 64 : 32;
     typedef Tile<T, C, KEYS> Keys;
-    __shared__ __attribute__((aligned(16))) char lds[2][2][Keys::kBytes];
+    __shared__ __attribute__((aligned(16))) char lds[4 * Keys::kBytes];
     const AttendShape &A = D.shape;
     const uint32_t group = by_xcd(blockIdx.x, gridDim.x), pair = fastdiv(group, D.by_blocks);
     const uint32_t block = D.blocks - 1 - (group - pair * D.blocks);       // long rows first
@@ -63,70 +63,47 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
     const float lse = col.live ? D.lse[col.row(A, shard)] * kLog2e : 0.f;
 
     const Span all(A, seq, first, kTileColumns), mine(A, seq, first + wave * 32, 32);
-    const KeyTiles<KEYS> tiles(A, all.low, all.high);
-
-    const char *const k = D.k + shard * A.kv_shard + key_head * A.kv_head;
-    const char *const v = D.v + shard * A.kv_shard + key_head * A.kv_head;
-    uint32_t off[Keys::kBytes / 16 / kThreads];
-    Keys::template load_offsets<kThreads>(off, A.kv_token, A.d);
-    const auto fetch = [&](int i, char *to) {
-        const int64_t at = int64_t{tiles.first(i)} * A.kv_token;
-        Keys::template load<kThreads, DIRECT>(to, off, k + at, A.kv_token, tiles.rows(i), A.d);
-        Keys::template load<kThreads, DIRECT>(to + Keys::kBytes, off, v + at, A.kv_token, tiles.rows(i), A.d);
-    };
-    // on to the next 32 keys that some column of the wave sees
-    int u = -1;
-    Seen seen;
-    const auto next = [&]() {
-        for (++u; u < tiles.tiles * PARTS; ++u) {
-            const int j = u / PARTS, t = u % PARTS, rows = tiles.rows(j) - 32 * t;
-            if (t == 0) {
-                wait_tiles();
-                lds_barrier();
-                if (j + 1 < tiles.tiles)
-                    fetch(j + 1, lds[~j & 1][0]);
-            }
-            seen = rows > 0 ? how_seen(A, mine.low, mine.high, tiles.first(j) + 32 * t, rows < 32 ? rows : 32) : Seen::none;
-            if (seen != Seen::none)
-                return true;
-        }
-        return false;
-    };
-    // P and dP of these keys; P is 0 where a key is hidden
-    const auto weigh = [&](f32x16 &p, f32x16 &dp) {
-        const int j = u / PARTS, t = u % PARTS, from = tiles.first(j) + 32 * t, rows = tiles.rows(j) - 32 * t;
-        p = rows_times<T, C, KEYS>(lds[j & 1][0], 32 * t, q);
-        dp = rows_times<T, C, KEYS>(lds[j & 1][1], 32 * t, g);
+    const int64_t at = shard * A.kv_shard + key_head * A.kv_head;
+    KeyWalk<T, C, KEYS, 32, kThreads, DIRECT> walk(A, lds, D.k + at, D.v + at, all, mine);
+    // P and dP of the next 32 keys; P is 0 where a key is hidden
+    const auto weigh = [&](const auto &at, f32x16 &p, f32x16 &dp) {
+        RowOperands<T, C, KEYS> keys, values;
+        keys.read(at.keys(), at.row0());
+        pin_reads();
+        values.read(at.values(), at.row0());
+        p = keys.times(q);
+        pin_reads();
+        dp = values.times(g);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], A.scale_log2, -lse));
-        const bool part = seen == Seen::some || rows < 32;
-        if (part) {
-            const Sight sees(A, col.position, from + rows);
+        const bool hides = at.hides();
+        if (hides) {
+            const Sight sees(A, col.position, at.key() + 4 * half, at.key_end());
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const bool is = sees(from + row_of(i, half));
+                const bool is = sees(row_of(i, 0));
                 p[i] = is ? p[i] : 0.f;
                 dp[i] = is ? dp[i] : 0.f;
             }
         }
-        return part;
+        return hides;
     };
 
     // delta = <dO, O> = sum P dP.  O has been rounded to its type, which shows
     // where a row sees few keys: there delta is summed first, in fp32.
     float delta = 0.f;
-    if (tiles.tiles <= kFewTiles) {
-        if (tiles.tiles)
-            fetch(0, lds[0][0]);
-        while (next()) {
+    if (walk.tiles <= kFewTiles) {
+        auto once = walk;
+        once.begin();
+        wait_tiles();
+        while (once.next()) {
             f32x16 p, dp;
-            weigh(p, dp);
+            weigh(once, p, dp);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 delta = fmaf(p[i], dp[i], delta);
         }
-        u = -1;
         lds_barrier();
     } else if (col.live) {
         const char *const o = D.o + col.at(A, shard);
@@ -150,28 +127,31 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             sums[b][i] = 0.f;
-    if (tiles.tiles)
-        fetch(0, lds[0][0]);
-    bool more = next();
+    walk.begin();
+    wait_tiles();                   // for the columns, too, and on every way into the loop
+    bool more = walk.next();
     while (more) {
         f32x16 ds[1];
         for (;;) {
             f32x16 dp;
-            const bool part = weigh(ds[0], dp);
+            const bool hides = weigh(walk, ds[0], dp);
+            SumOperands<T, C, KEYS> operands;
+            operands.read(walk.keys(), walk.row0());
+            pin_reads();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 ds[0][i] *= dp[i] - delta;
-            const char *const keys = lds[u / PARTS & 1][0];
-            if (part && wild_rows<T, C, KEYS, 32>(keys, u % PARTS * 32))
+            if (hides && wild_rows<T, C, KEYS, 32>(walk.keys(), walk.row0()))
                 break;
-            add_rows<T, C, KEYS, 32>(sums, keys, u % PARTS * 32, ds);
-            more = next();
+            operands.add(sums, 0, ds[0]);
+            operands.add(sums, 1, ds[0]);
+            more = walk.next();
             if (!more)
                 break;
         }
         if (more) {
-            add_wild_rows<T, C, KEYS, 32>(sums, lds[u / PARTS & 1][0], u % PARTS * 32, ds);
-            more = next();
+            add_wild_rows<T, C, KEYS, 32>(sums, walk.keys(), walk.row0(), ds);
+            more = walk.next();
         }
     }
     if (!col.exists)
@@ -207,16 +187,117 @@ __device__ inline void store_key(const AttendShape &A, char *to, uint32_t shard,
     }
 }
 
+// A work-group's way through the queries [begin, end) of each head of a group and
+// their gradients, as KeyWalk's through keys: tiles of ROWS in LDS, with lse and
+// delta of each, used in parts of 32.
+template <typename T, int C, int ROWS, bool DIRECT>
+struct QueryWalk {
+    typedef Tile<T, C, ROWS> Rows;
+    char *lds;                                  // [2][2][Rows::kBytes]
+    float *lds_rows;                            // [2][2][64]
+    uint32_t place, token, off[Rows::kBytes / 16 / kThreads];
+    int d, count, tiles, all;                   // queries, and tiles of a head and of all heads
+    int use_from, use_to, all_from, all_to;     // parts of a head in which some query sees some of the wave's keys, and all all
+    int start;                                  // position of the first query
+    const char *q, *g;                          // of the next tile to fetch
+    const float *numbers;                       // lse (first wave) or delta (second) of its first query
+    int64_t step, turn;                         // from tile to tile, and from a head's last to the next one's first
+    int queries, fetched, fetch_left;
+    int i, in_head, left, part;
+
+    __device__ inline QueryWalk(const AttendShape &A, char *lds_, float *lds_rows_, const AttendGradDesc &D, int64_t at, int64_t row,
+                                int first_position, int begin, int end, int key)
+        : lds(lds_), lds_rows(lds_rows_), place(lds_place(lds_)), token(A.q_token), d(A.d)
+    {
+        Rows::template load_offsets<kThreads>(off, token, d);
+        count = end - begin;
+        tiles = count > 0 ? (count + ROWS - 1) / ROWS : 0;
+        all = tiles * A.ratio;
+        start = first_position + begin;
+        queries = A.queries;
+        // part n of a head holds positions start + 32 * n to start + 32 * n + 31, the
+        // wave keys `key` to key + 31
+        use_from = (key - 31 - start + 31) >> 5;
+        use_to = key < A.firsts ? 0x7fffffff : (A.reach - 1 + key + 31 - start) >> 5;
+        all_from = (key + 31 - start + 31) >> 5;
+        all_to = key + 31 < A.firsts ? 0x7fffffff : (A.reach - 1 + key - 31 - start) >> 5;
+        step = int64_t{ROWS} * token;
+        turn = A.q_head - int64_t{tiles - 1} * step;
+        q = D.q + at + int64_t{begin} * token;
+        g = D.dout + at + int64_t{begin} * token;
+        numbers = D.rows + scalar(threadIdx.x >> 6) * D.lse_elems + row + begin;
+    }
+    __device__ inline void begin()
+    {
+        fetched = 0;
+        fetch_left = count;
+        i = -1;
+        in_head = -1;
+        left = 0;
+        part = ROWS / 32;
+        if (all)
+            fetch();
+    }
+    __device__ inline void fetch()
+    {
+        const int rows = fetch_left < ROWS ? fetch_left : ROWS, buffer = fetched & 1, at = buffer * 2 * Rows::kBytes;
+        Rows::template load<kThreads, DIRECT>(lds + at, place + at, off, q, token, rows, d);
+        Rows::template load<kThreads, DIRECT>(lds + at + Rows::kBytes, place + at + Rows::kBytes, off, g, token, rows, d);
+        const uint32_t wave = scalar(threadIdx.x >> 6);
+        if (wave < 2)
+            load_floats(lds_rows + (buffer * 2 + wave) * 64, numbers, rows);
+        ++fetched;
+        const bool last = fetch_left <= ROWS;
+        q += last ? turn : step;
+        g += last ? turn : step;
+        numbers += last ? queries - (tiles - 1) * ROWS : ROWS;
+        fetch_left = last ? count : fetch_left - ROWS;
+    }
+    // On to the next 32 queries of which some see some key of the wave.
+    __device__ inline bool next()
+    {
+        for (;;) {
+            if (ROWS > 32 && ++part < ROWS / 32 && left > part * 32) {
+                ++in_head;
+            } else {
+                part = 0;
+                if (++i >= all)
+                    return false;
+                left -= ROWS;
+                ++in_head;
+                if (left <= 0) {
+                    left = count;
+                    in_head = 0;
+                }
+                wait_tiles();
+                lds_barrier();
+                if (fetched < all)
+                    fetch();
+            }
+            if ((in_head >= use_from) & (in_head <= use_to))
+                return true;
+        }
+    }
+    __device__ inline const char *queries_at() const { return lds + (i & 1) * 2 * Rows::kBytes; }
+    __device__ inline const char *grads() const { return queries_at() + Rows::kBytes; }
+    __device__ inline int row0() const { return ROWS > 32 ? part * 32 : 0; }
+    __device__ inline int position() const { return start + 32 * in_head; }
+    __device__ inline int rows() const { return left - row0(); }
+    __device__ inline const float *lse() const { return lds_rows + (i & 1) * 128 + row0(); }
+    __device__ inline const float *delta() const { return lse() + 64; }
+    __device__ inline bool hides() const { return (in_head < all_from) | (in_head > all_to) | (rows() < 32); }
+};
+
 // 128 keys a work-group, 32 a wave, and a chunk of the queries that see them,
 // head by head of the group: tiles of 64 queries (32 in fp32) and their
 // gradients go through LDS, the next one on its way while one is used.
 template <typename T, int C, bool DIRECT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && C <= 64 ? 2 : 1) void attend_dkv_kernel(const AttendGradDesc D)
 {
-    constexpr int ROWS = sizeof(T) == 2 ? 64 : 32, PARTS = ROWS / 32;
+    constexpr int ROWS = sizeof(T) == 2 ? 64 : 32;
     typedef Tile<T, C, ROWS> Rows;
-    __shared__ __attribute__((aligned(16))) char lds[2][2][Rows::kBytes];
-    __shared__ __attribute__((aligned(16))) float lds_rows[2][2][64];
+    __shared__ __attribute__((aligned(16))) char lds[4 * Rows::kBytes];
+    __shared__ __attribute__((aligned(16))) float lds_rows[2 * 2 * 64];
     const AttendShape &A = D.shape;
     const uint32_t group = by_xcd(blockIdx.x, gridDim.x), pair = fastdiv(group, D.by_items), item = group - pair * D.items;
     const uint32_t shard = fastdiv(pair, A.by_heads), key_head = pair - shard * A.Hl_kv;
@@ -250,83 +331,58 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && C <= 64 ? 2 : 1) void a
     const int length = sinks ? D.sink_chunk : D.chunk;
     begin += part * length;
     end = end < begin + length ? end : begin + length;
-    const int tiles = end > begin ? (end - begin + ROWS - 1) / ROWS : 0, all = tiles * A.ratio;
-
-    uint32_t off[Rows::kBytes / 16 / kThreads];
-    Rows::template load_offsets<kThreads>(off, A.q_token, A.d);
-    const auto fetch = [&](int head, int tile, int buffer) {
-        char *const to = lds[buffer][0];
-        const int from = begin + tile * ROWS, rows = end - from < ROWS ? end - from : ROWS;
-        const uint32_t q_head = key_head * A.ratio + head;
-        const int64_t at = shard * A.q_shard + q_head * A.q_head + int64_t{from} * A.q_token;
-        Rows::template load<kThreads, DIRECT>(to, off, D.q + at, A.q_token, rows, A.d);
-        Rows::template load<kThreads, DIRECT>(to + Rows::kBytes, off, D.dout + at, A.q_token, rows, A.d);
-        if (wave < 2)
-            load_floats(lds_rows[buffer][wave], D.rows + wave * D.lse_elems + (int64_t{shard} * A.Hl_q + q_head) * A.queries + from,
-                        rows);
-    };
-    if (all)
-        fetch(0, 0, 0);
-    // on to the next 32 queries that see some key of the wave
-    int u = -1, at = 0, tile = 0, head = 0;
-    Seen seen;
-    const auto next = [&]() {
-        for (++u; u < all * PARTS; ++u) {
-            const int j = u / PARTS, t = u % PARTS;
-            if (t == 0) {
-                wait_tiles();
-                lds_barrier();
-                at = begin + tile * ROWS;
-                tile = tile + 1 < tiles ? tile + 1 : 0;
-                head += tile == 0;
-                if (j + 1 < all)
-                    fetch(head, tile, ~j & 1);
-            } else {
-                at += 32;
-            }
-            const int low = seq.start + at, high = seq.start + (at + 32 < end ? at + 32 : end) - 1;
-            seen = how_seen(A, low, high, wave_key, 32);
-            if (seen != Seen::none)
-                return true;
-        }
-        return false;
-    };
-    bool more = next();
+    QueryWalk<T, C, ROWS, DIRECT> walk(A, lds, lds_rows, D, shard * A.q_shard + key_head * A.ratio * A.q_head,
+                                       (int64_t{shard} * A.Hl_q + key_head * A.ratio) * A.queries, seq.start, begin, end, wave_key);
+    walk.begin();
+    wait_tiles();                   // for the keys, too, and on every way into the loop
+    bool more = walk.next();
     while (more) {
         f32x16 p[1], ds[1];
         for (;;) {
-            const int buffer = u / PARTS & 1, row0 = u % PARTS * 32, rows = end - at;
-            const char *const queries = lds[buffer][0], *const grads = lds[buffer][1];
-            p[0] = rows_times<T, C, ROWS>(queries, row0, k);
-            ds[0] = rows_times<T, C, ROWS>(grads, row0, v);
+            const char *const queries = walk.queries_at(), *const grads = walk.grads();
+            const int row0 = walk.row0();
+            RowOperands<T, C, ROWS> of_queries, of_grads;
+            SumOperands<T, C, ROWS> operands;
+            of_queries.read(queries, row0);
+            pin_reads();
+            of_grads.read(grads, row0);
+            p[0] = of_queries.times(k);
+            pin_reads();
+            ds[0] = of_grads.times(v);
+            operands.read(grads, row0);
+            pin_reads();
+            const float *const lse = walk.lse() + 4 * half, *const delta = walk.delta() + 4 * half;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int row = row0 + row_of(i, half);
-                p[0][i] = __builtin_amdgcn_exp2f(fmaf(p[0][i], A.scale_log2, -lds_rows[buffer][0][row]));
-                ds[0][i] = p[0][i] * (ds[0][i] - lds_rows[buffer][1][row]);
+                p[0][i] = __builtin_amdgcn_exp2f(fmaf(p[0][i], A.scale_log2, -lse[row_of(i, 0)]));
+                ds[0][i] = p[0][i] * (ds[0][i] - delta[row_of(i, 0)]);
             }
-            const bool part = seen == Seen::some || rows < 32;
-            if (part) {
+            if (walk.hides()) {
+                // the rows from `first` on that see the key: up to `last`
+                const int first = walk.position() + 4 * half, from = key - first, rows = walk.rows() - 4 * half;
+                const int last = key < A.firsts ? rows - 1 : key + A.reach - 1 - first < rows - 1 ? key + A.reach - 1 - first : rows - 1;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int row = row_of(i, half);
-                    const bool is = (row < rows) & Sight(A, seq.start + at + row, A.S)(key);
+                    const bool is = (row_of(i, 0) >= from) & (row_of(i, 0) <= last);
                     p[0][i] = is ? p[0][i] : 0.f;
                     ds[0][i] = is ? ds[0][i] : 0.f;
                 }
                 if (wild_rows<T, C, ROWS, 32>(queries, row0) || wild_rows<T, C, ROWS, 32>(grads, row0))
                     break;
             }
-            add_rows<T, C, ROWS, 32>(dv, grads, row0, p);
-            add_rows<T, C, ROWS, 32>(dk, queries, row0, ds);
-            more = next();
+            operands.add(dv, 0, p[0]);
+            operands.add(dv, 1, p[0]);
+            operands.read(queries, row0);
+            operands.add(dk, 0, ds[0]);
+            operands.add(dk, 1, ds[0]);
+            more = walk.next();
             if (!more)
                 break;
         }
         if (more) {
-            add_wild_rows<T, C, ROWS, 32>(dv, lds[u / PARTS & 1][1], u % PARTS * 32, p);
-            add_wild_rows<T, C, ROWS, 32>(dk, lds[u / PARTS & 1][0], u % PARTS * 32, ds);
-            more = next();
+            add_wild_rows<T, C, ROWS, 32>(dv, walk.grads(), walk.row0(), p);
+            add_wild_rows<T, C, ROWS, 32>(dk, walk.queries_at(), walk.row0(), ds);
+            more = walk.next();
         }
     }
     if ((sinks ? D.sink_chunks : D.chunks) == 1) {
