@@ -90,6 +90,7 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
         for (;;) {
             const char *const keys = walk.keys(), *const values = walk.values();
             const bool hides = walk.hides();
+            wild = hides && wild_rows<T, C, ROWS, ROWS>(values, 0);
             RowOperands<T, C, ROWS> rows[TILES];
             SumOperands<T, C, ROWS> sums[TILES];
             rows[0].read(keys, 0);
@@ -121,7 +122,6 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
             behind = __ballot(most > run.m + A.slack);
             if (behind)
                 break;
-            wild = hides && wild_rows<T, C, ROWS, ROWS>(values, 0);
             if (wild)
                 break;
             // weights and their products in steps of 16 keys: exponentials are

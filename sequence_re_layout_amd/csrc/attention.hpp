@@ -123,6 +123,16 @@ __device__ inline float other_half(float x)
 
 typedef __attribute__((address_space(3))) char lds_char;
 
+// The lane's number, of which the compiler does not know that it is the same in
+// every step: addresses made of it are computed where they are used instead of
+// being kept in registers.
+__device__ inline uint32_t lane_here()
+{
+    uint32_t lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // The place of an LDS address in the work-group's share.
 __device__ inline uint32_t lds_place(const void *p)
 {
@@ -171,9 +181,9 @@ struct Tile {
     }
 
     // The A operand of scores: row `row0` + lane % 32, channels 16*s on.
-    static __device__ inline Vec8<T> along_channels(const char *tile, int row0, int s)
+    static __device__ inline Vec8<T> along_channels(const char *tile, int row0, int s, uint32_t lane = threadIdx.x & 63)
     {
-        const uint32_t lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
+        const uint32_t r = lane & 31, half = lane >> 5;
         const char *const at = tile + (row0 + r) * kRow;
         if constexpr (sizeof(T) == 2) {
             const uint32_t c = (2 * s) ^ (half ^ swizzle(r));
@@ -188,9 +198,9 @@ struct Tile {
 
     // The A operand of sums over rows: channel 32*block + lane % 32 of the slots
     // of the 16 rows from row0 on.
-    static __device__ inline Vec8<T> along_rows(const char *tile, int row0, int block)
+    static __device__ inline Vec8<T> along_rows(const char *tile, int row0, int block, uint32_t lane = threadIdx.x & 63)
     {
-        const uint32_t lane = threadIdx.x & 63, half = lane >> 5;
+        const uint32_t half = lane >> 5;
         if constexpr (sizeof(T) == 2) {
             // 16 lanes read four rows of 16 channels, four channels each, and
             // receive a channel each of the four rows
@@ -325,9 +335,9 @@ struct RowOperands {
         for (int c = 0; c < C / 16; ++c)
             a[c] = Tile<T, C, ROWS>::along_channels(tile, row0, c);
     }
-    __device__ inline f32x16 times(const Vec8<T> (&columns)[C / 16]) const
+    __device__ inline f32x16 times(const Vec8<T> (&columns)[C / 16], f32x16 begin = f32x16{}) const
     {
-        f32x16 r = product(a[0], columns[0], f32x16{});
+        f32x16 r = product(a[0], columns[0], begin);
 #pragma unroll
         for (int c = 1; c < C / 16; ++c)
             r = product(a[c], columns[c], r);
@@ -368,9 +378,10 @@ __device__ inline bool wild_rows(const char *tile, int row0)
 {
     float sum = 0.f;
 #pragma unroll
-    for (uint32_t i = 0; i < N * Tile<T, C, ROWS>::kRow / 1024; i += sizeof(T) / 2)
+    for (uint32_t i = 0; i < N * Tile<T, C, ROWS>::kRow / 1024; i += sizeof(T) / 2) {
         sum = zeros_of(*reinterpret_cast<const Vec8<T> *>(tile + row0 * Tile<T, C, ROWS>::kRow + i * 1024 +
                                                           (threadIdx.x & 63) * 8 * sizeof(T)), sum);
+    }
     return __ballot(sum != 0.f);
 }
 

@@ -35,7 +35,7 @@ struct AttendGradDesc {
     const char *q, *k, *v, *o, *dout;
     const float *lse;
     char *dq, *dk, *dv;
-    float *rows, *partials;         // rows: [2][lse_elems], lse in powers of two, and delta
+    float *rows, *partials;         // rows: [2][lse_elems], -lse / scale and -delta
     int64_t lse_elems;
     FastDiv by_blocks, by_items, by_sink_chunks, by_chunks;
     int32_t blocks, items, sink_blocks, sink_chunk, sink_chunks, chunk, chunks, key_blocks;
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
     Vec8<T> q[C / 16], g[C / 16];
     load_column<T, C, DIRECT>(A, D.q + col.at(A, shard), col.live, q);
     load_column<T, C, DIRECT>(A, D.dout + col.at(A, shard), col.live, g);
-    const float lse = col.live ? D.lse[col.row(A, shard)] * kLog2e : 0.f;
+    const float lse_at = col.live ? D.lse[col.row(A, shard)] : 0.f, lse = lse_at * kLog2e;
 
     const Span all(A, seq, first, kTileColumns), mine(A, seq, first + wave * 32, 32);
     const int64_t at = shard * A.kv_shard + key_head * A.kv_head;
@@ -77,8 +77,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], A.scale_log2, -lse));
-        const bool hides = at.hides();
-        if (hides) {
+        if (at.hides()) {
             const Sight sees(A, col.position, at.key() + 4 * half, at.key_end());
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -87,7 +86,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
                 dp[i] = is ? dp[i] : 0.f;
             }
         }
-        return hides;
     };
 
     // delta = <dO, O> = sum P dP.  O has been rounded to its type, which shows
@@ -117,8 +115,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
     }
     delta += other_half(delta);
     if (col.live && half == 0) {
-        D.rows[col.row(A, shard)] = lse;
-        D.rows[D.lse_elems + col.row(A, shard)] = delta;
+        D.rows[col.row(A, shard)] = -lse_at / A.scale;
+        D.rows[D.lse_elems + col.row(A, shard)] = -delta;
     }
 
     f32x16 sums[C / 32];
@@ -134,14 +132,15 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_ke
         f32x16 ds[1];
         for (;;) {
             f32x16 dp;
-            const bool hides = weigh(walk, ds[0], dp);
+            const bool wild = walk.hides() && wild_rows<T, C, KEYS, 32>(walk.keys(), walk.row0());
+            weigh(walk, ds[0], dp);
             SumOperands<T, C, KEYS> operands;
             operands.read(walk.keys(), walk.row0());
             pin_reads();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 ds[0][i] *= dp[i] - delta;
-            if (hides && wild_rows<T, C, KEYS, 32>(walk.keys(), walk.row0()))
+            if (wild)
                 break;
             operands.add(sums, 0, ds[0]);
             operands.add(sums, 1, ds[0]);
@@ -188,8 +187,9 @@ __device__ inline void store_key(const AttendShape &A, char *to, uint32_t shard,
 }
 
 // A work-group's way through the queries [begin, end) of each head of a group and
-// their gradients, as KeyWalk's through keys: tiles of ROWS in LDS, with lse and
-// delta of each, used in parts of 32.
+// their gradients, as KeyWalk's through keys: tiles of ROWS in LDS, used in parts
+// of 32, with -lse / scale and -delta of each query.  The products begin from
+// these instead of 0, so that P = exp(scale * result) and dS = P * result.
 template <typename T, int C, int ROWS, bool DIRECT>
 struct QueryWalk {
     typedef Tile<T, C, ROWS> Rows;
@@ -200,7 +200,7 @@ struct QueryWalk {
     int use_from, use_to, all_from, all_to;     // parts of a head in which some query sees some of the wave's keys, and all all
     int start;                                  // position of the first query
     const char *q, *g;                          // of the next tile to fetch
-    const float *numbers;                       // lse (first wave) or delta (second) of its first query
+    const float *numbers;                       // -lse / scale (first wave) or -delta (second) of its first query
     int64_t step, turn;                         // from tile to tile, and from a head's last to the next one's first
     int queries, fetched, fetch_left;
     int i, in_head, left, part;
@@ -283,19 +283,41 @@ struct QueryWalk {
     __device__ inline int row0() const { return ROWS > 32 ? part * 32 : 0; }
     __device__ inline int position() const { return start + 32 * in_head; }
     __device__ inline int rows() const { return left - row0(); }
-    __device__ inline const float *lse() const { return lds_rows + (i & 1) * 128 + row0(); }
-    __device__ inline const float *delta() const { return lse() + 64; }
+    // The numbers of the rows of a result's registers.
+    __device__ inline f32x16 numbers_at(int which, int half) const
+    {
+        typedef float x4 __attribute__((ext_vector_type(4)));
+        const float *const from = lds_rows + (i & 1) * 128 + which * 64 + row0() + 4 * half;
+        f32x16 r;
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+            const x4 x = *reinterpret_cast<const x4 *>(from + row_of(j, 0));
+            r[j] = x[0];
+            r[j + 1] = x[1];
+            r[j + 2] = x[2];
+            r[j + 3] = x[3];
+        }
+        return r;
+    }
+    __device__ inline f32x16 lse(int half) const { return numbers_at(0, half); }
+    __device__ inline f32x16 delta(int half) const { return numbers_at(1, half); }
     __device__ inline bool hides() const { return (in_head < all_from) | (in_head > all_to) | (rows() < 32); }
 };
 
 // 128 keys a work-group, 32 a wave, and a chunk of the queries that see them,
-// head by head of the group: tiles of 64 queries (32 in fp32) and their
-// gradients go through LDS, the next one on its way while one is used.
+// head by head of the group: tiles of 64 queries (32 in fp32) and their gradients
+// go through LDS, the next one on its way while one is used.  Where the keys'
+// sums take half of the registers that two waves of a SIMD have (16-bit types,
+// over 64 channels), the values are kept in LDS instead, and tiles are of 32
+// queries to leave room for them.
 template <typename T, int C, bool DIRECT>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && C <= 64 ? 2 : 1) void attend_dkv_kernel(const AttendGradDesc D)
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dkv_kernel(const AttendGradDesc D)
 {
-    constexpr int ROWS = sizeof(T) == 2 ? 64 : 32;
+    constexpr bool VALUES_IN_LDS = sizeof(T) == 2 && C > 64;
+    constexpr int ROWS = sizeof(T) == 2 && !VALUES_IN_LDS ? 64 : 32;
     typedef Tile<T, C, ROWS> Rows;
+    typedef Tile<T, C, kKeyBlock> Values;
+    __shared__ __attribute__((aligned(16))) char lds_values[VALUES_IN_LDS ? Values::kBytes : 16];
     __shared__ __attribute__((aligned(16))) char lds[4 * Rows::kBytes];
     __shared__ __attribute__((aligned(16))) float lds_rows[2 * 2 * 64];
     const AttendShape &A = D.shape;
@@ -310,10 +332,20 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && C <= 64 ? 2 : 1) void a
     const int half = lane >> 5, wave_key = key_block * kKeyBlock + int(wave) * 32, key = wave_key + int(lane & 31);
     const bool exists = key < seq.length;
 
-    Vec8<T> k[C / 16], v[C / 16];
+    Vec8<T> k[C / 16], v[VALUES_IN_LDS ? 1 : C / 16];
     const int64_t at_key = shard * A.kv_shard + key_head * A.kv_head + int64_t{exists ? key : 0} * A.kv_token;
     load_column<T, C, DIRECT>(A, D.k + at_key, exists, k);
-    load_column<T, C, DIRECT>(A, D.v + at_key, exists, v);
+    if constexpr (VALUES_IN_LDS) {
+        const int first = key_block * kKeyBlock, rows = seq.length - first < kKeyBlock ? seq.length - first : kKeyBlock;
+        uint32_t off[Values::kBytes / 16 / kThreads];
+        Values::template load_offsets<kThreads>(off, A.kv_token, A.d);
+        if (rows > 0)
+            Values::template load<kThreads, DIRECT>(lds_values, lds_place(lds_values), off,
+                                                    D.v + shard * A.kv_shard + key_head * A.kv_head + int64_t{first} * A.kv_token,
+                                                    A.kv_token, rows, A.d);
+    } else {
+        load_column<T, C, DIRECT>(A, D.v + at_key, exists, v);
+    }
     f32x16 dk[C / 32], dv[C / 32];
 #pragma unroll
     for (int b = 0; b < C / 32; ++b)
@@ -341,21 +373,67 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && C <= 64 ? 2 : 1) void a
         for (;;) {
             const char *const queries = walk.queries_at(), *const grads = walk.grads();
             const int row0 = walk.row0();
+            const bool wild = walk.hides() && (wild_rows<T, C, ROWS, 32>(queries, row0) || wild_rows<T, C, ROWS, 32>(grads, row0));
+            // Operands are read a stage of products ahead; 32 registers of them
+            // where the values are in LDS, so that nothing is spilled: a register
+            // that comes back from memory would wait for the tile on its way.
+            constexpr int HALF = VALUES_IN_LDS ? C / 32 : 1;
+            Vec8<T> one[HALF], other[HALF];
             RowOperands<T, C, ROWS> of_queries, of_grads;
             SumOperands<T, C, ROWS> operands;
-            of_queries.read(queries, row0);
-            pin_reads();
-            of_grads.read(grads, row0);
-            p[0] = of_queries.times(k);
-            pin_reads();
-            ds[0] = of_grads.times(v);
-            operands.read(grads, row0);
-            pin_reads();
-            const float *const lse = walk.lse() + 4 * half, *const delta = walk.delta() + 4 * half;
+            if constexpr (VALUES_IN_LDS) {
+                const int mine = int(wave) * 32;
+                const uint32_t here = lane_here();
+                f32x16 s = walk.lse(half), dp;
+#pragma unroll
+                for (int c = 0; c < HALF; ++c)
+                    one[c] = Rows::along_channels(queries, row0, c, here);
+                pin_reads();
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) {
+                    s = product(one[c], k[c], s);
+                    one[c] = Rows::along_channels(queries, row0, HALF + c, here);
+                }
+                pin_reads();
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) {
+                    s = product(one[c], k[HALF + c], s);
+                    if (c == 0)
+                        dp = walk.delta(half);
+                    one[c] = Rows::along_channels(grads, row0, c, here);
+                    other[c] = Values::along_channels(lds_values, mine, c, here);
+                }
+                pin_reads();
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) {
+                    dp = product(one[c], other[c], dp);
+                    one[c] = Rows::along_channels(grads, row0, HALF + c, here);
+                    other[c] = Values::along_channels(lds_values, mine, HALF + c, here);
+                }
+                pin_reads();
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) {
+                    dp = product(one[c], other[c], dp);
+                    one[c] = Rows::along_rows(grads, row0, c, here);
+                    other[c] = Rows::along_rows(grads, row0 + 16, c, here);
+                }
+                pin_reads();
+                p[0] = s;
+                ds[0] = dp;
+            } else {
+                of_queries.read(queries, row0);
+                pin_reads();
+                of_grads.read(grads, row0);
+                p[0] = of_queries.times(k, walk.lse(half));
+                pin_reads();
+                ds[0] = of_grads.times(v, walk.delta(half));
+                operands.read(grads, row0);
+                pin_reads();
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                p[0][i] = __builtin_amdgcn_exp2f(fmaf(p[0][i], A.scale_log2, -lse[row_of(i, 0)]));
-                ds[0][i] = p[0][i] * (ds[0][i] - delta[row_of(i, 0)]);
+                p[0][i] = __builtin_amdgcn_exp2f(p[0][i] * A.scale_log2);
+                ds[0][i] *= p[0][i];
             }
             if (walk.hides()) {
                 // the rows from `first` on that see the key: up to `last`
@@ -367,14 +445,37 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && C <= 64 ? 2 : 1) void a
                     p[0][i] = is ? p[0][i] : 0.f;
                     ds[0][i] = is ? ds[0][i] : 0.f;
                 }
-                if (wild_rows<T, C, ROWS, 32>(queries, row0) || wild_rows<T, C, ROWS, 32>(grads, row0))
-                    break;
             }
-            operands.add(dv, 0, p[0]);
-            operands.add(dv, 1, p[0]);
-            operands.read(queries, row0);
-            operands.add(dk, 0, ds[0]);
-            operands.add(dk, 1, ds[0]);
+            if (wild)
+                break;
+            if constexpr (VALUES_IN_LDS) {
+                const uint32_t here = lane_here();
+                const Vec8<T> p0 = operand<T>(p[0], 0), p1 = operand<T>(p[0], 1);
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) {
+                    dv[c] = product(one[c], p0, dv[c]);
+                    one[c] = Rows::along_rows(queries, row0, c, here);
+                }
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) {
+                    dv[c] = product(other[c], p1, dv[c]);
+                    other[c] = Rows::along_rows(queries, row0 + 16, c, here);
+                }
+                pin_reads();
+                const Vec8<T> ds0 = operand<T>(ds[0], 0), ds1 = operand<T>(ds[0], 1);
+#pragma unroll
+                for (int c = 0; c < HALF; ++c)
+                    dk[c] = product(one[c], ds0, dk[c]);
+#pragma unroll
+                for (int c = 0; c < HALF; ++c)
+                    dk[c] = product(other[c], ds1, dk[c]);
+            } else {
+                operands.add(dv, 0, p[0]);
+                operands.add(dv, 1, p[0]);
+                operands.read(queries, row0);
+                operands.add(dk, 0, ds[0]);
+                operands.add(dk, 1, ds[0]);
+            }
             more = walk.next();
             if (!more)
                 break;
