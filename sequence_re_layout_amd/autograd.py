@@ -28,6 +28,15 @@ their gradients in the same way:
   plan's grad_dtype until autograd casts it to the table's):
   ``basp_embed_to_seq_grad``.
 
+What a layer computes between them (include/basp.h, "The rest of a layer"):
+
+* ``attention_qkv(attention_plan, qkv)`` on the fused head-sharded buffer, or
+  ``attention(attention_plan, q, k, v)``; backward: ``basp_attention_grad`` (q,
+  k, v, the output and its lse are kept until then);
+* ``layer_norm(norm_plan, x, weight, bias)``; backward: ``basp_layer_norm_grad``;
+* ``balance_loss(expert_plan, logits, ids)`` returns the loss and the experts'
+  counts; backward, for the scores: ``basp_balance_loss_grad``.
+
 Tensors are contiguous and of the plan's dtype and element counts, as the
 binding checks; outputs are allocated with torch on the inputs' device.  Only
 buffers are marshalled here: every element is moved by the library's kernels.
@@ -252,3 +261,132 @@ def embed_to_seq(plan, ids, table, scale=1.0):
     """Scaled rows [T][D] of the table in the plan's order, with backward for
     the table."""
     return _EmbedToSeq.apply(plan, ids, table, scale)
+
+
+# ------------------------------------- attention, layer norm, balance loss --
+
+def _attention_forward(plan, q, k, v, starts, lengths, scale):
+    o = torch.empty(plan.info["q_elems"], dtype=q.dtype, device=q.device)
+    lse = torch.empty(plan.info["lse_elems"], dtype=torch.float32, device=q.device)
+    b.basp_attention(plan, q, k, v, starts, lengths, scale, o, lse, _workspace(plan, q.device))
+    return o, lse
+
+
+def _attention_grad(plan, q, k, v, o, lse, dout, starts, lengths, scale, dq, dk, dv):
+    ws = torch.empty(plan.info["grad_workspace_bytes"], dtype=torch.uint8, device=q.device)
+    b.basp_attention_grad(plan, q, k, v, o, lse, dout.contiguous(), starts, lengths, scale, dq, dk, dv, ws)
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, q, k, v, starts, lengths, scale):
+        o, lse = _attention_forward(plan, q, k, v, starts, lengths, scale)
+        ctx.plan, ctx.scale = plan, scale
+        ctx.save_for_backward(q, k, v, o, lse, starts, lengths)
+        return o
+
+    @staticmethod
+    def backward(ctx, grad):
+        *tensors, starts, lengths = ctx.saved_tensors
+
+        def compute(grad, q, k, v, o, lse):
+            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+            _attention_grad(ctx.plan, q, k, v, o, lse, grad, starts, lengths, ctx.scale, dq, dk, dv)
+            return dq, dk, dv
+
+        return (None, *_Gradient.apply(compute, grad, *tensors), None, None, None)
+
+
+class _AttentionQKV(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, qkv, starts, lengths, scale):
+        o, lse = _attention_forward(plan, *_parts(plan, qkv), starts, lengths, scale)
+        ctx.plan, ctx.scale = plan, scale
+        ctx.save_for_backward(qkv, o, lse, starts, lengths)
+        return o
+
+    @staticmethod
+    def backward(ctx, grad):
+        *tensors, starts, lengths = ctx.saved_tensors
+
+        def compute(grad, qkv, o, lse):
+            dqkv = torch.empty_like(qkv)
+            _attention_grad(ctx.plan, *_parts(ctx.plan, qkv), o, lse, grad, starts, lengths, ctx.scale, *_parts(ctx.plan, dqkv))
+            return dqkv
+
+        return None, _Gradient.apply(compute, grad, *tensors), None, None, None
+
+
+def _parts(plan, qkv):
+    """Q, K and V of a fused buffer."""
+    return qkv.view(-1).split([plan.info["q_elems"], plan.info["kv_elems"], plan.info["kv_elems"]])
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, x, weight, bias, eps):
+        y = torch.empty_like(x)
+        mean, rstd = (torch.empty(plan.info["T"], dtype=torch.float32, device=x.device) for _ in range(2))
+        b.basp_layer_norm(plan, x, weight, bias, eps, y, mean, rstd)
+        ctx.plan, ctx.bias = plan, bias is not None
+        ctx.save_for_backward(x, weight, mean, rstd)
+        return y
+
+    @staticmethod
+    def backward(ctx, grad):
+        def compute(grad, x, weight, mean, rstd):
+            dx, dweight = torch.empty_like(x), torch.empty_like(weight)
+            dbias = torch.empty_like(weight) if ctx.bias else None
+            b.basp_layer_norm_grad(ctx.plan, grad.contiguous(), x, weight, mean, rstd, dx, dweight, dbias,
+                                   _workspace(ctx.plan, x.device))
+            return dx, dweight, dbias
+
+        return (None, *_Gradient.apply(compute, grad, *ctx.saved_tensors), None)
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, logits, ids, mask, coef):
+        dev = logits.device
+        loss, slope = torch.empty(1, device=dev), torch.empty(plan.info["E"], device=dev)
+        counts = torch.empty(plan.info["E"], dtype=torch.int32, device=dev)
+        b.basp_balance_loss(plan, logits, ids, mask, coef, loss, counts, slope,
+                            torch.empty(plan.balance_bytes, dtype=torch.uint8, device=dev))
+        ctx.plan = plan
+        ctx.save_for_backward(logits, mask, slope)
+        ctx.mark_non_differentiable(counts)
+        return loss, counts
+
+    @staticmethod
+    def backward(ctx, grad, _):
+        logits, mask, slope = ctx.saved_tensors
+
+        def compute(grad, logits):
+            dlogits = torch.empty_like(logits)
+            b.basp_balance_loss_grad(ctx.plan, logits, mask, slope, grad.contiguous(), dlogits)
+            return dlogits
+
+        return None, _Gradient.apply(compute, grad, logits), None, None, None
+
+
+def attention(plan, q, k, v, starts=None, lengths=None, scale=None):
+    """Attention output of q, k and v on head shards (an AttentionPlan), with
+    backward for all three.  scale: d ** -0.5 unless given."""
+    return _Attention.apply(plan, q, k, v, starts, lengths, plan.info["d"] ** -0.5 if scale is None else scale)
+
+
+def attention_qkv(plan, qkv, starts=None, lengths=None, scale=None):
+    """The same on the fused buffer of ``seq_to_head_qkv`` (queries = S), whose
+    gradient is a fused buffer, too."""
+    return _AttentionQKV.apply(plan, qkv, starts, lengths, plan.info["d"] ** -0.5 if scale is None else scale)
+
+
+def layer_norm(plan, x, weight, bias=None, eps=1e-5):
+    """Normed rows of x (a NormPlan), with backward for x, weight and bias."""
+    return _LayerNorm.apply(plan, x, weight, bias, eps)
+
+
+def balance_loss(plan, logits, ids, mask=None, coef=0.01):
+    """(loss [1], counts [E]) of a router (an ExpertPlan whose weight_dtype is the
+    scores'), with backward for the scores."""
+    return _BalanceLoss.apply(plan, logits, ids, mask, coef)

@@ -351,34 +351,39 @@ __global__ __launch_bounds__(kThreads, 1) void attend_step_kernel(const AttendDe
     finish_columns<T, SHARE>(D, col, shard, wave * SHARE, x, m, total);
 }
 
-// The sums of a block's work-groups, relative to the largest of their maxima.
+// The sums of a block's work-groups, relative to the largest of their maxima: a
+// wave takes four of a result's registers (blockIdx.y: sixteen a work-group), so
+// that there are many loads at a time.
 template <typename T, int C>
 __global__ __launch_bounds__(kThreads) void attend_join_kernel(const AttendDesc D)
 {
-    constexpr int WAVES = kThreads / 64, REGS = C / 2, SHARE = REGS / WAVES;
+    constexpr int SHARE = 4;
     const AttendShape &A = D.shape;
     const uint32_t whole = blockIdx.x, pair = fastdiv(whole, D.by_blocks), block = whole - pair * D.blocks;
     const uint32_t shard = fastdiv(pair, A.by_heads), key_head = pair - shard * A.Hl_kv;
+    const uint32_t from_reg = (blockIdx.y * (kThreads / 64) + scalar(threadIdx.x >> 6)) * SHARE;
+    const uint32_t lane = threadIdx.x & 63, c = lane & 31;
     const Sequence seq = sequence_of(A, shard);
-    const uint32_t wave = scalar(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 31;
     const Column col(A, seq, block * kStepColumns + c, key_head);
     const float *const from = D.partials + int64_t{whole} * D.splits * step_partial(C);
     float m = -INFINITY, total = 0.f, x[SHARE];
+#pragma unroll 8
     for (int s = 0; s < D.splits; ++s)
         m = fmaxf(m, from[s * step_partial(C) + C * 32 + c]);
     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int j = 0; j < SHARE; ++j)
         x[j] = 0.f;
+#pragma unroll 4
     for (int s = 0; s < D.splits; ++s) {
         const float *const part = from + s * step_partial(C);
         const float factor = __builtin_amdgcn_exp2f((part[C * 32 + c] - base) * A.scale_log2);
         total += part[C * 32 + 32 + c] * factor;
 #pragma unroll
         for (int j = 0; j < SHARE; ++j)
-            x[j] += part[(wave * SHARE + j) * 64 + lane] * factor;
+            x[j] += part[(from_reg + j) * 64 + lane] * factor;
     }
-    finish_columns<T, SHARE>(D, col, shard, wave * SHARE, x, m, total);
+    finish_columns<T, SHARE>(D, col, shard, from_reg, x, m, total);
 }
 
 // --------------------------------------------------------------- launches --
@@ -397,8 +402,8 @@ basp_status launch_attention(const basp_attention_plan &p, const AttendDesc &D, 
                                         grid, kThreads, D, stream, true, p.splits == 1);
     if (s != BASP_OK || p.splits == 1)
         return s;
-    return launch_kernel(reinterpret_cast<const void *>(attend_join_kernel<T, C>), dim3(uint32_t(pairs * p.blocks)), kThreads, D,
-                         stream, false, true);
+    return launch_kernel(reinterpret_cast<const void *>(attend_join_kernel<T, C>), dim3(uint32_t(pairs * p.blocks), C / 32), kThreads,
+                         D, stream, false, true);
 }
 
 }  // namespace

@@ -370,9 +370,9 @@ struct SumOperands {
 
 // Where some rows are hidden from some columns, their weight is 0, and a product
 // of 0 and an infinity or NaN would be NaN.  So rows with such numbers
-// (wild_rows) are added up one by one and without the zeros.  The kernels leave
-// their loop for that and come back: a branch inside it would cost a copy of all
-// sums in every step.
+// (wild_rows) are added up one by one and without the zeros.  The kernels look for
+// them before all else, while few registers are in use, and leave their loop for
+// them: a branch inside it would cost a copy of all sums in every step.
 template <typename T, int C, int ROWS, int N>
 __device__ inline bool wild_rows(const char *tile, int row0)
 {
