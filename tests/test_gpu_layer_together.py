@@ -37,7 +37,7 @@ def library(p, tokens, lengths, plans, target):
     boundary, embed, norm, attend, experts = plans
     h = ag.embed_to_seq(embed, tokens, p["table"], 2.0)
     x = ag.layer_norm(norm, h, p["w1"], p["b1"], EPS)
-    qkv = ag.seq_to_head_qkv(boundary, *(x @ p[n] for n in ("wq", "wk", "wv")))
+    qkv = ag.seq_to_head_qkv(boundary, *((x @ p[n]).view(-1) for n in ("wq", "wk", "wv")))
     o = ag.head_to_seq_o(boundary, ag.attention_qkv(attend, qkv, lengths=lengths))
     h = h + o.view(B * S, D) @ p["wo"]
     x = ag.layer_norm(norm, h, p["w2"], p["b2"], EPS)
@@ -105,7 +105,7 @@ def test_layer_with_gradients():
     # a chain of about ten products and sums of up to 128 terms in fp32, each off
     # by at most 2 * 130 * 2^-24 = 1.6e-5 of its terms and by a tenth of that in the
     # mean square: 2e-5 in 2-norm, five times that is allowed
-    assert abs(float(loss) - float(want)) <= 1e-4 * float(want)
+    assert abs(loss.item() - want.item()) <= 1e-4 * want.item()
     for (n, got), w in zip(zip(dev, grads), wants):
         off = float((got.cpu().double() - w).norm() / w.norm())
         assert off <= 1e-4, (n, off)
