@@ -181,14 +181,14 @@ __device__ inline void finish_columns(const AttendDesc &D, const Column &col, ui
 // 128 columns a work-group, 32 a wave; its four waves share tiles of 64 keys (32
 // in fp32), of which the next one is on its way while one is used.
 template <typename T, int C, bool DIRECT>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_tile_kernel(const AttendDesc D)
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void attend_tile_kernel(const AttendDesc D)
 {
     constexpr int KEYS = sizeof(T) == 2 ? 64 : 32;
     typedef Tile<T, C, KEYS> Keys;
     __shared__ __attribute__((aligned(16))) char lds[4 * Keys::kBytes];
     const AttendShape &A = D.shape;
-    const uint32_t group = by_xcd(blockIdx.x, gridDim.x), pair = fastdiv(group, D.by_blocks);
-    const uint32_t block = D.blocks - 1 - (group - pair * D.blocks);       // long rows first
+    const Place place = place_of<T>(A, blockIdx.x, gridDim.x, D.by_blocks, D.blocks);
+    const uint32_t pair = place.pair, block = D.blocks - 1 - place.nth;    // later queries see more
     const uint32_t shard = fastdiv(pair, A.by_heads), key_head = pair - shard * A.Hl_kv;
     const Sequence seq = sequence_of(A, shard);
     const uint32_t wave = scalar(threadIdx.x >> 6), lane = threadIdx.x & 63, first = block * kTileColumns;

@@ -44,14 +44,14 @@ struct AttendGradDesc {
 // 128 columns (queries and heads) a work-group, 32 a wave; tiles of keys and
 // values as in the forward pass.
 template <typename T, int C, bool DIRECT>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dq_kernel(const AttendGradDesc D)
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void attend_dq_kernel(const AttendGradDesc D)
 {
     constexpr int KEYS = sizeof(T) == 2 ? 64 : 32;
     typedef Tile<T, C, KEYS> Keys;
     __shared__ __attribute__((aligned(16))) char lds[4 * Keys::kBytes];
     const AttendShape &A = D.shape;
-    const uint32_t group = by_xcd(blockIdx.x, gridDim.x), pair = fastdiv(group, D.by_blocks);
-    const uint32_t block = D.blocks - 1 - (group - pair * D.blocks);       // long rows first
+    const Place place = place_of<T>(A, blockIdx.x, gridDim.x, D.by_blocks, D.blocks);
+    const uint32_t pair = place.pair, block = D.blocks - 1 - place.nth;    // later queries see more
     const uint32_t shard = fastdiv(pair, A.by_heads), key_head = pair - shard * A.Hl_kv;
     const Sequence seq = sequence_of(A, shard);
     const uint32_t wave = scalar(threadIdx.x >> 6), lane = threadIdx.x & 63, first = block * kTileColumns;
@@ -311,7 +311,7 @@ struct QueryWalk {
 // over 64 channels), the values are kept in LDS instead, and tiles are of 32
 // queries to leave room for them.
 template <typename T, int C, bool DIRECT>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dkv_kernel(const AttendGradDesc D)
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void attend_dkv_kernel(const AttendGradDesc D)
 {
     constexpr bool VALUES_IN_LDS = sizeof(T) == 2 && C > 64;
     constexpr int ROWS = sizeof(T) == 2 && !VALUES_IN_LDS ? 64 : 32;
@@ -321,7 +321,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attend_dkv_k
     __shared__ __attribute__((aligned(16))) char lds[4 * Rows::kBytes];
     __shared__ __attribute__((aligned(16))) float lds_rows[2 * 2 * 64];
     const AttendShape &A = D.shape;
-    const uint32_t group = by_xcd(blockIdx.x, gridDim.x), pair = fastdiv(group, D.by_items), item = group - pair * D.items;
+    const Place place = place_of<T>(A, blockIdx.x, gridDim.x, D.by_items, D.items);
+    const uint32_t pair = place.pair, item = place.nth;
     const uint32_t shard = fastdiv(pair, A.by_heads), key_head = pair - shard * A.Hl_kv;
     const uint32_t in_sinks = uint32_t(D.sink_blocks) * D.sink_chunks;
     const bool sinks = item < in_sinks;

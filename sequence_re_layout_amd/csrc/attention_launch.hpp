@@ -34,6 +34,8 @@ inline AttendShape attend_shape(const basp_attention_plan &p, const int32_t *sta
     A.by_heads = make_fastdiv(uint32_t(p.Hl_kv));
     A.by_Bl = make_fastdiv(uint32_t(p.Bl));
     A.by_P = make_fastdiv(uint32_t(p.P));
+    A.pairs = uint32_t(p.shards) * p.Hl_kv;
+    A.by_pairs = make_fastdiv(A.pairs);
     A.scale = scale;
     A.scale_log2 = float(double(scale) * 1.4426950408889634);
     A.slack = float(8.0 / (double(scale) * 1.4426950408889634));

@@ -22,7 +22,7 @@ struct basp_attention_plan {
     int64_t q_elems, kv_elems, lse_elems;
     // strides in bytes
     int64_t q_token, q_head, q_shard, kv_token, kv_head, kv_shard;
-    basp::FastDiv by_ratio, by_blocks, by_heads;
+    basp::FastDiv by_ratio;
     // forward pass: columns (query, head of a group) of a work-group, its
     // blocks of a key head, and work-groups that share the keys of a block
     int32_t columns, blocks, splits;
