@@ -168,21 +168,21 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
         }
 }
 
-// Sixteen channels of a result's column of keys as stored.
-template <typename T>
-__device__ inline void store_key(const AttendShape &A, char *to, uint32_t shard, uint32_t key_head, int key, int block, int half,
-                                 const f32x16 &sums, float scale)
+// N registers of a result's column of keys as stored, the first ones of `channel` on.
+template <typename T, int N, typename Sums>
+__device__ inline void store_key(const AttendShape &A, char *to, uint32_t shard, uint32_t key_head, int key, int channel, int half,
+                                 const Sums &sums, float scale)
 {
     if (key >= A.S)
         return;
     char *const row = to + shard * A.kv_shard + key_head * A.kv_head + int64_t{key} * A.kv_token;
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
+    for (int i = 0; i < N; i += 4) {
         float x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             x[j] = sums[i + j] * scale;
-        store_four<T>(row, 32 * block + row_of(i, half), A.d, x);
+        store_four<T>(row, channel + row_of(i, half), A.d, x);
     }
 }
 
@@ -490,8 +490,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
     if ((sinks ? D.sink_chunks : D.chunks) == 1) {
 #pragma unroll
         for (int b = 0; b < C / 32; ++b) {
-            store_key<T>(A, D.dk, shard, key_head, key, b, half, dk[b], A.scale);
-            store_key<T>(A, D.dv, shard, key_head, key, b, half, dv[b], 1.f);
+            store_key<T, 16>(A, D.dk, shard, key_head, key, 32 * b, half, dk[b], A.scale);
+            store_key<T, 16>(A, D.dv, shard, key_head, key, 32 * b, half, dv[b], 1.f);
         }
         return;
     }
@@ -510,35 +510,47 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
 
 struct AttendJoinDesc {
     AttendShape shape;
-    const float *partials;          // of the first pair's first block of these
+    const float *partials;
     char *dk, *dv;
     int64_t pair_stride;            // numbers from one pair's to the next one's
     FastDiv by_blocks;
-    int32_t blocks, first_block, chunks;
+    int32_t blocks, first_block;    // unfinished blocks of a pair, of which the first
+    int32_t sink_blocks, sink_chunks, chunks;       // blocks of sink_chunks chunks, then of `chunks`
 };
 
-// The sums of a block of keys over its chunks: a wave takes 32 keys and 32
-// channels of dK or dV.
+// The sums of a block of keys over its chunks: a wave takes 32 keys and 16
+// channels of dK or dV, four chunks on their way at a time.  13 us for the 44 MB of
+// chunks of three fp32 sequences of 998, whose 96 blocks have 6 or 16 of them.
 template <typename T, int C>
 __global__ __launch_bounds__(kThreads) void attend_grad_join_kernel(const AttendJoinDesc D)
 {
     const AttendShape &A = D.shape;
+    constexpr int EACH = 2 * kKeyBlock * C, AHEAD = 4;
     const uint32_t pair = fastdiv(blockIdx.x, D.by_blocks), block = blockIdx.x - pair * D.blocks;
     const uint32_t shard = fastdiv(pair, A.by_heads), key_head = pair - shard * A.Hl_kv;
     const uint32_t unit = blockIdx.y * (kThreads / 64) + scalar(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const uint32_t b = unit % (C / 32), wave = unit / (C / 32);            // wave: 0 to 3 of dK, 4 to 7 of dV
-    const float *from = D.partials + pair * D.pair_stride + int64_t{block} * D.chunks * (2 * kKeyBlock * C) +
-                        (wave * (C / 2) + b * 16) * 64 + lane;
-    f32x16 sums;
+    const uint32_t part = unit % (C / 16), wave = unit / (C / 16);         // wave: 0 to 3 of dK, 4 to 7 of dV
+    const bool sinks = block < uint32_t(D.sink_blocks);
+    const int64_t before = sinks ? int64_t{block} * D.sink_chunks
+                                 : int64_t{D.sink_blocks} * D.sink_chunks + int64_t{block - D.sink_blocks} * D.chunks;
+    const int chunks = sinks ? D.sink_chunks : D.chunks;
+    const float *from = D.partials + pair * D.pair_stride + before * EACH + (wave * (C / 2) + part * 8) * 64 + lane;
+    float sums[8] = {};
+    for (int c = 0; c < chunks; c += AHEAD, from += AHEAD * EACH) {
+        float x[AHEAD][8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        sums[i] = 0.f;
-    for (int c = 0; c < D.chunks; ++c, from += 2 * kKeyBlock * C)
+        for (int n = 0; n < AHEAD; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            sums[i] += from[i * 64];
+            for (int i = 0; i < 8; ++i)
+                x[n][i] = c + n < chunks ? from[n * EACH + i * 64] : 0.f;
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sums[i] += x[n][i];
+    }
     const int key = int(D.first_block + block) * kKeyBlock + int(wave & 3) * 32 + int(lane & 31);
-    store_key<T>(A, wave < 4 ? D.dk : D.dv, shard, key_head, key, int(b), int(lane >> 5), sums, wave < 4 ? A.scale : 1.f);
+    store_key<T, 8>(A, wave < 4 ? D.dk : D.dv, shard, key_head, key, int(part) * 16, int(lane >> 5), sums, wave < 4 ? A.scale : 1.f);
 }
 
 // --------------------------------------------------------------- launches --
@@ -555,23 +567,21 @@ basp_status launch_attention_grad(const basp_attention_plan &p, const AttendGrad
         s = launch_kernel(direct ? reinterpret_cast<const void *>(attend_dkv_kernel<T, C, true>)
                                  : reinterpret_cast<const void *>(attend_dkv_kernel<T, C, false>),
                           dim3(uint32_t(pairs * D.items)), kThreads, D, stream, false, !cut[0] && !cut[1]);
-    const int64_t numbers = 2 * kKeyBlock * C, sink_part = p.sink_chunks > 1 ? int64_t{p.sink_blocks} * p.sink_chunks : 0;
-    const int64_t part = p.chunks > 1 ? int64_t{p.key_blocks - p.sink_blocks} * p.chunks : 0;
-    for (int i = 0; i < 2 && s == BASP_OK; ++i) {
-        if (!cut[i])
-            continue;
+    if (s == BASP_OK && (cut[0] || cut[1])) {
         AttendJoinDesc J = {};
         J.shape = D.shape;
-        J.partials = D.partials + (i ? sink_part : 0) * numbers;
+        J.partials = D.partials;
         J.dk = D.dk;
         J.dv = D.dv;
-        J.pair_stride = (sink_part + part) * numbers;
-        J.blocks = i ? p.key_blocks - p.sink_blocks : p.sink_blocks;
+        J.sink_blocks = cut[0] ? p.sink_blocks : 0;
+        J.blocks = J.sink_blocks + (cut[1] ? p.key_blocks - p.sink_blocks : 0);
         J.by_blocks = make_fastdiv(uint32_t(J.blocks));
-        J.first_block = i ? p.sink_blocks : 0;
-        J.chunks = i ? p.chunks : p.sink_chunks;
+        J.first_block = cut[0] ? 0 : p.sink_blocks;
+        J.sink_chunks = p.sink_chunks;
+        J.chunks = p.chunks;
+        J.pair_stride = (int64_t{J.sink_blocks} * J.sink_chunks + int64_t{J.blocks - J.sink_blocks} * J.chunks) * (2 * kKeyBlock * C);
         s = launch_kernel(reinterpret_cast<const void *>(attend_grad_join_kernel<T, C>),
-                          dim3(uint32_t(pairs * J.blocks), 2 * (C / 32)), kThreads, J, stream, false, i == 1 || !cut[1]);
+                          dim3(uint32_t(pairs * J.blocks), 4 * (C / 32)), kThreads, J, stream, false, true);
     }
     return s;
 }
