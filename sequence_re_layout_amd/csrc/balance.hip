@@ -27,85 +27,149 @@
 namespace basp {
 namespace {
 
+// Partial results [groups][2][stride], the counts' last number the live tokens,
+// and what becomes of them.
+struct BalanceParts {
+    float *parts;
+    float *loss, *slope;
+    int32_t *counts;
+    int32_t groups, E, K, stride;
+    float coef;
+};
+
 struct BalanceDesc {
     const char *logits;
     const void *ids;
     const uint8_t *mask;
-    float *sums;                    // [groups][E]
-    int32_t *counts;                // [groups][E + 1], the last: live tokens
     int64_t T, per_group;           // tokens, and of a work-group
     uint32_t row, vecs;
-    int32_t K, E, wide_ids;
+    int32_t wide_ids;
     FastDiv by_K;
+    BalanceParts out;
 };
 
-// Scores of one token in a team's registers, -inf where a lane has no column
-// of its own, and their softmax in place of them.
+// The scores of a token in a team's registers: vector lane + r * LANES of the row,
+// the last one of which may overlap the one before, or be beyond the row.
 template <typename E, int VW, int LANES, int R>
 struct Scores {
     static constexpr int N = VW / sizeof(E);
-    float f[R][N];
+    typedef typename MemVec<VW>::type Raw;
 
-    __device__ inline void load(const char *row_at, uint32_t lane, uint32_t row, uint32_t vecs)
+    uint32_t lane, row, vecs, seen;         // seen: numbers of the last vector that the one before has
+    bool has;                               // a last vector
+
+    __device__ inline Scores(uint32_t lane_, uint32_t row_, uint32_t vecs_) : lane(lane_), row(row_), vecs(vecs_)
+    {
+        seen = first(R - 1);
+        has = lane + (R - 1) * LANES < vecs;
+    }
+    __device__ inline uint32_t at(int r) const { return vec_offset<VW>(lane + r * LANES, row); }
+    __device__ inline uint32_t first(int r) const { return ((lane + r * LANES) * VW - at(r)) / sizeof(E); }
+    __device__ inline bool mine(int r, int i) const { return r < R - 1 || (has && uint32_t(i) >= seen); }
+
+    __device__ inline void load(Raw (&x)[R], const char *row_at) const
     {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const uint32_t a = lane + r * LANES, off = vec_offset<VW>(a, row), seen = (a * VW - off) / sizeof(E);
-            if (a < vecs)
-                unpack<E, VW>(load_vec<VW, false>(row_at + off), f[r]);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                f[r][i] = a < vecs && uint32_t(i) >= seen ? f[r][i] : -INFINITY;
-        }
+        for (int r = 0; r < R; ++r)         // beyond the row: its end, again
+            x[r] = load_vec<VW, false>(row_at + at(r));
     }
 
-    __device__ inline void clear()
-    {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                f[r][i] = 0.f;
-    }
-
-    __device__ inline void softmax()
+    // exp(score - most) in f, 0 where another lane has the number; the return
+    // value is their sum over the lane
+    __device__ inline float powers(const Raw (&x)[R], float (&f)[R][N]) const
     {
         float most = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r) {
+            unpack<E, VW>(x[r], f[r]);
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < N; ++i) {
+                f[r][i] = mine(r, i) ? f[r][i] : -INFINITY;
                 most = fmaxf(most, f[r][i]);
-        most = team_max<LANES>(most);
-        float total[1] = {0.f};
+            }
+        }
+        most = team_fold<LANES>(most, [](float a, float b) { return fmaxf(a, b); });
+        float total = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 f[r][i] = __builtin_amdgcn_exp2f((f[r][i] - most) * 1.4426950408889634f);
-                total[0] += f[r][i];
+                total += f[r][i];
             }
-        team_sum<LANES, 1>(total, nullptr);
-        const float inv = 1.f / total[0];
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                f[r][i] *= inv;
+        return total;
     }
 };
+
+typedef float x4 __attribute__((ext_vector_type(4)));
+typedef int i4 __attribute__((ext_vector_type(4)));
+
+// Counts, slope and loss by one work-group, from the sums and counts of columns 4 c
+// to 4 c + 3 in the threads that have some.
+__device__ inline void finish_balance(const BalanceParts &D, int c, bool mine, x4 P, i4 n)
+{
+    constexpr int WAVES = kBalanceThreads / 64;
+    __shared__ float wave_loss[WAVES];
+    __shared__ int live_tokens;
+    if (mine && c == D.E / 4)
+        live_tokens = n[D.E % 4];
+    lds_barrier();
+    float term = 0.f;
+    if (mine) {
+        const float L = float(live_tokens);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = 4 * c + i;
+            if (e < D.E) {
+                const float slope = live_tokens ? D.coef * (float(n[i]) * float(D.E) / (float(D.K) * L)) / L : 0.f;
+                D.counts[e] = n[i];
+                D.slope[e] = slope;
+                term += live_tokens ? slope * P[i] : 0.f;
+            }
+        }
+    }
+    term = team_fold<64>(term, [](float a, float b) { return a + b; });
+    if ((threadIdx.x & 63) == 0)
+        wave_loss[threadIdx.x >> 6] = term;
+    lds_barrier();
+    if (threadIdx.x == 0) {
+        float loss = 0.f;
+        for (int w = 0; w < WAVES; ++w)
+            loss += wave_loss[w];
+        *D.loss = loss;
+    }
+}
 
 template <typename E, int VW, int LANES, int R>
 __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const BalanceDesc D)
 {
-    constexpr int N = VW / sizeof(E), TEAMS = kBalanceThreads / LANES, WAVES = kBalanceThreads / 64;
-    __shared__ float part[WAVES][(LANES < 64 ? LANES : 64) * N];
-    __shared__ int hist[kMaxExperts + 1];
+    typedef Scores<E, VW, LANES, R> Row;
+    constexpr int N = Row::N, TEAMS = kBalanceThreads / LANES, WAVES = kBalanceThreads / 64, WIDTH = R * LANES * N;
+    __shared__ float part[WAVES][WIDTH];
+    __shared__ __attribute__((aligned(16))) float total[kMaxExperts + 4];
+    __shared__ __attribute__((aligned(16))) int hist[kMaxExperts + 4];
+    const BalanceParts &out = D.out;
     const int64_t begin = blockIdx.x * D.per_group, end = begin + D.per_group < D.T ? begin + D.per_group : D.T;
-    for (int e = threadIdx.x; e <= D.E; e += kBalanceThreads)
+    const Row row(threadIdx.x % LANES, D.row, D.vecs);
+    // one token ahead; a masked token's scores are loaded too, and then ignored
+    typename Row::Raw x[R];
+    bool is = false;
+    int64_t t = begin + threadIdx.x / LANES;
+    if (t < end) {
+        row.load(x, D.logits + t * D.row);
+        is = !D.mask || D.mask[t];
+    }
+    for (int e = threadIdx.x; e < out.stride; e += kBalanceThreads) {
         hist[e] = 0;
+        total[e] = 0.f;
+    }
     lds_barrier();
-    const uint32_t lane = threadIdx.x % LANES;
+    for (int64_t s = begin * out.K + threadIdx.x; s < end * out.K; s += kBalanceThreads) {
+        const int64_t id = D.wide_ids ? static_cast<const int64_t *>(D.ids)[s] : static_cast<const int32_t *>(D.ids)[s];
+        const bool live = !D.mask || D.mask[begin + fastdiv(uint32_t(s - begin * out.K), D.by_K)];
+        if (live && id >= 0 && id < out.E)
+            atomicAdd(&hist[id], 1);
+    }
     float acc[R][N];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -113,127 +177,111 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const BalanceD
         for (int i = 0; i < N; ++i)
             acc[r][i] = 0.f;
     int live = 0;
-    // four tokens at a time: the sums over lanes of one are as long a chain as a
-    // load from memory
-    constexpr int U = 4;
-    for (int64_t t = begin + threadIdx.x / LANES; t < end; t += TEAMS * U) {
-        Scores<E, VW, LANES, R> s[U];
-        bool is[U];
+    while (t < end) {
+        typename Row::Raw now[R];
+        const bool counts = is;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t at = t + u * TEAMS;
-            if (at < end)               // a masked token's scores are loaded too, and then ignored
-                s[u].load(D.logits + at * D.row, lane, D.row, D.vecs);
-            else
-                s[u].clear();
-            is[u] = at < end && (!D.mask || D.mask[at]);
+        for (int r = 0; r < R; ++r)
+            now[r] = x[r];
+        t += TEAMS;
+        if (t < end) {
+            row.load(x, D.logits + t * D.row);
+            is = !D.mask || D.mask[t];
         }
+        float f[R][N], sum[1] = {row.powers(now, f)};
+        team_sum<LANES, 1>(sum, nullptr);
+        const float inv = 1.f / sum[0];
+        live += counts;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            s[u].softmax();
-            live += is[u];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    acc[r][i] += is[u] ? s[u].f[r][i] : 0.f;
-        }
-    }
-    if (lane == 0 && live)
-        atomicAdd(&hist[D.E], live);
-    for (int64_t s = begin * D.K + threadIdx.x; s < end * D.K; s += kBalanceThreads) {
-        const int64_t id = D.wide_ids ? static_cast<const int64_t *>(D.ids)[s] : static_cast<const int32_t *>(D.ids)[s];
-        if (id >= 0 && id < D.E && (!D.mask || D.mask[begin + fastdiv(uint32_t(s - begin * D.K), D.by_K)]))
-            atomicAdd(&hist[id], 1);
-    }
-    // the teams' sums: those of a wave first, then the waves in their order
-    const uint32_t wave = threadIdx.x >> 6, in_wave = threadIdx.x & 63;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int d = LANES; d < 64; d <<= 1)
-                acc[r][i] += __shfl_xor(acc[r][i], d);
-        lds_barrier();
-        if (in_wave < LANES)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                part[wave][lane * N + i] = acc[r][i];
-        lds_barrier();
-        for (uint32_t c = threadIdx.x; c < LANES * N; c += kBalanceThreads) {
-            const uint32_t a = c / N + r * LANES, off = vec_offset<VW>(a, D.row), seen = (a * VW - off) / sizeof(E);
-            float sum = 0.f;
-            for (int w = 0; w < WAVES; ++w)
-                sum += part[w][c];
-            if (a < D.vecs && c % N >= seen)
-                D.sums[int64_t(blockIdx.x) * D.E + off / sizeof(E) + c % N] = sum;
+                acc[r][i] += counts ? f[r][i] * inv : 0.f;
+    }
+    if (row.lane == 0 && live)
+        atomicAdd(&hist[out.E], live);
+    // the teams' sums: those of a wave first, then the waves in their order
+    const uint32_t wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            acc[r][i] = sum_of_teams<LANES>(acc[r][i]);
+            if ((threadIdx.x & 63) < LANES)
+                part[wave][(row.lane + r * LANES) * N + i] = acc[r][i];
         }
+    lds_barrier();
+    const bool alone = out.groups == 1;
+    float *const parts = out.parts + int64_t(blockIdx.x) * 2 * out.stride, *const sums = alone ? total : parts;
+    for (uint32_t c = threadIdx.x; c < WIDTH; c += kBalanceThreads) {
+        const uint32_t a = c / N, off = vec_offset<VW>(a, D.row), seen = (a * VW - off) / sizeof(E);
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            sum += part[w][c];
+        if (a < D.vecs && c % N >= seen)
+            sums[off / sizeof(E) + c % N] = sum;
+    }
+    if (!alone) {
+        for (int e = threadIdx.x; e <= out.E; e += kBalanceThreads)
+            reinterpret_cast<int *>(parts)[out.stride + e] = hist[e];
+        return;
     }
     lds_barrier();
-    for (int e = threadIdx.x; e <= D.E; e += kBalanceThreads)
-        D.counts[int64_t(blockIdx.x) * (D.E + 1) + e] = hist[e];
+    const int c = threadIdx.x;
+    const bool mine = 4 * c < out.stride;
+    finish_balance(out, c, mine, mine ? reinterpret_cast<const x4 *>(total)[c] : x4{}, mine ? reinterpret_cast<const i4 *>(hist)[c] : i4{});
 }
 
-struct BalanceJoinDesc {
-    const float *sums;
-    const int32_t *group_counts;
-    float *loss, *slope;
-    int32_t *counts;
-    int32_t groups, E, K, columns_log2;
-    float coef;
-};
-
-// One work-group: a power of two of columns side by side, and the rest of the
-// threads over the partial sums.
-__global__ __launch_bounds__(kBalanceThreads) void balance_join_kernel(const BalanceJoinDesc D)
+// One work-group: four columns a thread, the threads of a column over the partial
+// results, eight of them on their way at a time.
+__global__ __launch_bounds__(kBalanceThreads) void balance_join_kernel(const BalanceParts D)
 {
-    __shared__ float sums[kBalanceThreads];
-    __shared__ int counts[kBalanceThreads];
-    __shared__ float wave_loss[kBalanceThreads / 64];
-    __shared__ int live_tokens;
-    const int columns = 1 << D.columns_log2, e = threadIdx.x & (columns - 1), s = threadIdx.x >> D.columns_log2;
-    const int slices = kBalanceThreads >> D.columns_log2;
-    if (threadIdx.x == 0)
-        live_tokens = 0;
-    lds_barrier();
-    float P = 0.f;
-    int n = 0;
-    if (e < D.E)
-#pragma unroll 8
-        for (int g = s; g < D.groups; g += slices) {
-            P += D.sums[int64_t(g) * D.E + e];
-            n += D.group_counts[int64_t(g) * (D.E + 1) + e];
+    constexpr int AHEAD = 8;
+    __shared__ __attribute__((aligned(16))) x4 sums[kBalanceThreads];
+    __shared__ __attribute__((aligned(16))) i4 counts[kBalanceThreads];
+    const int fours = D.stride / 4;
+    int columns = 1;                // threads side by side
+    while (columns < fours)
+        columns *= 2;
+    const int c = threadIdx.x & (columns - 1), slices = kBalanceThreads / columns;
+    x4 P = {0.f, 0.f, 0.f, 0.f};
+    i4 n = {0, 0, 0, 0};
+    const float *const from = D.parts + 4 * (c < fours ? c : 0);
+    for (int g = threadIdx.x / columns; g < D.groups; g += AHEAD * slices) {
+        x4 x[AHEAD];
+        i4 y[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int at = g + i * slices < D.groups ? g + i * slices : g;
+            x[i] = *reinterpret_cast<const x4 *>(from + int64_t{at} * 2 * D.stride);
+            y[i] = *reinterpret_cast<const i4 *>(from + (int64_t{at} * 2 + 1) * D.stride);
         }
-    for (int g = threadIdx.x; g < D.groups; g += kBalanceThreads)
-        atomicAdd(&live_tokens, D.group_counts[int64_t(g) * (D.E + 1) + D.E]);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (g + i * slices < D.groups) {
+                P += x[i];
+                n += y[i];
+            }
+    }
+    for (int d = columns; d < 64; d *= 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            P[i] += __shfl_xor(P[i], d);
+            n[i] += __shfl_xor(n[i], d);
+        }
+    // then by waves, or by rows of threads where those are wider
+    const int wide = columns < 64 ? 64 : columns;
     sums[threadIdx.x] = P;
     counts[threadIdx.x] = n;
     lds_barrier();
-    float term = 0.f;
-    if (s == 0 && e < D.E) {
-        for (int j = 1; j < slices; ++j) {
-            P += sums[j * columns + e];
-            n += counts[j * columns + e];
+    const bool mine = int(threadIdx.x) < fours;
+    if (mine)
+        for (int j = wide; j < kBalanceThreads; j += wide) {
+            P += sums[j + c];
+            n += counts[j + c];
         }
-        const float L = float(live_tokens);
-        const float slope = live_tokens ? D.coef * (float(n) * float(D.E) / (float(D.K) * L)) / L : 0.f;
-        D.counts[e] = n;
-        D.slope[e] = slope;
-        term = live_tokens ? slope * P : 0.f;
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        term += __shfl_xor(term, d);
-    if ((threadIdx.x & 63) == 0)
-        wave_loss[threadIdx.x >> 6] = term;
-    lds_barrier();
-    if (threadIdx.x == 0) {
-        float loss = 0.f;
-        for (int w = 0; w < kBalanceThreads / 64; ++w)
-            loss += wave_loss[w];
-        *D.loss = loss;
-    }
+    finish_balance(D, c, mine, P, n);
 }
 
 struct BalanceGradDesc {
@@ -246,50 +294,58 @@ struct BalanceGradDesc {
 
 constexpr int kGradThreads = 256;
 
+// Tokens of a team, one after the other, all on their way from the start.
+constexpr int grad_tokens(int R) { return R <= 2 ? 4 : 2; }
+
 template <typename E, int VW, int LANES, int R>
 __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const BalanceGradDesc D)
 {
-    constexpr int N = VW / sizeof(E), TEAMS = kGradThreads / LANES;
-    const uint32_t lane = threadIdx.x % LANES, t = blockIdx.x * TEAMS + threadIdx.x / LANES;
-    if (t >= D.tokens)
+    typedef Scores<E, VW, LANES, R> Row;
+    constexpr int N = Row::N, TEAMS = kGradThreads / LANES, U = grad_tokens(R);
+    const uint32_t first = blockIdx.x * TEAMS * U + threadIdx.x / LANES;
+    if (first >= D.tokens)
         return;
-    char *const out = D.dlogits + uint64_t(t) * D.row;
-    Scores<E, VW, LANES, R> s;      // all loads first; a masked token's scores are then ignored
-    float slope[R][N], dot[1] = {0.f};
-    s.load(D.logits + uint64_t(t) * D.row, lane, D.row, D.vecs);
-    const bool live = !D.mask || D.mask[t];
+    const Row row(threadIdx.x % LANES, D.row, D.vecs);
+    typename Row::Raw x[U][R];      // a masked token's, too, and then ignored
+    bool live[U];
+    float slope[R][N];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const uint32_t a = lane + r * LANES;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            slope[r][i] = 0.f;
-        if (a < D.vecs)
-            load_values<float, N>(reinterpret_cast<const char *>(D.slope) + vec_offset<VW>(a, D.row) / sizeof(E) * 4, slope[r]);
+    for (int u = 0; u < U; ++u) {
+        const uint32_t t = first + u * TEAMS < D.tokens ? first + u * TEAMS : first;
+        row.load(x[u], D.logits + uint64_t(t) * D.row);
+        live[u] = !D.mask || D.mask[t];
     }
-    const float g = *D.dloss;
-    s.softmax();
 #pragma unroll
     for (int r = 0; r < R; ++r)
+        load_values<float, N>(reinterpret_cast<const char *>(D.slope) + row.at(r) / sizeof(E) * 4, slope[r]);
+    const float g = *D.dloss;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            dot[0] += s.f[r][i] * slope[r][i];
-    team_sum<LANES, 1>(dot, nullptr);
+    for (int u = 0; u < U; ++u) {
+        const uint32_t t = first + u * TEAMS;
+        float f[R][N], sums[2] = {row.powers(x[u], f), 0.f};
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const uint32_t a = lane + r * LANES, off = vec_offset<VW>(a, D.row), seen = (a * VW - off) / sizeof(E);
-        float o[N];
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            o[i] = live ? g * s.f[r][i] * (slope[r][i] - dot[0]) : 0.f;
-        if (a < D.vecs) {
-            if (seen == 0)
-                store_vec<VW>(out + off, pack<E, VW>(o));
+            for (int i = 0; i < N; ++i)
+                sums[1] += f[r][i] * slope[r][i];
+        team_sum<LANES, 2>(sums, nullptr);
+        const float inv = 1.f / sums[0], dot = sums[1] * inv, scale = g * inv;
+        if (t >= D.tokens)
+            return;
+        char *const out = D.dlogits + uint64_t(t) * D.row;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float o[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                o[i] = live[u] ? scale * f[r][i] * (slope[r][i] - dot) : 0.f;
+            if (r < R - 1 || (row.has && row.seen == 0))
+                store_vec<VW>(out + row.at(r), pack<E, VW>(o));
             else
 #pragma unroll
                 for (int i = 0; i < N; ++i)     // the others belong to the lane before
-                    if (uint32_t(i) >= seen)
-                        reinterpret_cast<E *>(out + off)[i] = static_cast<E>(o[i]);
+                    if (row.mine(r, i))
+                        reinterpret_cast<E *>(out + row.at(r))[i] = static_cast<E>(o[i]);
         }
     }
 }
@@ -298,69 +354,48 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const Balanc
 
 struct BalanceShape {
     const void *sum, *grad;
-    int lanes;
+    int tokens;                     // of a team of the gradient
 };
 
 template <typename E, int VW, int LANES, int R>
 BalanceShape shape_of()
 {
     return {reinterpret_cast<const void *>(balance_kernel<E, VW, LANES, R>),
-            reinterpret_cast<const void *>(balance_grad_kernel<E, VW, LANES, R>), LANES};
+            reinterpret_cast<const void *>(balance_grad_kernel<E, VW, LANES, R>), grad_tokens(R)};
 }
 
-// As many lanes as a token has vectors, so that few are idle; at most a wave.
 template <typename E, int VW>
-BalanceShape balance_shape(int64_t vecs)
+BalanceShape balance_shape(const LogitRow &r)
 {
-    if (vecs <= 4)
-        return shape_of<E, VW, 4, 1>();
     if constexpr (VW == 16) {
-        if (vecs <= 16)
-            return shape_of<E, VW, 16, 1>();
-        if (vecs <= 32)
-            return shape_of<E, VW, 32, 1>();
-        if (vecs <= 64)
-            return shape_of<E, VW, 64, 1>();
-        if (vecs <= 128)
-            return shape_of<E, VW, 64, 2>();
-        return shape_of<E, VW, 64, 4>();
+        if (r.lanes == 8)
+            return r.regs == 1   ? shape_of<E, VW, 8, 1>()
+                   : r.regs == 2 ? shape_of<E, VW, 8, 2>()
+                   : r.regs == 3 ? shape_of<E, VW, 8, 3>()
+                                 : shape_of<E, VW, 8, 4>();
+        if (r.lanes == 16)
+            return r.regs == 3 ? shape_of<E, VW, 16, 3>() : shape_of<E, VW, 16, 4>();
+        if (r.lanes == 32)
+            return r.regs == 3 ? shape_of<E, VW, 32, 3>() : shape_of<E, VW, 32, 4>();
+        if constexpr (kMaxExperts * sizeof(E) > 128 * VW)
+            if (r.lanes == 64)
+                return r.regs == 3 ? shape_of<E, VW, 64, 3>() : shape_of<E, VW, 64, 4>();
     }
-    return {};                       // shorter vectors: a row holds at most two
-}
-
-struct LogitRow {
-    int vw;
-    int64_t row, vecs;
-};
-
-LogitRow logit_row(const basp_expert_plan &p)
-{
-    LogitRow r;
-    r.vw = row_vector(p.E, p.ws_es);
-    r.row = int64_t{p.E} * p.ws_es;
-    r.vecs = (r.row + r.vw - 1) / r.vw;
-    return r;
+    return shape_of<E, VW, 4, 1>();     // rows of shorter vectors have at most two
 }
 
 basp_status launch_balance(const basp_expert_plan &p, const void *logits, const void *ids, const uint8_t *mask, float coef,
                            float *loss, int32_t *counts, float *slope, void *ws, void *stream)
 {
     const LogitRow r = logit_row(p);
-    const BalanceShape shape = BASP_BY_ROW(balance_shape, p.weight_dtype, r.vw, r.vecs);
-    const int groups = p.T ? balance_groups(p) : 0;
-    float *const sums = static_cast<float *>(ws);
-    int32_t *const group_counts = reinterpret_cast<int32_t *>(sums + int64_t{groups} * p.E);
-    const BalanceDesc D = {static_cast<const char *>(logits), ids, mask, sums, group_counts, p.T,
-                           groups ? (p.T + groups - 1) / groups : 0, uint32_t(r.row), uint32_t(r.vecs), p.K, p.E,
-                           p.id_bytes == 8, make_fastdiv(uint32_t(p.K))};
-    basp_status s = BASP_OK;
-    if (groups)
-        s = launch_kernel(shape.sum, dim3(groups), kBalanceThreads, D, stream, true, false);
-    BalanceJoinDesc J = {sums, group_counts, loss, slope, counts, groups, p.E, p.K, 0, coef};
-    while ((1 << J.columns_log2) < p.E)
-        ++J.columns_log2;
-    if (s == BASP_OK)
-        s = launch_kernel(reinterpret_cast<const void *>(balance_join_kernel), dim3(1), kBalanceThreads, J, stream, !groups, true);
+    const BalanceShape shape = BASP_BY_ROW(balance_shape, p.weight_dtype, r.vw, r);
+    const int groups = balance_groups(p);
+    const BalanceDesc D = {static_cast<const char *>(logits), ids, mask, p.T, (p.T + groups - 1) / groups, uint32_t(r.row),
+                           uint32_t(r.vecs), p.id_bytes == 8, make_fastdiv(uint32_t(p.K)),
+                           {static_cast<float *>(ws), loss, slope, counts, groups, p.E, p.K, int32_t(balance_stride(p)), coef}};
+    basp_status s = launch_kernel(shape.sum, dim3(groups), kBalanceThreads, D, stream, true, groups == 1);
+    if (s == BASP_OK && groups > 1)
+        s = launch_kernel(reinterpret_cast<const void *>(balance_join_kernel), dim3(1), kBalanceThreads, D.out, stream, false, true);
     return s;
 }
 
@@ -368,14 +403,14 @@ basp_status launch_balance_grad(const basp_expert_plan &p, const void *logits, c
                                 const float *dloss, void *dlogits, void *stream)
 {
     const LogitRow r = logit_row(p);
-    const BalanceShape shape = BASP_BY_ROW(balance_shape, p.weight_dtype, r.vw, r.vecs);
-    const int64_t teams = kGradThreads / shape.lanes, step = (int64_t{1} << 22) * teams;
+    const BalanceShape shape = BASP_BY_ROW(balance_shape, p.weight_dtype, r.vw, r);
+    const int64_t each = int64_t{kGradThreads / r.lanes} * shape.tokens, step = (int64_t{1} << 22) * each;
     basp_status s = BASP_OK;
     for (int64_t t0 = 0; t0 < p.T && s == BASP_OK; t0 += step) {
         const int64_t n = std::min(step, p.T - t0);
         const BalanceGradDesc D = {static_cast<const char *>(logits) + t0 * r.row, mask ? mask + t0 : nullptr, slope, dloss,
                                    static_cast<char *>(dlogits) + t0 * r.row, uint32_t(n), uint32_t(r.row), uint32_t(r.vecs)};
-        s = launch_kernel(shape.grad, dim3(uint32_t((n + teams - 1) / teams)), kGradThreads, D, stream, t0 == 0, t0 + n == p.T);
+        s = launch_kernel(shape.grad, dim3(uint32_t((n + each - 1) / each)), kGradThreads, D, stream, t0 == 0, t0 + n == p.T);
     }
     return s;
 }
@@ -393,7 +428,7 @@ extern "C" basp_status basp_balance_loss(const basp_expert_plan *p, const void *
             return BASP_ERR_INVALID;
         const CallBuf in[] = {{logits, p->T * p->E * p->ws_es, p->ws_es}, {ids, p->slots * p->id_bytes, p->id_bytes},
                               {mask, mask ? p->T : 0, 1}};
-        const int64_t need = int64_t{basp::balance_groups(*p)} * (2 * p->E + 1) * 4;
+        const int64_t need = int64_t(basp_balance_workspace_bytes(p));
         const CallBuf out[] = {{loss, 4, 4}, {counts, int64_t{4} * p->E, 4}, {slope, int64_t{4} * p->E, 4}, {ws, need, 16}};
         const basp_status s = basp::check_call(in, 3, out, 4);
         return s != BASP_OK ? s : basp::launch_balance(*p, logits, ids, mask, coef, loss, counts, slope, ws, stream);

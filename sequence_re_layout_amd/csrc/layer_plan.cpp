@@ -78,6 +78,5 @@ extern "C" size_t basp_balance_workspace_bytes(const basp_expert_plan *p)
         return 0;
     }
     record(BASP_OK);
-    // a sum and a count of every expert, and the number of live tokens
-    return size_t(basp::balance_groups(*p)) * (size_t(2) * p->E + 1) * 4;
+    return size_t(basp::balance_groups(*p)) * 2 * basp::balance_stride(*p) * 4;
 }

@@ -32,15 +32,40 @@ constexpr int kNormGradGroups = 512;
 // again by columns.
 constexpr int64_t kNormGradVecs = 2048;
 
-// The balance loss: tokens are summed in up to 256 work-groups of
-// kBalanceThreads, one partial sum and one count of every expert each, and one
-// more work-group joins them, which reads about 130 GB/s: at most 2^17 of each.
+// The balance loss.  A team of lanes takes a token's scores, up to four vectors a
+// lane: sums over few lanes cost least, and with three or four vectors few lanes
+// are idle.
 constexpr int kBalanceThreads = 1024;
 
+struct LogitRow {
+    int vw;                         // bytes of a vector
+    int64_t row, vecs;              // bytes and vectors of a token
+    int lanes, regs;                // lanes of a team and vectors of a lane
+};
+
+inline LogitRow logit_row(const basp_expert_plan &p)
+{
+    LogitRow r;
+    r.vw = row_vector(p.E, p.ws_es);
+    r.row = int64_t{p.E} * p.ws_es;
+    r.vecs = (r.row + r.vw - 1) / r.vw;
+    r.lanes = r.vecs <= 4 ? 4 : r.vecs <= 32 ? 8 : r.vecs <= 64 ? 16 : r.vecs <= 128 ? 32 : 64;
+    r.regs = int((r.vecs + r.lanes - 1) / r.lanes);
+    return r;
+}
+
+// Tokens are summed in up to 256 work-groups of kBalanceThreads, one partial sum
+// and one count of every expert each, at most 2^17 of each; one more work-group
+// joins them.  What one work-group does in a few steps is not worth that launch.
 inline int balance_groups(const basp_expert_plan &p)
 {
-    const int64_t wanted = (p.T + 15) / 16, most = p.E <= 512 ? 256 : (int64_t{1} << 17) / p.E;
-    return int(wanted < 1 ? 1 : wanted > most ? most : wanted);
+    const int64_t teams = kBalanceThreads / logit_row(p).lanes, most = p.E <= 512 ? 256 : (int64_t{1} << 17) / p.E;
+    const int64_t wanted = p.T <= 4 * teams ? 1 : (p.T + teams - 1) / teams;
+    return int(wanted > most ? most : wanted);
 }
+
+// Numbers of a partial result: a sum of every expert and a count, or the counts
+// and the number of live tokens, in whole groups of four.
+inline int64_t balance_stride(const basp_expert_plan &p) { return (int64_t{p.E} + 1 + 3) / 4 * 4; }
 
 }  // namespace basp
