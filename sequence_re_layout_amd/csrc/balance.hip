@@ -234,10 +234,10 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const BalanceD
 }
 
 // One work-group: four columns a thread, the threads of a column over the partial
-// results, eight of them on their way at a time.
+// results, four of them on their way at a time.
 __global__ __launch_bounds__(kBalanceThreads) void balance_join_kernel(const BalanceParts D)
 {
-    constexpr int AHEAD = 8;
+    constexpr int AHEAD = 4;
     __shared__ __attribute__((aligned(16))) x4 sums[kBalanceThreads];
     __shared__ __attribute__((aligned(16))) i4 counts[kBalanceThreads];
     const int fours = D.stride / 4;
