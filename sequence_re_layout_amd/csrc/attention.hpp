@@ -265,30 +265,39 @@ struct Tile {
             for (int p = 0; p < STEPS; ++p)
                 copy_to_lds<16>(place + (p * THREADS + wave * 64) * 16, rows_of, off[p]);
         } else {
+            // all on their way before the first is stored
+            typedef T xn __attribute__((ext_vector_type(kPer)));
+            xn x[STEPS];
 #pragma unroll
             for (int p = 0; p < STEPS; ++p) {
-                const uint32_t i = p * THREADS + threadIdx.x % THREADS, r = i / kChunks, c = (i % kChunks) ^ swizzle(r);
-                typedef T xn __attribute__((ext_vector_type(kPer)));
-                xn x = {};
-                if (int(r) < rows)
-                    x = chunk(from + uint64_t(r) * token, int(c) * kPer, d);
-                *reinterpret_cast<xn *>(tile + i * 16) = x;
+                const int r = (p * THREADS + threadIdx.x % THREADS) / kChunks, c = (threadIdx.x % kChunks) ^ swizzle(r);
+                x[p] = chunk(from + uint64_t(r < rows ? r : rows - 1) * token, c * kPer, d);        // rows > 0
+                x[p] = r < rows ? x[p] : xn{};
             }
+#pragma unroll
+            for (int p = 0; p < STEPS; ++p)
+                *reinterpret_cast<xn *>(tile + (p * THREADS + threadIdx.x % THREADS) * 16) = x[p];
         }
     }
 
-    // Channels c to c + kPer - 1 of a row of d, zeros after it.
+    // Channels c to c + kPer - 1 of a row of d, zeros after it: what the row's last
+    // chunk has of them, moved down.
     static __device__ inline auto chunk(const char *row, int c, int d)
     {
         typedef T xn __attribute__((ext_vector_type(kPer)));
-        xn x = {};
-        if (c + kPer <= d)
-            return __builtin_bit_cast(xn, *reinterpret_cast<const u32x4m *>(row + c * sizeof(T)));
+        if (d < kPer) {
+            xn x = {};
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (c + i < d)
-                x[i] = reinterpret_cast<const T *>(row)[c + i];
-        return x;
+            for (int i = 0; i < kPer; ++i)
+                if (c + i < d)
+                    x[i] = reinterpret_cast<const T *>(row)[c + i];
+            return x;
+        }
+        const int at = c + kPer <= d ? c : d - kPer;
+        const u32x4 raw = *reinterpret_cast<const u32x4m *>(row + at * sizeof(T));
+        const unsigned __int128 x = __builtin_bit_cast(unsigned __int128, raw);
+        const int down = (c - at) * int(sizeof(T)) * 8;
+        return __builtin_bit_cast(xn, down < 128 ? x >> down : 0);
     }
 };
 

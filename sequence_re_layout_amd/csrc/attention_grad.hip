@@ -37,8 +37,10 @@ struct AttendGradDesc {
     char *dq, *dk, *dv;
     float *rows, *partials;         // rows: [2][lse_elems], -lse / scale and -delta
     int64_t lse_elems;
-    FastDiv by_blocks, by_items, by_sink_chunks, by_chunks;
-    int32_t blocks, items, sink_blocks, sink_chunk, sink_chunks, chunk, chunks, key_blocks;
+    FastDiv by_blocks, by_items, by_sink_chunks, by_chunks, by_sink_cuts, by_cuts;
+    int32_t heads;                  // of a group, that a work-group of the gradient of keys and values takes
+    // chunks: of a block, in all; cuts: of its queries
+    int32_t blocks, items, sink_blocks, sink_chunk, sink_chunks, sink_cuts, chunk, chunks, cuts, key_blocks;
 };
 
 // 128 columns (queries and heads) a work-group, 32 a wave; tiles of keys and
@@ -206,13 +208,13 @@ struct QueryWalk {
     int i, in_head, left, part;
 
     __device__ inline QueryWalk(const AttendShape &A, char *lds_, float *lds_rows_, const AttendGradDesc &D, int64_t at, int64_t row,
-                                int first_position, int begin, int end, int key)
+                                int first_position, int begin, int end, int heads, int key)
         : lds(lds_), lds_rows(lds_rows_), place(lds_place(lds_)), token(A.q_token), d(A.d)
     {
         Rows::template load_offsets<kThreads>(off, token, d);
         count = end - begin;
         tiles = count > 0 ? (count + ROWS - 1) / ROWS : 0;
-        all = tiles * A.ratio;
+        all = tiles * heads;
         start = first_position + begin;
         queries = A.queries;
         // part n of a head holds positions start + 32 * n to start + 32 * n + 31, the
@@ -362,10 +364,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
     if (!sinks)
         end = end < last_key + A.reach - seq.start ? end : last_key + A.reach - seq.start;
     const int length = sinks ? D.sink_chunk : D.chunk;
-    begin += part * length;
+    const int head_part = fastdiv(part, sinks ? D.by_sink_cuts : D.by_cuts);
+    begin += (part - head_part * (sinks ? D.sink_cuts : D.cuts)) * length;
     end = end < begin + length ? end : begin + length;
-    QueryWalk<T, C, ROWS, DIRECT> walk(A, lds, lds_rows, D, shard * A.q_shard + key_head * A.ratio * A.q_head,
-                                       (int64_t{shard} * A.Hl_q + key_head * A.ratio) * A.queries, seq.start, begin, end, wave_key);
+    const int head = key_head * A.ratio + head_part * D.heads;
+    QueryWalk<T, C, ROWS, DIRECT> walk(A, lds, lds_rows, D, shard * A.q_shard + head * A.q_head,
+                                       (int64_t{shard} * A.Hl_q + head) * A.queries, seq.start, begin, end, D.heads, wave_key);
     walk.begin();
     wait_tiles();                   // for the keys, too, and on every way into the loop
     bool more = walk.next();
@@ -626,6 +630,11 @@ extern "C" basp_status basp_attention_grad(const basp_attention_plan *p, const v
         D.sink_chunks = p->sink_chunks;
         D.chunk = p->chunk;
         D.chunks = p->chunks;
+        D.sink_cuts = p->sink_chunks / p->head_parts;
+        D.cuts = p->chunks / p->head_parts;
+        D.heads = p->ratio / p->head_parts;
+        D.by_sink_cuts = basp::make_fastdiv(uint32_t(D.sink_cuts));
+        D.by_cuts = basp::make_fastdiv(uint32_t(D.cuts));
         D.key_blocks = p->key_blocks;
         D.items = p->sink_blocks * p->sink_chunks + (p->key_blocks - p->sink_blocks) * p->chunks;
         D.by_items = basp::make_fastdiv(uint32_t(D.items));

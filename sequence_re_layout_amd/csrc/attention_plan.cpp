@@ -81,11 +81,12 @@ extern "C" basp_attention_plan *basp_attention_plan_create(const basp_plan *layo
     r.splits = 1;
     // Few columns, or few work-groups for the keys that there are: the waves of a
     // work-group share a block of 32 columns, and work-groups share its keys.
-    if (cols <= basp::kStepColumns || (pairs * tile_blocks < kWanted / 4 && seen >= 1024)) {
+    const bool slow = r.es == 4;    // 32 keys take as long as 512 in 16 bits
+    if (cols <= basp::kStepColumns || (pairs * tile_blocks < kWanted / 4 && seen >= (slow ? 64 : 1024))) {
         r.columns = basp::kStepColumns;
         const int64_t groups = pairs * std::max<int64_t>(1, ceil_div(cols, basp::kStepColumns));
-        // at least 256 keys a work-group: two tiles a wave
-        r.splits = int32_t(std::max<int64_t>(1, std::min({ceil_div(kWanted, groups), ceil_div(seen, 256), int64_t{256}})));
+        // at least 256 keys a work-group: two tiles a wave; in fp32 one
+        r.splits = int32_t(std::max<int64_t>(1, std::min({ceil_div(kWanted, groups), ceil_div(seen, slow ? 128 : 256), int64_t{256}})));
     }
     const int64_t blocks = std::max<int64_t>(1, ceil_div(cols, r.columns));
     if (blocks * r.splits > kGroups / pairs)
@@ -108,12 +109,22 @@ extern "C" basp_attention_plan *basp_attention_plan_create(const basp_plan *layo
     const auto cut = [&](int64_t n, int64_t parts) { return std::max(least, ceil_div(ceil_div(n, parts), 64) * 64); };
     const int64_t chunk = cut(in_window, std::max<int64_t>(1, (r.es == 4 ? 2 * kWanted : kWanted) / (pairs * key_blocks)));
     const int64_t sink_chunk = std::max(chunk, cut(queries, ceil_div(2 * kWanted, pairs * std::max<int64_t>(1, sink_blocks))));
+    // Where that still leaves few work-groups with long loops, by heads of a group,
+    // too: in fp32 those of 64 queries are long (8 queries of 8 heads, 128 channels:
+    // 106 -> 38 us), in 16 bits those of 4096.
+    const int64_t whole = sink_blocks * ceil_div(queries, sink_chunk) + (key_blocks - sink_blocks) * ceil_div(in_window, chunk);
+    const int64_t rows = std::min(queries, sink_blocks ? sink_chunk : chunk), much = r.es == 4 ? 64 : 4096;
+    int64_t parts = 1;
+    for (int64_t h = 2; h <= ratio && pairs * whole * parts < kWanted / 2 && ceil_div(rows, 32) * 32 * ratio / parts > much; ++h)
+        if (ratio % h == 0)
+            parts = h;
     r.key_blocks = int32_t(key_blocks);
     r.sink_blocks = int32_t(sink_blocks);
+    r.head_parts = int32_t(parts);
     r.chunk = int32_t(chunk);
-    r.chunks = int32_t(ceil_div(in_window, chunk));
+    r.chunks = int32_t(ceil_div(in_window, chunk) * parts);
     r.sink_chunk = int32_t(sink_chunk);
-    r.sink_chunks = int32_t(std::max<int64_t>(1, ceil_div(queries, sink_chunk)));
+    r.sink_chunks = int32_t(std::max<int64_t>(1, ceil_div(queries, sink_chunk)) * parts);
     const int64_t items = sink_blocks * r.sink_chunks + (key_blocks - sink_blocks) * r.chunks;
     r.grad_blocks = int32_t(tile_blocks);
     if (items > kGroups / pairs || tile_blocks > kGroups / pairs)

@@ -27,9 +27,9 @@ struct basp_attention_plan {
     // blocks of a key head, and work-groups that share the keys of a block
     int32_t columns, blocks, splits;
     // gradient of keys and values: key blocks of a key head, the first of them
-    // with sinks; of those and of the others: queries that a work-group takes, and
-    // such chunks
-    int32_t key_blocks, sink_blocks, sink_chunk, sink_chunks, chunk, chunks;
+    // with sinks; parts of a group's heads; of the two kinds of blocks, queries that
+    // a work-group takes, and such chunks of all parts
+    int32_t key_blocks, sink_blocks, head_parts, sink_chunk, sink_chunks, chunk, chunks;
     int32_t grad_blocks;            // blocks of columns of a key head
     int64_t partials_at;            // in the gradient's workspace, after two numbers a row
     int64_t workspace_bytes, grad_workspace_bytes;
