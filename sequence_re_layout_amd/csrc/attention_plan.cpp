@@ -111,9 +111,10 @@ extern "C" basp_attention_plan *basp_attention_plan_create(const basp_plan *layo
     const int64_t sink_chunk = std::max(chunk, cut(queries, ceil_div(2 * kWanted, pairs * std::max<int64_t>(1, sink_blocks))));
     // Where that still leaves few work-groups with long loops, by heads of a group,
     // too: in fp32 those of 64 queries are long (8 queries of 8 heads, 128 channels:
-    // 106 -> 38 us), in 16 bits those of 4096.
+    // 106 us for a gradient, 60 us by heads), in 16 bits those of 256 (a sequence of
+    // 1024 of 4 heads a key head: 78 us, 68 us by heads).
     const int64_t whole = sink_blocks * ceil_div(queries, sink_chunk) + (key_blocks - sink_blocks) * ceil_div(in_window, chunk);
-    const int64_t rows = std::min(queries, sink_blocks ? sink_chunk : chunk), much = r.es == 4 ? 64 : 4096;
+    const int64_t rows = std::min(queries, sink_blocks ? sink_chunk : chunk), much = r.es == 4 ? 64 : 256;
     int64_t parts = 1;
     for (int64_t h = 2; h <= ratio && pairs * whole * parts < kWanted / 2 && ceil_div(rows, 32) * 32 * ratio / parts > much; ++h)
         if (ratio % h == 0)
