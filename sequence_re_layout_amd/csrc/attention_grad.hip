@@ -10,7 +10,8 @@
 // of five, but every sum has one owner and one order: no atomics, no buffer of
 // fp32 sums of dQ, and the sums over the heads of a group stay in registers.
 // A block of keys with sinks is seen by all later queries; these are cut into
-// chunks of a work-group each, whose sums a third launch adds in their order.
+// chunks of a work-group each, whose sums a third launch adds in their order;
+// other blocks, too, where there are few work-groups.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -44,7 +45,10 @@ struct AttendGradDesc {
 };
 
 // 128 columns (queries and heads) a work-group, 32 a wave; tiles of keys and
-// values as in the forward pass.
+// values as in the forward pass.  Three products a tile: matrix units are busy
+// half of the time, next to the exponents and the reads of both forms of the keys
+// from LDS (two sequences of 8192 with a window of 2048, 32 heads of 128 channels
+// in bf16: 790 us).
 template <typename T, int C, bool DIRECT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void attend_dq_kernel(const AttendGradDesc D)
 {
@@ -311,7 +315,10 @@ struct QueryWalk {
 // go through LDS, the next one on its way while one is used.  Where the keys'
 // sums take half of the registers that two waves of a SIMD have (16-bit types,
 // over 64 channels), the values are kept in LDS instead, and tiles are of 32
-// queries to leave room for them.
+// queries to leave room for them.  Four products a tile, and what it reads from
+// LDS is as much for each wave: two sequences of 8192 with a window of 2048, 32
+// heads of 128 channels in bf16, 1100 us with matrix units busy 48% of the time,
+// 1467 us with the values in registers, some of which were spilled.
 template <typename T, int C, bool DIRECT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void attend_dkv_kernel(const AttendGradDesc D)
 {

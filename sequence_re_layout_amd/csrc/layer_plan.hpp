@@ -26,10 +26,10 @@ inline int float_bytes(basp_dtype t)
 }
 
 // Work-groups whose rows' shares of the weight's gradient are summed apart: two
-// a compute unit (32768 x 2048 in bf16: see norm.hip).
+// a compute unit.
 constexpr int kNormGradGroups = 512;
-// Vectors that the one-pass gradient holds in registers; longer rows are read
-// again by columns.
+// Vectors of 16 bytes that the one-pass gradient holds in registers; longer rows
+// are read again by columns.
 constexpr int64_t kNormGradVecs = 2048;
 
 // The balance loss.  A team of lanes takes a token's scores, up to four vectors a
