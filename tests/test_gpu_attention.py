@@ -96,6 +96,12 @@ CASES = {
     "groups": dict(N=4, B=4, G=2, S=66, Hq=4, Hkv=4, d=64, window=30),
     "long_chunks": dict(S=2100, d=64, window=300, sinks=4),
     "long_whole": dict(S=1500, d=128, dtype="fp16"),
+    "heads_apart": dict(S=300, d=64, Hq=8, Hkv=1, window=60, sinks=2, dtype="fp32"),
+    "heads_and_sinks_apart": dict(S=520, d=128, Hq=6, Hkv=1, window=200, sinks=130),
+    "heads_apart_whole": dict(S=700, d=40, Hq=12, Hkv=2, dtype="fp16"),
+    "few_rows_many_heads": dict(N=2, S=8, d=80, Hq=32, Hkv=4, dtype="fp32"),
+    "three_channels": dict(S=75, d=3, Hq=2, window=40),
+    "channels_past_a_chunk": dict(S=75, d=11, Hq=2, Hkv=1, dtype="fp16"),
     "sharp": dict(S=300, d=64, Hq=2, sharp=30.0),
     "sharp_fp16": dict(S=300, d=128, Hq=2, sharp=30.0, dtype="fp16"),
 }
@@ -156,6 +162,7 @@ STEPS = {
     "more_than_a_block": dict(B=1, S=1500, d=64, Hq=8, Hkv=1, queries=9),
     "prompt_on_a_long_cache": dict(B=1, S=4000, d=64, Hq=2, Hkv=1, queries=70),
     "odd_rows": dict(B=2, S=900, d=20, Hq=3, Hkv=1, queries=2, dtype="bf16"),
+    "two_blocks_fp32": dict(B=2, S=305, d=96, Hq=16, Hkv=2, queries=5, dtype="fp32"),
     "tiny_cache": dict(B=2, S=3, d=64, Hq=2, Hkv=1, queries=2),
 }
 

@@ -55,6 +55,10 @@ NORMS = [  # T, D, dtype, weights, bias, mean of the rows, shift of the buffers
     (3, 16400, "bf16", "fp32", True, 0.0, 0),
     (2, 40001, "fp32", "bf16", True, 1.0, 0),
     (5000, 16, "bf16", "fp32", True, 0.0, 0),
+    (1100, 4200, "bf16", "fp32", True, 0.0, 0),
+    (530, 5001, "fp32", "fp32", True, 0.0, 1),
+    (520, 9000, "fp16", "fp16", False, 0.0, 0),
+    (300, 12000, "fp32", "bf16", True, 1.0, 0),
 ]
 
 
@@ -175,6 +179,11 @@ BALANCES = [  # T, K, E, dtype, id_bytes, share masked, share of ids outside
     (90, 1, 1024, "fp32", 8, 0.0, 0.0),
     (20000, 2, 16, "fp32", 8, 0.1, 0.0),
     (9000, 4, 513, "fp16", 4, 0.1, 0.1),
+    (400, 2, 408, "bf16", 8, 0.1, 0.0),
+    (400, 3, 700, "fp32", 8, 0.0, 0.1),
+    (3000, 2, 128, "fp32", 4, 0.1, 0.0),
+    (70, 2, 96, "fp32", 8, 0.1, 0.0),
+    (2, 2, 1000, "fp16", 8, 0.0, 0.0),
 ]
 
 
