@@ -684,8 +684,8 @@ void basp_attention_plan_destroy(basp_attention_plan *plan); /* NULL is allowed 
 basp_status basp_attention_plan_query(const basp_attention_plan *plan, basp_attention_info *info);
 
 /*
- * o and lse (NULL: not wanted).  scale must be finite and positive
- * (BASP_ERR_INVALID).
+ * o and lse (NULL: not wanted).  scale from 2^-100 to 2^100, here and in the
+ * gradient (BASP_ERR_INVALID): lse / scale and scale * log2(e) are fp32 numbers.
  */
 basp_status basp_attention(const basp_attention_plan *plan, const void *q, const void *k, const void *v,
                            const int32_t *starts, const int32_t *lengths, float scale, void *o, float *lse, void *ws,
@@ -696,7 +696,8 @@ basp_status basp_attention(const basp_attention_plan *plan, const void *q, const
  * wrote them:  with dP = <dout, v_j> and dS = P (dP - <dout, o>),
  *   dq = scale sum_j dS_j k_j,   dk_j = scale sum dS_j q,   dv_j = sum P_j dout,
  * the latter two over the rows of all query heads of the key head that see j.
- * Every element is written; zeros for keys that no row sees.
+ * Every element is written; zeros for keys that no row sees.  P and dS are rounded
+ * to the inputs' type for their products (a dS beyond fp16 is an infinity).
  */
 basp_status basp_attention_grad(const basp_attention_plan *plan, const void *q, const void *k, const void *v, const void *o,
                                 const float *lse, const void *dout, const int32_t *starts, const int32_t *lengths, float scale,

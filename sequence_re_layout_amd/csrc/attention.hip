@@ -427,7 +427,7 @@ extern "C" basp_status basp_attention(const basp_attention_plan *p, const void *
                                       void *stream)
 {
     return basp::timed_call([&]() -> basp_status {
-        if (!p || !(scale > 0.f) || std::isinf(scale))
+        if (!p || !basp::scale_in_range(scale))
             return BASP_ERR_INVALID;
         const int64_t nq = p->q_elems * p->es, nkv = p->kv_elems * p->es, each = int64_t{4} * p->B;
         const CallBuf in[] = {{q, nq, p->es}, {k, nkv, p->es}, {v, nkv, p->es}, {starts, starts ? each : 0, 4},

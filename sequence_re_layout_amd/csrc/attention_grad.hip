@@ -607,7 +607,7 @@ extern "C" basp_status basp_attention_grad(const basp_attention_plan *p, const v
                                            float scale, void *dq, void *dk, void *dv, void *ws, void *stream)
 {
     return basp::timed_call([&]() -> basp_status {
-        if (!p || !(scale > 0.f) || std::isinf(scale))
+        if (!p || !basp::scale_in_range(scale))
             return BASP_ERR_INVALID;
         const int64_t nq = p->q_elems * p->es, nkv = p->kv_elems * p->es, each = int64_t{4} * p->B;
         const CallBuf in[] = {{q, nq, p->es}, {k, nkv, p->es}, {v, nkv, p->es}, {o, nq, p->es}, {lse, p->lse_elems * 4, 4},

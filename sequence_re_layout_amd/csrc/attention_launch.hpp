@@ -8,6 +8,9 @@
 
 namespace basp {
 
+// lse / scale, and the scores that are not worth a rescaling, are fp32 numbers.
+inline bool scale_in_range(float scale) { return scale >= 0x1p-100f && scale <= 0x1p100f; }
+
 inline AttendShape attend_shape(const basp_attention_plan &p, const int32_t *starts, const int32_t *lengths, float scale)
 {
     AttendShape A = {};

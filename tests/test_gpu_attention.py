@@ -246,7 +246,7 @@ def test_same_bits_every_time(name):
 def test_scales():
     """Scores of any size: the running maximum moves up all along, and weights
     below the type's range."""
-    for scale, dtype in ((3.0, "fp16"), (1e-6, "bf16"), (20.0, "fp32"), (2.0 ** -60, "bf16")):
+    for scale, dtype in ((3.0, "fp16"), (1e-6, "bf16"), (20.0, "fp32"), (2.0 ** -60, "bf16"), (2.0 ** -100, "fp32")):
         c = lc.Attention(S=333, d=64, Hq=2, Hkv=1, dtype=dtype)
         q, k, v, do = c.inputs(1)
         k *= torch.linspace(0.0, 2.0, c.S, dtype=torch.float64)[:, None].expand(c.S, c.d)

@@ -164,7 +164,7 @@ def test_attention_refuses_pointers(dtype, es):
         optional_refusals(lambda *a: lib.basp_attention_grad(h, *a[:8], 0.1, *a[8:], None), bwd, (6, 7))
 
 
-@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan"), float("inf")])
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan"), float("inf"), 2.0 ** -101, 2.0 ** 101, 1e-45, 3e38])
 def test_attention_refuses_scales(scale):
     lib = b.library()
     h = b.basp_attention_plan_create(layout(), 64, 8)
