@@ -9,17 +9,16 @@
 // A team of lanes holds a token's scores in registers, each lane the same
 // columns of every token, and adds up the columns of p as it goes.  The scores
 // are read once; small next to what a launch costs, so one launch makes a
-// partial sum and a count a work-group, and one work-group joins them, or the
-// only one does it itself.  Sums are fp32 in a fixed order, counts whole numbers.
+// partial sum and a count a work-group, and a second one joins them, or the only
+// work-group does it itself.  Sums are fp32 in a fixed order, counts whole numbers.
 // Scores of -infinity have no share and no gradient; rounding is to the scores'
 // type at the end.
 //
 // Vector instructions bound it as much as reading does, so teams are small: 32768
 // tokens x 320 in bf16 take 11 us in teams of 16 lanes with three vectors (21 MB),
 // 13 us as a wave a token; the gradient 11 us, 15 us as a wave a token.  The join
-// is one work-group's rate of reading: 7 us for 256 x 128, 10 us for 256 x 320;
-// half as many partial sums cost the first launch as much as they save here.
-// 250 tokens x 8: 4 us.
+// takes 7 us, a round of loads and an exchange between work-groups; one work-group
+// needed 10 us for 256 x 320, at its rate of reading.  250 tokens x 8: 4 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -39,7 +38,8 @@ namespace {
 // Partial results [groups][2][stride], the counts' last number the live tokens,
 // and what becomes of them.
 struct BalanceParts {
-    float *parts;
+    float *parts, *shares;          // shares: of the loss, by the join's work-groups
+    uint32_t *came;                 // those that are done
     float *loss, *slope;
     int32_t *counts;
     int32_t groups, E, K, stride;
@@ -113,40 +113,23 @@ struct Scores {
 typedef float x4 __attribute__((ext_vector_type(4)));
 typedef int i4 __attribute__((ext_vector_type(4)));
 
-// Counts, slope and loss by one work-group, from the sums and counts of columns 4 c
-// to 4 c + 3 in the threads that have some.
-__device__ inline void finish_balance(const BalanceParts &D, int c, bool mine, x4 P, i4 n)
+// Counts and slopes of the experts 4 c to 4 c + 3 from their sums and counts; their
+// share of the loss.
+__device__ inline float finish_experts(const BalanceParts &D, int c, int live, x4 P, i4 n)
 {
-    constexpr int WAVES = kBalanceThreads / 64;
-    __shared__ float wave_loss[WAVES];
-    __shared__ int live_tokens;
-    if (mine && c == D.E / 4)
-        live_tokens = n[D.E % 4];
-    lds_barrier();
+    const float L = float(live);
     float term = 0.f;
-    if (mine) {
-        const float L = float(live_tokens);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = 4 * c + i;
-            if (e < D.E) {
-                const float slope = live_tokens ? D.coef * (float(n[i]) * float(D.E) / (float(D.K) * L)) / L : 0.f;
-                D.counts[e] = n[i];
-                D.slope[e] = slope;
-                term += live_tokens ? slope * P[i] : 0.f;
-            }
+    for (int i = 0; i < 4; ++i) {
+        const int e = 4 * c + i;
+        if (e < D.E) {
+            const float slope = live ? D.coef * (float(n[i]) * float(D.E) / (float(D.K) * L)) / L : 0.f;
+            D.counts[e] = n[i];
+            D.slope[e] = slope;
+            term += live ? slope * P[i] : 0.f;
         }
     }
-    term = team_fold<64>(term, [](float a, float b) { return a + b; });
-    if ((threadIdx.x & 63) == 0)
-        wave_loss[threadIdx.x >> 6] = term;
-    lds_barrier();
-    if (threadIdx.x == 0) {
-        float loss = 0.f;
-        for (int w = 0; w < WAVES; ++w)
-            loss += wave_loss[w];
-        *D.loss = loss;
-    }
+    return term;
 }
 
 template <typename E, int VW, int LANES, int R>
@@ -232,65 +215,98 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const BalanceD
             sums[off / sizeof(E) + c % N] = sum;
     }
     if (!alone) {
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            *out.came = 0;          // for the next launch
         for (int e = threadIdx.x; e <= out.E; e += kBalanceThreads)
             reinterpret_cast<int *>(parts)[out.stride + e] = hist[e];
         return;
     }
     lds_barrier();
     const int c = threadIdx.x;
-    const bool mine = 4 * c < out.stride;
-    finish_balance(out, c, mine, mine ? reinterpret_cast<const x4 *>(total)[c] : x4{}, mine ? reinterpret_cast<const i4 *>(hist)[c] : i4{});
+    float term = 0.f;
+    if (4 * c < out.stride)
+        term = finish_experts(out, c, hist[out.E], reinterpret_cast<const x4 *>(total)[c], reinterpret_cast<const i4 *>(hist)[c]);
+    term = team_fold<64>(term, [](float a, float b) { return a + b; });
+    if ((threadIdx.x & 63) == 0)
+        part[wave][0] = term;
+    lds_barrier();
+    if (threadIdx.x == 0) {
+        float loss = 0.f;
+        for (int w = 0; w < WAVES; ++w)
+            loss += part[w][0];
+        *out.loss = loss;
+    }
 }
 
-// One work-group: four columns a thread, the threads of a column over the partial
-// results, four of them on their way at a time.
+// kJoinColumns experts a work-group, four a thread, and 128 threads over the
+// partial results.  The last work-group to come adds the shares of the loss, all in
+// their order.
 __global__ __launch_bounds__(kBalanceThreads) void balance_join_kernel(const BalanceParts D)
 {
-    constexpr int AHEAD = 4;
-    __shared__ __attribute__((aligned(16))) x4 sums[kBalanceThreads];
-    __shared__ __attribute__((aligned(16))) i4 counts[kBalanceThreads];
-    const int fours = D.stride / 4;
-    int columns = 1;                // threads side by side
-    while (columns < fours)
-        columns *= 2;
-    const int c = threadIdx.x & (columns - 1), slices = kBalanceThreads / columns;
+    constexpr int ACROSS = kJoinColumns / 4, SLICES = kBalanceThreads / ACROSS, WAVES = kBalanceThreads / 64, ROUNDS = kBalanceGroups / SLICES;
+    __shared__ __attribute__((aligned(16))) x4 sums[WAVES][ACROSS];
+    __shared__ __attribute__((aligned(16))) i4 counts[WAVES][ACROSS];
+    __shared__ int live_tokens;
+    const int fours = D.stride / 4, c = blockIdx.x * ACROSS + threadIdx.x % ACROSS, slice = threadIdx.x / ACROSS;
+    if (threadIdx.x == 0)
+        live_tokens = 0;
+    const float *const from = D.parts + 4 * (c < fours ? c : 0);
+    x4 x[ROUNDS];
+    i4 y[ROUNDS];
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+        const int g = slice + i * SLICES < D.groups ? slice + i * SLICES : 0;
+        x[i] = *reinterpret_cast<const x4 *>(from + int64_t{g} * 2 * D.stride);
+        y[i] = *reinterpret_cast<const i4 *>(from + (int64_t{g} * 2 + 1) * D.stride);
+    }
+    lds_barrier();
+    if (int(threadIdx.x) < D.groups)
+        atomicAdd(&live_tokens, reinterpret_cast<const int *>(D.parts)[(int64_t{threadIdx.x} * 2 + 1) * D.stride + D.E]);
     x4 P = {0.f, 0.f, 0.f, 0.f};
     i4 n = {0, 0, 0, 0};
-    const float *const from = D.parts + 4 * (c < fours ? c : 0);
-    for (int g = threadIdx.x / columns; g < D.groups; g += AHEAD * slices) {
-        x4 x[AHEAD];
-        i4 y[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int at = g + i * slices < D.groups ? g + i * slices : g;
-            x[i] = *reinterpret_cast<const x4 *>(from + int64_t{at} * 2 * D.stride);
-            y[i] = *reinterpret_cast<const i4 *>(from + (int64_t{at} * 2 + 1) * D.stride);
+    for (int i = 0; i < ROUNDS; ++i)
+        if (slice + i * SLICES < D.groups) {
+            P += x[i];
+            n += y[i];
         }
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            if (g + i * slices < D.groups) {
-                P += x[i];
-                n += y[i];
-            }
-    }
-    for (int d = columns; d < 64; d *= 2)
+    for (int d = ACROSS; d < 64; d *= 2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             P[i] += __shfl_xor(P[i], d);
             n[i] += __shfl_xor(n[i], d);
         }
-    // then by waves, or by rows of threads where those are wider
-    const int wide = columns < 64 ? 64 : columns;
-    sums[threadIdx.x] = P;
-    counts[threadIdx.x] = n;
+    if ((threadIdx.x & 63) < ACROSS) {
+        sums[threadIdx.x >> 6][threadIdx.x % ACROSS] = P;
+        counts[threadIdx.x >> 6][threadIdx.x % ACROSS] = n;
+    }
     lds_barrier();
-    const bool mine = int(threadIdx.x) < fours;
-    if (mine)
-        for (int j = wide; j < kBalanceThreads; j += wide) {
-            P += sums[j + c];
-            n += counts[j + c];
+    if (threadIdx.x >= 64)
+        return;
+    float term = 0.f;
+    if (threadIdx.x < ACROSS && c < fours) {
+        for (int w = 1; w < WAVES; ++w) {
+            P += sums[w][threadIdx.x];
+            n += counts[w][threadIdx.x];
         }
-    finish_balance(D, c, mine, P, n);
+        term = finish_experts(D, c, live_tokens, P, n);
+    }
+    const auto add = [](float a, float b) { return a + b; };
+    term = team_fold<64>(term, add);
+    uint32_t came = 0;
+    if (threadIdx.x == 0) {
+        __hip_atomic_store(D.shares + blockIdx.x, term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        came = __hip_atomic_fetch_add(D.came, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (__builtin_amdgcn_readfirstlane(came) != gridDim.x - 1)
+        return;
+    float share = 0.f;              // gridDim.x is at most 33
+    if (threadIdx.x < gridDim.x)
+        share = __hip_atomic_load(D.shares + threadIdx.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    share = team_fold<64>(share, add);
+    if (threadIdx.x == 0)
+        *D.loss = share;
 }
 
 struct BalanceGradDesc {
@@ -399,12 +415,16 @@ basp_status launch_balance(const basp_expert_plan &p, const void *logits, const 
     const LogitRow r = logit_row(p);
     const BalanceShape shape = BASP_BY_ROW(balance_shape, p.weight_dtype, r.vw, r);
     const int groups = balance_groups(p);
+    float *const parts = static_cast<float *>(ws);
+    const int64_t partials = 2 * groups * balance_stride(p);
     const BalanceDesc D = {static_cast<const char *>(logits), ids, mask, p.T, (p.T + groups - 1) / groups, uint32_t(r.row),
                            uint32_t(r.vecs), p.id_bytes == 8, make_fastdiv(uint32_t(p.K)),
-                           {static_cast<float *>(ws), loss, slope, counts, groups, p.E, p.K, int32_t(balance_stride(p)), coef}};
+                           {parts, parts + partials + 1, reinterpret_cast<uint32_t *>(parts + partials), loss, slope, counts,
+                            groups, p.E, p.K, int32_t(balance_stride(p)), coef}};
     basp_status s = launch_kernel(shape.sum, dim3(groups), kBalanceThreads, D, stream, true, groups == 1);
     if (s == BASP_OK && groups > 1)
-        s = launch_kernel(reinterpret_cast<const void *>(balance_join_kernel), dim3(1), kBalanceThreads, D.out, stream, false, true);
+        s = launch_kernel(reinterpret_cast<const void *>(balance_join_kernel), dim3(balance_joins(p)), kBalanceThreads,
+                          D.out, stream, false, true);
     return s;
 }
 

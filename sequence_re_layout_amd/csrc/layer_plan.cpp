@@ -78,5 +78,6 @@ extern "C" size_t basp_balance_workspace_bytes(const basp_expert_plan *p)
         return 0;
     }
     record(BASP_OK);
-    return size_t(basp::balance_groups(*p)) * 2 * basp::balance_stride(*p) * 4;
+    // and how many of the work-groups that join them are done, with their results
+    return (size_t(basp::balance_groups(*p)) * 2 * basp::balance_stride(*p) + 1 + basp::balance_joins(*p)) * 4;
 }

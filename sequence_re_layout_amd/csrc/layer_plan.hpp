@@ -54,15 +54,20 @@ inline LogitRow logit_row(const basp_expert_plan &p)
     return r;
 }
 
-// Tokens are summed in up to 256 work-groups of kBalanceThreads, one partial sum
-// and one count of every expert each, at most 2^17 of each; one more work-group
-// joins them.  What one work-group does in a few steps is not worth that launch.
+// Tokens are summed in up to kBalanceGroups work-groups of kBalanceThreads, one
+// partial sum and one count of every expert each; a second launch joins them.
+// What one work-group does in a few steps is not worth that launch.
+constexpr int kBalanceGroups = 256;
+
 inline int balance_groups(const basp_expert_plan &p)
 {
-    const int64_t teams = kBalanceThreads / logit_row(p).lanes, most = p.E <= 512 ? 256 : (int64_t{1} << 17) / p.E;
-    const int64_t wanted = p.T <= 4 * teams ? 1 : (p.T + teams - 1) / teams;
-    return int(wanted > most ? most : wanted);
+    const int64_t teams = kBalanceThreads / logit_row(p).lanes, wanted = p.T <= 4 * teams ? 1 : (p.T + teams - 1) / teams;
+    return int(wanted > kBalanceGroups ? kBalanceGroups : wanted);
 }
+
+// Experts of a work-group that joins partial results; such work-groups.
+constexpr int kJoinColumns = 32;
+inline int balance_joins(const basp_expert_plan &p) { return p.E / kJoinColumns + 1; }
 
 // Numbers of a partial result: a sum of every expert and a count, or the counts
 // and the number of live tokens, in whole groups of four.
