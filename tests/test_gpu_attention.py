@@ -227,7 +227,7 @@ def test_infinities_and_nan_stay_where_they_are_seen(dtype, d, what):
         assert not bool((over & fine).any()), name
 
 
-@pytest.mark.parametrize("name", ["sinks_of_two_blocks", "long_chunks", "token_order_fp32", "whole_128"])
+@pytest.mark.parametrize("name", ["sinks_of_two_blocks", "heads_apart", "heads_and_sinks_apart", "long_chunks", "token_order_fp32", "whole_128"])
 def test_same_bits_every_time(name):
     c = lc.Attention(**CASES[name])
     q, k, v, do = c.inputs(9)

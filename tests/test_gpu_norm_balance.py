@@ -281,3 +281,22 @@ def test_balance_counts_are_those_of_the_sort():
     b.basp_balance_loss(plan, torch.zeros(T, E, device="cuda"), ids, None, 1.0, torch.empty(1, device="cuda"), mine,
                         torch.empty(E, device="cuda"), ws)
     assert torch.equal(counts, mine)
+
+
+def test_balance_same_bits_every_time():
+    """Work-groups that finish in any order, on a workspace that holds anything."""
+    T, K, E = 9000, 4, 700
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x = torch.randn(T, E, generator=g, device="cuda")
+    ids = torch.randint(0, E, (T, K), generator=g, device="cuda")
+    plan = b.basp_expert_plan_create(T, K, E, 1, weight_dtype=b.BASP_FP32)
+    first = None
+    for fill in range(0, 256, 15):
+        ws = torch.full((plan.balance_bytes,), fill, dtype=torch.uint8, device="cuda")
+        loss, slope = torch.empty(1, device="cuda"), torch.empty(E, device="cuda")
+        counts = torch.empty(E, dtype=torch.int32, device="cuda")
+        b.basp_balance_loss(plan, x, ids, None, 1.0, loss, counts, slope, ws)
+        out = [t.clone() for t in (loss, slope, counts)]
+        first = first or out
+        assert all(torch.equal(a, c) for a, c in zip(first, out))
