@@ -708,10 +708,12 @@ __device__ inline void wave_order()
     __builtin_amdgcn_wave_barrier();
 }
 
-// lse from a maximum in the scores' units and the sum relative to it.
+// lse from a maximum in the scores' units and the sum relative to it (to 0 where
+// no score is above -infinity).  A maximum passes over NaN, the sum does not: a row
+// that sees a score of NaN has NaN.
 __device__ inline float log_sum(float m, float l, const AttendShape &A)
 {
-    return m == -INFINITY ? -INFINITY : (m * A.scale_log2 + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    return ((m == -INFINITY ? 0.f : m * A.scale_log2) + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
 // Four channels of a result's rows as stored.
