@@ -348,7 +348,7 @@ class _BalanceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, logits, ids, mask, coef):
         dev = logits.device
-        loss, slope = torch.empty(1, device=dev), torch.empty(plan.info["E"], device=dev)
+        loss, slope = (torch.empty(n, dtype=torch.float32, device=dev) for n in (1, plan.info["E"]))
         counts = torch.empty(plan.info["E"], dtype=torch.int32, device=dev)
         b.basp_balance_loss(plan, logits, ids, mask, coef, loss, counts, slope,
                             torch.empty(plan.balance_bytes, dtype=torch.uint8, device=dev))
