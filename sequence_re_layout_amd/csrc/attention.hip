@@ -63,11 +63,10 @@ struct Running {
 };
 
 // The columns of a wave along its way through tiles of ROWS keys.  m is left
-// behind a column's maximum by up to 8 in the exponent of two, which keeps weights
-// below 2^8 (in range of fp16 too) and their relative precision: after the first
-// tile it hardly ever moves.  Where it does, the loop is left, the sums are
-// rescaled and the tile begun again (a branch in the loop would copy them in every
-// tile, see wild_rows).
+// behind a column's maximum by up to A.slack, about 8 in the exponent of two, which
+// keeps weights in range (weight_base): after the first tile it hardly ever moves.
+// Where it does, the loop is left, the sums are rescaled and the tile begun again (a
+// branch in the loop would copy them in every tile, see wild_rows).
 template <typename T, int C, int ROWS, typename Walk>
 __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C / 16], int position, Running<C / 32> &run, Walk &walk)
 {
@@ -119,14 +118,15 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
                 for (int i = 0; i < 16; ++i)
                     most = fmaxf(most, s[t][i]);
             most = fmaxf(most, other_half(most));
-            behind = __ballot(most > run.m + A.slack);
+            // a sum would be rounded, by more than fp16's range allows at large scores
+            behind = __ballot(kShifted<T> ? most - run.m > A.slack : most > run.m + A.slack);
             if (behind)
                 break;
             if (wild)
                 break;
             // weights and their products in steps of 16 keys: exponentials are
             // taken while the matrix unit is at the step before
-            const float base = run.m == -INFINITY ? 0.f : run.m * A.scale_log2;
+            const float base = weight_base<T>(run.m, A);
 #pragma unroll
             for (int t = 0; t < TILES; ++t) {
                 if (t + 1 < TILES)
@@ -145,7 +145,7 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
         if (behind) {
             run.rescale(most, A.scale_log2);
         } else {
-            const float base = run.m == -INFINITY ? 0.f : run.m * A.scale_log2;
+            const float base = weight_base<T>(run.m, A);
 #pragma unroll
             for (int j = 0; j < ROWS / 16; ++j)
                 weigh(s[j / 2], j % 2, base);
@@ -175,7 +175,7 @@ __device__ inline void finish_columns(const AttendDesc &D, const Column &col, ui
         store_four<T>(o, 32 * ((from + j) / 16) + row_of((from + j) % 16, half), A.d, y);
     }
     if (D.lse && from == 0 && half == 0)
-        D.lse[col.row(A, shard)] = col.live ? log_sum(m, total, A) : -INFINITY;
+        D.lse[col.row(A, shard)] = col.live ? log_sum<T>(m, total, A) : -INFINITY;
 }
 
 // 128 columns a work-group, 32 a wave; its four waves share tiles of 64 keys (32
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
             store_four<T>(o, 32 * b + row_of(i, half), A.d, x);
         }
     if (D.lse && half == 0)
-        D.lse[col.row(A, shard)] = col.live ? log_sum(run.m, l, A) : -INFINITY;
+        D.lse[col.row(A, shard)] = col.live ? log_sum<T>(run.m, l, A) : -INFINITY;
 }
 
 // A wave's way of its own: every step-th tile of 32 keys from number `from` on.

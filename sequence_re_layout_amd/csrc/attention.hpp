@@ -27,6 +27,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #define BASP_HD __host__ __device__
 #include "attention_plan.hpp"
@@ -708,12 +709,29 @@ __device__ inline void wave_order()
     __builtin_amdgcn_wave_barrier();
 }
 
+// Weights are kept times 2^7 in fp16, of which results hold nothing: its normal
+// numbers end at 2^-14 and its smallest is 2^-24, so that weights keep all bits from
+// 2^-21 of the largest on and are there from 2^-31 on.  Many small weights next to a
+// large one (a sink) count for as much as the large one.
+template <typename T> constexpr bool kShifted = std::is_same<T, _Float16>::value;
+
+// What is taken from the exponents (to the base of 2) of a column with maximum m.
+// Where weights are shifted, it is no less than the exponent of m, 7 (8, where 7 is
+// between two fp32 numbers) aside: the largest weight stays below 2^16 at any score.
+template <typename T>
+__device__ inline float weight_base(float m, const AttendShape &A)
+{
+    const float base = m == -INFINITY ? 0.f : m * A.scale_log2;
+    return kShifted<T> ? fmaf(fabsf(base), 0x1p-23f, base) - 7.f : base;
+}
+
 // lse from a maximum in the scores' units and the sum relative to it (to 0 where
 // no score is above -infinity).  A maximum passes over NaN, the sum does not: a row
 // that sees a score of NaN has NaN.
+template <typename T>
 __device__ inline float log_sum(float m, float l, const AttendShape &A)
 {
-    return ((m == -INFINITY ? 0.f : m * A.scale_log2) + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    return (weight_base<T>(m, A) + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
 // Four channels of a result's rows as stored.

@@ -41,7 +41,8 @@ inline AttendShape attend_shape(const basp_attention_plan &p, const int32_t *sta
     A.by_pairs = make_fastdiv(A.pairs);
     A.scale = scale;
     A.scale_log2 = float(double(scale) * 1.4426950408889634);
-    A.slack = float(8.0 / (double(scale) * 1.4426950408889634));
+    // 8 in the exponent of two, and with the shift of fp16's weights in their range
+    A.slack = float((p.dtype == BASP_FP16 ? 7.5 : 8.0) / (double(scale) * 1.4426950408889634));
     return A;
 }
 

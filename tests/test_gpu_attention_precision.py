@@ -64,3 +64,89 @@ def test_lse_of_a_key_of_nan(dtype):
     torch.cuda.synchronize()
     got = torch.isnan(call.lse.t.cpu())
     assert bool(got[41]) and int(got.sum()) == 1
+
+
+def dominant(c, size):
+    """A first key 17.5 above all others, which are equal; its value is 0, theirs
+    are 1.  Exact o of position p and dv of the keys but the first for do = size."""
+    q, k, v, do = (torch.zeros_like(x) for x in c.inputs(0))
+    q[..., 0] = 1.0
+    k[:, :, 0, 0] = 17.5
+    v[:, :, 1:] = 1.0
+    do[:] = size
+    p = (c.S - c.queries + torch.arange(c.queries)).double()
+    w = math.exp(-17.5)
+    o = p * w / (1 + p * w)
+    # row p gives each of the keys 1 to p the weight w / (1 + p w)
+    each = torch.zeros(c.S, dtype=torch.float64)
+    each[c.S - c.queries:] = w / (1 + p * w)
+    return (q, k, v, do), o, size * each.flip(0).cumsum(0).flip(0) * (c.hq // c.hkv)
+
+
+DOMINANT = {
+    "prompt": dict(S=4096, d=64, Hq=4, Hkv=4, dtype="fp16"),
+    "prompt_heads": dict(S=4096, d=128, Hq=8, Hkv=4, dtype="fp16"),
+    "few_tokens": dict(S=9000, d=64, Hq=8, Hkv=1, queries=2, dtype="fp16"),
+    "block_of_keys_shared": dict(S=700, d=40, Hq=2, Hkv=1, dtype="fp16"),
+}
+
+
+@pytest.mark.parametrize("name", DOMINANT)
+def test_small_weights_in_fp16(name):
+    """Many weights of 2^-25 of the largest.  They are rounded to fp16 after a
+    shift by 2^7, so each is off by half a step of its size or by 2^-25 / 2^7 of the
+    largest weight."""
+    c = lc.Attention(**DOMINANT[name])
+    (q, k, v, do), want, _ = dominant(c, 1.0)
+    call = Call(c, q, k, v, do, scale=1.0)
+    call.forward()
+    torch.cuda.synchronize()
+    o = c.shaped(call.o.t.cpu().double(), c.hq, c.queries)
+    # the weights' rounding, the result's, and fp32: 2 (n + 8) 2^-24 of it
+    allowed = (c.S * 2.0 ** -32 + want * (2 * H16 + 2 * (c.S + 8) * lc.U) + 2.0 ** -25)[None, None, :, None]
+    assert bool(((o - want[None, None, :, None]).abs() <= allowed).all())
+
+
+@pytest.mark.parametrize("S,queries", [(600, 600), (600, 3), (4000, 4000)])
+@pytest.mark.parametrize("first", [False, True])
+def test_scores_of_fifty_million_in_fp16(S, queries, first):
+    """Every key's score is 10^4 and more from its neighbours': a row's value is that
+    of its largest."""
+    c = lc.Attention(S=S, d=64, queries=queries, dtype="fp16")
+    q, k, v, do = c.inputs(1)
+    q[:], k[:] = 0.0, 0.0
+    step = 64 if S < 1000 else 16
+    j = torch.arange(S).double()
+    q[..., 0], k[..., 0] = 60000.0, (step * (-1 - j if first else 1 + j)).half().double()
+    call = Call(c, q, k, v, do, scale=2.0 ** -6)
+    call.forward()
+    torch.cuda.synchronize()
+    top = torch.zeros(queries, dtype=torch.long) if first else torch.arange(S - queries, S)
+    if S > 1000:        # past 2^11 * 16 two neighbours have the same key
+        top = top[:2000]
+    o = c.shaped(call.o.t.cpu().double(), 1, queries)[0, 0, :len(top)]
+    # one weight of 1: its rounding, the result's, and the sum's
+    assert bool(((o - v[0, 0, top]).abs() <= 2.5 * H16 * v[0, 0, top].abs()).all())
+    lse, want = call.lse.t.cpu().double()[:len(top)], 60000.0 / 64 * k[0, 0, top, 0]
+    assert bool(((lse - want).abs() <= 8 * lc.U * want.abs()).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("large", [2.0 ** 10, 2.0 ** 16, 2.0 ** 20, 2.0 ** 22, 2.0 ** 23, 2.0 ** 24, 2.0 ** 25])
+def test_weights_of_large_scores_stay_in_range(large, d):
+    """Scores that rise by 0 to 40 a row above a large one, which fp32 holds in steps
+    of up to 4: a mean of ones is 1."""
+    c = lc.Attention(B=4, S=1000, d=d, Hq=4, Hkv=4, dtype="fp16")
+    q, k, v, do = c.inputs(1)
+    noise = torch.rand(k.shape[:-1], dtype=torch.float64, generator=torch.Generator().manual_seed(int(large))) * 40
+    for sign in (1.0, -1.0):
+        q[:], k[:], v[:] = 0.0, 0.0, 1.0
+        q[..., 0], q[..., 1] = 1024.0, 1.0
+        k[..., 0] = sign * 2.0
+        k[..., 1] = (noise / (large / 2048.0)).half().double()
+        q, k = q.half().double(), k.half().double()
+        call = Call(c, q, k, v, do, scale=large / 2048.0)
+        call.forward()
+        torch.cuda.synchronize()
+        # weights and the result are rounded once each
+        assert bool(((call.o.t.double() - 1.0).abs() <= 3 * H16).all()), sign
