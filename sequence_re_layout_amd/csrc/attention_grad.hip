@@ -31,6 +31,12 @@ constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kFewTiles = 3;        // tiles of keys up to which <dO, O> is summed again from P and dP
 
+// P, at most 1 here, is taken times 2^12 in the products of the gradient of V in
+// fp16: it keeps all bits from 2^-26 on, where 50000 equal weights are below fp16's
+// normal numbers as they are.  2^4 is left for the rounding of large scores.
+template <typename T> constexpr float kWeightExponent = kShifted<T> ? 12.f : 0.f;
+template <typename T> constexpr float kOneWeight = kShifted<T> ? 0x1p-12f : 1.f;
+
 struct AttendGradDesc {
     AttendShape shape;
     const char *q, *k, *v, *o, *dout;
@@ -444,8 +450,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                p[0][i] = __builtin_amdgcn_exp2f(p[0][i] * A.scale_log2);
-                ds[0][i] *= p[0][i];
+                p[0][i] = __builtin_amdgcn_exp2f(kShifted<T> ? fmaf(p[0][i], A.scale_log2, kWeightExponent<T>) : p[0][i] * A.scale_log2);
+                ds[0][i] *= p[0][i] * kOneWeight<T>;
             }
             if (walk.hides()) {
                 // the rows from `first` on that see the key: up to `last`
@@ -502,7 +508,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
 #pragma unroll
         for (int b = 0; b < C / 32; ++b) {
             store_key<T, 16>(A, D.dk, shard, key_head, key, 32 * b, half, dk[b], A.scale);
-            store_key<T, 16>(A, D.dv, shard, key_head, key, 32 * b, half, dv[b], 1.f);
+            store_key<T, 16>(A, D.dv, shard, key_head, key, 32 * b, half, dv[b], kOneWeight<T>);
         }
         return;
     }
@@ -561,7 +567,8 @@ __global__ __launch_bounds__(kThreads) void attend_grad_join_kernel(const Attend
                 sums[i] += x[n][i];
     }
     const int key = int(D.first_block + block) * kKeyBlock + int(wave & 3) * 32 + int(lane & 31);
-    store_key<T, 8>(A, wave < 4 ? D.dk : D.dv, shard, key_head, key, int(part) * 16, int(lane >> 5), sums, wave < 4 ? A.scale : 1.f);
+    store_key<T, 8>(A, wave < 4 ? D.dk : D.dv, shard, key_head, key, int(part) * 16, int(lane >> 5), sums,
+                    wave < 4 ? A.scale : kOneWeight<T>);
 }
 
 // --------------------------------------------------------------- launches --

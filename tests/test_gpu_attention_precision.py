@@ -150,3 +150,33 @@ def test_weights_of_large_scores_stay_in_range(large, d):
         torch.cuda.synchronize()
         # weights and the result are rounded once each
         assert bool(((call.o.t.double() - 1.0).abs() <= 3 * H16).all()), sign
+
+
+@pytest.mark.parametrize("name", DOMINANT)
+def test_small_weights_in_the_gradient_of_values(name):
+    c = lc.Attention(**DOMINANT[name])
+    (q, k, v, do), _, want = dominant(c, 1024.0)
+    call = Call(c, q, k, v, do, scale=1.0)
+    call.forward()
+    call.backward()
+    torch.cuda.synchronize()
+    dv = c.shaped(call.dv.t.cpu().double(), c.hkv, c.S)[:, :, 1:]
+    want = want[1:, None]
+    # rounding of the weights and of the result; lse and the exponent in fp32: 17.5
+    # and its logarithm to the base of 2 have a half step of 2^-20 at most, four times
+    n = c.queries * c.hq // c.hkv
+    assert bool(((dv - want).abs() <= want * (2 * H16 + 4 * 2.0 ** -20 + 2 * (n + 4) * lc.U) + 2.0 ** -25).all())
+
+
+@pytest.mark.parametrize("keys", [3000, 50000])
+def test_equal_weights_in_the_gradient_of_values(keys):
+    """1/50000 is below fp16's normal numbers: a step there is 1/335 of it."""
+    c = lc.Attention(S=keys, d=64, queries=1, dtype="fp16")
+    q, k, v, do = (torch.zeros_like(x) for x in c.inputs(0))
+    do[:] = 100.0
+    call = Call(c, q, k, v, do, scale=1.0)
+    call.forward()
+    call.backward()
+    torch.cuda.synchronize()
+    dv = call.dv.t.cpu().double()
+    assert bool(((dv - 100.0 / keys).abs() <= 100.0 / keys * (2 * H16 + 4 * 2.0 ** -20) + 2.0 ** -25).all())
