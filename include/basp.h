@@ -697,7 +697,8 @@ basp_status basp_attention(const basp_attention_plan *plan, const void *q, const
  *   dq = scale sum_j dS_j k_j,   dk_j = scale sum dS_j q,   dv_j = sum P_j dout,
  * the latter two over the rows of all query heads of the key head that see j.
  * Every element is written; zeros for keys that no row sees.  P and dS are rounded
- * to the inputs' type for their products (a dS beyond fp16 is an infinity).
+ * to the inputs' type for their products, in fp16 times powers of two, so that small
+ * ones keep their bits next to dout and large ones are in range.
  */
 basp_status basp_attention_grad(const basp_attention_plan *plan, const void *q, const void *k, const void *v, const void *o,
                                 const float *lse, const void *dout, const int32_t *starts, const int32_t *lengths, float scale,

@@ -37,17 +37,67 @@ constexpr int kFewTiles = 3;        // tiles of keys up to which <dO, O> is summ
 template <typename T> constexpr float kWeightExponent = kShifted<T> ? 12.f : 0.f;
 template <typename T> constexpr float kOneWeight = kShifted<T> ? 0x1p-12f : 1.f;
 
+// dS may have any size next to dout: P is small where a row sees many keys.  In
+// fp16 it is rounded times a power of two, which the sums are freed of at the end.
+// In the gradient of q that is a column's own.  The sizes of its dO and of the first
+// values give one that hardly ever has to move: most dS are below 2^9 then, and all
+// bits are kept where P is 2^-21 and more.  It comes down where a |dS| is above 2^15,
+// so that nothing overflows.  A wave leaves the largest |dS| of its 32 columns for
+// the gradients of k and v, which take the power of a chunk's queries from them, so
+// that their largest is 2^11 to 2^12: all bits are kept down to 2^-25 of it.  (To
+// find it on the way there, too, takes more registers than there are: 1350 us
+// instead of 1120 for two sequences of 8192, 128 channels and a window of 2048.)
+//
+// The power that takes numbers of exponent `of` to `to`, 2^60 at most.
+__device__ inline float power_for(int to, int of) { return __builtin_amdgcn_ldexpf(1.f, to - of < 60 ? to - of : 60); }
+
+// The largest of `most` and a lane's numbers.
+__device__ inline float largest(const f32x16 &x, float most)
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        most = fmaxf(most, fabsf(x[i]));
+    return most;
+}
+
+// Whether it is to come down; infinities stay, such sums have no finite value.
+__device__ inline bool too_large(float most) { return most > 0x1p15f && most < INFINITY; }
+
+// The exponent of two of a positive number.
+__device__ inline int exponent_of(float x) { return int(__builtin_bit_cast(uint32_t, x) >> 23) - 127; }
+
+template <int BLOCKS>
+__device__ inline void times(f32x16 (&sums)[BLOCKS], float factor)
+{
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            sums[b][i] *= factor;
+}
+
+// The largest of a wave's finite numbers that are not below 0.
+__device__ inline float largest_of_wave(float x)
+{
+    x = x < INFINITY ? x : 0.f;
+#pragma unroll
+    for (int far = 1; far < 64; far *= 2)
+        x = fmaxf(x, __shfl_xor(x, far));
+    return x;
+}
+
 struct AttendGradDesc {
     AttendShape shape;
     const char *q, *k, *v, *o, *dout;
     const float *lse;
     char *dq, *dk, *dv;
     float *rows, *partials;         // rows: [2][lse_elems], -lse / scale and -delta
+    float *most;                    // in fp16: [pairs][units], the largest |dS| of 32 columns
     int64_t lse_elems;
     FastDiv by_blocks, by_items, by_sink_chunks, by_chunks, by_sink_cuts, by_cuts;
     int32_t heads;                  // of a group, that a work-group of the gradient of keys and values takes
     // chunks: of a block, in all; cuts: of its queries
-    int32_t blocks, items, sink_blocks, sink_chunk, sink_chunks, sink_cuts, chunk, chunks, cuts, key_blocks;
+    int32_t blocks, units, items, sink_blocks, sink_chunk, sink_chunks, sink_cuts, chunk, chunks, cuts, key_blocks;
 };
 
 // 128 columns (queries and heads) a work-group, 32 a wave; tiles of keys and
@@ -140,8 +190,24 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
     walk.begin();
     wait_tiles();                   // for the columns, too, and on every way into the loop
     bool more = walk.next();
+    float power = 1.f, most = 0.f;
+    if constexpr (kShifted<T>) {
+        const Vec8<T> some = *reinterpret_cast<const Vec8<T> *>(walk.values() + lane * 16);
+        float of_g = 0.f, of_v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            of_v = fmaxf(of_v, fabsf(float(some[i])));
+#pragma unroll
+            for (int c = 0; c < C / 16; ++c)
+                of_g = fmaxf(of_g, fabsf(float(g[c][i])));
+        }
+        of_g = fmaxf(of_g, other_half(of_g));
+        power = power_for(7, exponent_of(of_g) + exponent_of(more ? largest_of_wave(of_v) : 0.f));
+        delta *= power;
+    }
     while (more) {
         f32x16 ds[1];
+        bool beyond = false;
         for (;;) {
             f32x16 dp;
             const bool wild = walk.hides() && wild_rows<T, C, KEYS, 32>(walk.keys(), walk.row0());
@@ -151,8 +217,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
             pin_reads();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                ds[0][i] *= dp[i] - delta;
-            if (wild)
+                ds[0][i] *= kShifted<T> ? fmaf(dp[i], power, -delta) : dp[i] - delta;
+            if constexpr (kShifted<T>) {
+                most = largest(ds[0], most);
+                beyond = __ballot(too_large(most));
+            }
+            if (beyond | wild)
                 break;
             operands.add(sums, 0, ds[0]);
             operands.add(sums, 1, ds[0]);
@@ -160,10 +230,24 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
             if (!more)
                 break;
         }
-        if (more) {
+        if (beyond) {               // a lane and its opposite alike, and then these keys again
+            most = fmaxf(most, other_half(most));
+            const float down = too_large(most) ? __builtin_amdgcn_ldexpf(1.f, 7 - exponent_of(most)) : 1.f;
+            power *= down;
+            delta *= down;
+            most *= down;
+            times(sums, down);
+        } else if (more) {
             add_wild_rows<T, C, KEYS, 32>(sums, walk.keys(), walk.row0(), ds);
             more = walk.next();
         }
+    }
+    if constexpr (kShifted<T>) {
+        const float here = largest_of_wave(most / power);
+        const uint32_t unit = first / 32 + wave;
+        if (lane == 0 && unit < uint32_t(D.units))
+            D.most[int64_t{pair} * D.units + unit] = here;
+        times(sums, 1.f / power);
     }
     if (!col.exists)
         return;
@@ -384,6 +468,15 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
     QueryWalk<T, C, ROWS, DIRECT> walk(A, lds, lds_rows, D, shard * A.q_shard + head * A.q_head,
                                        (int64_t{shard} * A.Hl_q + head) * A.queries, seq.start, begin, end, D.heads, wave_key);
     walk.begin();
+    float power = 1.f;
+    if constexpr (kShifted<T>) {
+        const uint32_t units_end = end > begin ? (uint32_t(end) * A.ratio + 31) / 32 : 0;
+        float most = 0.f;
+        for (uint32_t u = uint32_t(begin) * A.ratio / 32 + lane; u < units_end; u += 64)
+            most = fmaxf(most, D.most[int64_t{pair} * D.units + u]);
+        power = power_for(11, int(scalar(uint32_t(exponent_of(largest_of_wave(most))))));
+    }
+    const float factor = kOneWeight<T> * power;     // from weights as they are taken to those of dS
     wait_tiles();                   // for the keys, too, and on every way into the loop
     bool more = walk.next();
     while (more) {
@@ -451,7 +544,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 p[0][i] = __builtin_amdgcn_exp2f(kShifted<T> ? fmaf(p[0][i], A.scale_log2, kWeightExponent<T>) : p[0][i] * A.scale_log2);
-                ds[0][i] *= p[0][i] * kOneWeight<T>;
+                ds[0][i] *= kShifted<T> ? p[0][i] * factor : p[0][i];
             }
             if (walk.hides()) {
                 // the rows from `first` on that see the key: up to `last`
@@ -504,6 +597,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
             more = walk.next();
         }
     }
+    if constexpr (kShifted<T>)
+        times(dk, 1.f / power);
     if ((sinks ? D.sink_chunks : D.chunks) == 1) {
 #pragma unroll
         for (int b = 0; b < C / 32; ++b) {
@@ -636,6 +731,8 @@ extern "C" basp_status basp_attention_grad(const basp_attention_plan *p, const v
         D.dv = static_cast<char *>(dv);
         D.rows = static_cast<float *>(ws);
         D.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + p->partials_at);
+        D.most = D.rows + 2 * p->lse_elems;
+        D.units = p->grad_units;
         D.lse_elems = p->lse_elems;
         D.blocks = p->grad_blocks;
         D.by_blocks = basp::make_fastdiv(uint32_t(p->grad_blocks));

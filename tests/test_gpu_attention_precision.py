@@ -180,3 +180,122 @@ def test_equal_weights_in_the_gradient_of_values(keys):
     torch.cuda.synchronize()
     dv = call.dv.t.cpu().double()
     assert bool(((dv - 100.0 / keys).abs() <= 100.0 / keys * (2 * H16 + 4 * 2.0 ** -20) + 2.0 ** -25).all())
+
+
+def two_norm(got, want, extra=0.0):
+    """Relative error in 2-norm, and half a smallest subnormal of fp16 an element of it."""
+    return float((got - want).norm() / want.norm()), 2.0 ** -25 * want.numel() ** 0.5 / float(want.norm())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [3e2, 1.0, 1e-2, 1e-3, 1e-4, 1e-6])
+def test_small_gradients_in_fp16(size, d):
+    """dS of thousands of keys is far below dout.  Its rounding to fp16 and those of
+    the weights, of o in delta and of the result are off by half a step each, in
+    the mean square by 1 / sqrt(3) of that: two half steps in 2-norm, and the
+    result's smallest subnormal."""
+    c = lc.Attention(S=6000, d=d, Hq=2, Hkv=1, queries=64, dtype="fp16")
+    q, k, v, do = c.inputs(6)
+    for shift in (64.0, 1.0 / 64.0):        # the scores stay, dq and dk in turn are in range
+        call = Call(c, q / shift, k * shift, v, (do * size).half().double())
+        call.forward()
+        call.backward()
+        torch.cuda.synchronize()
+        want = c.exact(call_values(call.q, c, c.hq, c.queries), call_values(call.k, c, c.hkv, c.S), v, call_values(call.do, c, c.hq, c.queries),
+                       [c.S - c.queries], [c.S], call.scale)
+        for name, got in (("dq", call.dq), ("dk", call.dk), ("dv", call.dv)):
+            exact = want[name][0]
+            off, least = two_norm(c.shaped(got.t.cpu().double(), exact.shape[1], exact.shape[2]), exact)
+            assert off <= 2 * H16 + least, (name, shift, off, least)
+
+
+def call_values(x, c, heads, tokens):
+    return c.shaped(x.cpu().double(), heads, tokens)
+
+
+GROWING = {
+    "prompt": dict(S=600, d=64, Hq=2, Hkv=1, dtype="fp16"),
+    "prompt_128": dict(S=500, d=128, Hq=2, Hkv=1, window=90, sinks=3, dtype="fp16"),
+    "by_heads": dict(S=300, d=64, Hq=8, Hkv=1, dtype="fp16"),
+    "ragged": dict(S=333, d=33, Hq=2, Hkv=2, window=100, dtype="fp16", order="token"),
+}
+
+
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("name", GROWING)
+def test_gradients_of_growing_size(name, down):
+    """dout from 2^-20 to 2^12 along the queries, and keys whose scores rise: a
+    column's largest dS moves all along."""
+    c = lc.Attention(**GROWING[name])
+    q, k, v, do = c.inputs(3)
+    ramp = torch.linspace(-20, 12, c.S, dtype=torch.float64)
+    do = (do * torch.exp2(ramp.flip(0) if down else ramp)[:, None]).to(c.dtype).double()
+    k = (k * torch.linspace(0.0, 2.0, c.S, dtype=torch.float64)[:, None]).to(c.dtype).double()
+    call = Call(c, q, k, v, do)
+    call.forward()
+    call.backward()
+    call.check(c.exact(q, k, v, do, [0], [c.S], call.scale))
+
+
+def test_gradients_beyond_fp16_on_the_way():
+    """dS of 10^5 and more, whose sums times the scale are in range."""
+    c = lc.Attention(S=200, d=64, Hq=2, Hkv=1, window=8, dtype="fp16")
+    q, k, v, do = c.inputs(6)
+    do, v = (do * 8000).half().double(), v * 16
+    call = Call(c, q, k, v, do, scale=2.0 ** -7)
+    call.forward()
+    call.backward()
+    want = c.exact(q, k, v, do, [0], [c.S], call.scale)
+    torch.cuda.synchronize()
+    for name, got, heads in (("dq", call.dq, c.hq), ("dk", call.dk, c.hkv)):
+        got = c.shaped(got.t.cpu().double(), heads, c.S)
+        off, least = two_norm(got, want[name][0])
+        assert bool(torch.isfinite(got).all()) and off <= 2 * H16 + least, (name, off)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -12, 2.0 ** 6])
+@pytest.mark.parametrize("of", [dict(S=3000, d=64, Hq=2, queries=32), dict(S=200, d=128, Hq=4, Hkv=2, window=20), dict(S=700, d=40, Hq=1)])
+def test_gradients_by_size_of_the_values(size, of):
+    """Values far from 1, of which one key's are larger still."""
+    c = lc.Attention(dtype="fp16", **{"Hkv": 1, **of})
+    q, k, v, do = c.inputs(8)
+    v = v * size
+    v[:, :, c.S // 2] *= 64.0
+    v, do = v.half().double(), (do / 1024).half().double()
+    q, k = q / 8, k * 8
+    call = Call(c, q, k, v, do)
+    call.forward()
+    call.backward()
+    torch.cuda.synchronize()
+    want = c.exact(q, k, v, do, [c.S - c.queries], [c.S], call.scale)
+    for name, got, heads in (("dq", call.dq, c.hq), ("dk", call.dk, c.hkv)):
+        exact, err = want[name]
+        got = c.shaped(got.t.cpu().double(), heads, exact.shape[2])
+        off, least = two_norm(got, exact)
+        # a half step each of the weights, of o in delta, of dS and of the result
+        assert off <= 4 * H16 + least, (name, off, least)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", ["v", "do", "k"])
+def test_infinities_beside_large_gradients(what, d):
+    """A column whose largest dS is infinite next to one whose dS has to come down."""
+    c = lc.Attention(S=260, d=d, Hq=4, Hkv=2, window=45, sinks=2, dtype="fp16")
+    q, k, v, do = c.inputs(5)
+    v, do = v * 16, (do * 8000).half().double()
+    x = {"v": v, "do": do, "k": k}[what]
+    x[0, 0, 100, 0] = math.inf
+    x[0, 1, 200] = NAN
+    call = Call(c, q, k, v, do, scale=2.0 ** -8)
+    call.forward()
+    call.backward()
+    torch.cuda.synchronize()
+    want = c.exact(q, k, v, do, [0], [c.S], call.scale)
+    for name, got, heads in (("dq", call.dq, c.hq), ("dk", call.dk, c.hkv), ("dv", call.dv, c.hkv)):
+        exact, err = want[name]
+        got = c.shaped(got.t.cpu().double(), heads, c.S)
+        fine = torch.isfinite(exact) & torch.isfinite(err) & (exact.abs() + err < 65000)
+        assert bool(torch.isfinite(got[fine]).all()), name
+        if what != "k":     # a score of -infinity has the weight 0, and 0 times the key's infinity may be left out or NaN
+            assert not bool(torch.isfinite(got[~torch.isfinite(exact)]).any()), name
+        assert bool(((got - exact).abs()[fine] <= (err + H16 * (exact.abs() + err) + 2.0 ** -25)[fine]).all()), name
