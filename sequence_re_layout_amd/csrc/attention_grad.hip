@@ -29,6 +29,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
+// Whether scores begin from -lse / scale in the gradients of k and v (QueryWalk).
+template <typename T> constexpr bool kFromLse = sizeof(T) == 2;
+
 constexpr int kFewTiles = 3;        // tiles of keys up to which <dO, O> is summed again from P and dP
 
 // P, at most 1 here, is taken times 2^12 in the products of the gradient of V in
@@ -91,7 +94,7 @@ struct AttendGradDesc {
     const char *q, *k, *v, *o, *dout;
     const float *lse;
     char *dq, *dk, *dv;
-    float *rows, *partials;         // rows: [2][lse_elems], -lse / scale and -delta
+    float *rows, *partials;         // rows: [2][lse_elems], -lse / scale (or log2(e) * -lse) and -delta
     float *most;                    // in fp16: [pairs][units], the largest |dS| of 32 columns
     int64_t lse_elems;
     FastDiv by_blocks, by_items, by_sink_chunks, by_chunks, by_sink_cuts, by_cuts;
@@ -177,7 +180,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
     }
     delta += other_half(delta);
     if (col.live && half == 0) {
-        D.rows[col.row(A, shard)] = -lse_at / A.scale;
+        D.rows[col.row(A, shard)] = kFromLse<T> ? -lse_at / A.scale : -lse;
         D.rows[D.lse_elems + col.row(A, shard)] = -delta;
     }
 
@@ -284,8 +287,11 @@ __device__ inline void store_key(const AttendShape &A, char *to, uint32_t shard,
 
 // A work-group's way through the queries [begin, end) of each head of a group and
 // their gradients, as KeyWalk's through keys: tiles of ROWS in LDS, used in parts
-// of 32, with -lse / scale and -delta of each query.  The products begin from
-// these instead of 0, so that P = exp(scale * result) and dS = P * result.
+// of 32, with two numbers of each query.  The products begin from -lse / scale and
+// -delta instead of 0, so that P = exp(scale * result) and dS = P * result.  In fp32
+// the first would round every step of a product at lse's size instead of the score's
+// (3000 equal keys of 128 channels: dv off by 2.5e-6 of it, 7e-7 this way): there
+// log2(e) * -lse is added afterwards.
 template <typename T, int C, int ROWS, bool DIRECT>
 struct QueryWalk {
     typedef Tile<T, C, ROWS> Rows;
@@ -296,7 +302,7 @@ struct QueryWalk {
     int use_from, use_to, all_from, all_to;     // parts of a head in which some query sees some of the wave's keys, and all all
     int start;                                  // position of the first query
     const char *q, *g;                          // of the next tile to fetch
-    const float *numbers;                       // -lse / scale (first wave) or -delta (second) of its first query
+    const float *numbers;                       // of its first query: for the scores (first wave), or -delta (second)
     int64_t step, turn;                         // from tile to tile, and from a head's last to the next one's first
     int queries, fetched, fetch_left;
     int i, in_head, left, part;
@@ -379,15 +385,18 @@ struct QueryWalk {
     __device__ inline int row0() const { return ROWS > 32 ? part * 32 : 0; }
     __device__ inline int position() const { return start + 32 * in_head; }
     __device__ inline int rows() const { return left - row0(); }
-    // The numbers of the rows of a result's registers.
+    // The numbers of the rows of a result's registers, and of four of them from j on.
+    typedef float x4 __attribute__((ext_vector_type(4)));
+    __device__ inline x4 four_numbers(int which, int half, int j) const
+    {
+        return *reinterpret_cast<const x4 *>(lds_rows + (i & 1) * 128 + which * 64 + row0() + 4 * half + row_of(j, 0));
+    }
     __device__ inline f32x16 numbers_at(int which, int half) const
     {
-        typedef float x4 __attribute__((ext_vector_type(4)));
-        const float *const from = lds_rows + (i & 1) * 128 + which * 64 + row0() + 4 * half;
         f32x16 r;
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
-            const x4 x = *reinterpret_cast<const x4 *>(from + row_of(j, 0));
+            const x4 x = four_numbers(which, half, j);
             r[j] = x[0];
             r[j + 1] = x[1];
             r[j + 2] = x[2];
@@ -535,16 +544,29 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
                 of_queries.read(queries, row0);
                 pin_reads();
                 of_grads.read(grads, row0);
-                p[0] = of_queries.times(k, walk.lse(half));
+                p[0] = of_queries.times(k, kFromLse<T> ? walk.lse(half) : f32x16{});
                 pin_reads();
                 ds[0] = of_grads.times(v, walk.delta(half));
                 operands.read(grads, row0);
                 pin_reads();
             }
+            if constexpr (kFromLse<T>) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                p[0][i] = __builtin_amdgcn_exp2f(kShifted<T> ? fmaf(p[0][i], A.scale_log2, kWeightExponent<T>) : p[0][i] * A.scale_log2);
-                ds[0][i] *= kShifted<T> ? p[0][i] * factor : p[0][i];
+                for (int i = 0; i < 16; ++i) {
+                    p[0][i] = __builtin_amdgcn_exp2f(kShifted<T> ? fmaf(p[0][i], A.scale_log2, kWeightExponent<T>) : p[0][i] * A.scale_log2);
+                    ds[0][i] *= kShifted<T> ? p[0][i] * factor : p[0][i];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const auto lse = walk.four_numbers(0, half, j);
+#pragma unroll
+                    for (int i = j; i < j + 4; ++i) {
+                        p[0][i] = __builtin_amdgcn_exp2f(fmaf(p[0][i], A.scale_log2, lse[i - j]));
+                        ds[0][i] *= p[0][i];
+                    }
+                    pin_reads();        // few of these in registers at a time
+                }
             }
             if (walk.hides()) {
                 // the rows from `first` on that see the key: up to `last`

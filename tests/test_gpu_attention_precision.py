@@ -299,3 +299,23 @@ def test_infinities_beside_large_gradients(what, d):
         if what != "k":     # a score of -infinity has the weight 0, and 0 times the key's infinity may be left out or NaN
             assert not bool(torch.isfinite(got[~torch.isfinite(exact)]).any()), name
         assert bool(((got - exact).abs()[fine] <= (err + H16 * (exact.abs() + err) + 2.0 ** -25)[fine]).all()), name
+
+
+def test_equal_weights_in_fp32_gradients():
+    """3000 keys of nearly equal scores, 128 channels.  lse is 8: its half step,
+    2^-21, and that of the exponent to the base of 2, three times in its way, are
+    each off by 1 / sqrt(3) in the mean square, 5e-7 together.  Sums of 32 rows add a
+    fifth of that.  dk is a sum of dS, whose dP are off by less: 2 sqrt(128) 2^-24
+    / sqrt(3) of their size, 8e-7."""
+    c = lc.Attention(S=3000, d=128, queries=32, dtype="fp32")
+    q, k, v, do = c.inputs(4, 0.05)
+    call = Call(c, q, k, v, do)
+    call.forward()
+    call.backward()
+    torch.cuda.synchronize()
+    want = c.exact(q, k, v, do, [c.S - c.queries], [c.S], call.scale)
+    off = {}
+    for name, got, heads in (("dv", call.dv, c.hkv), ("dk", call.dk, c.hkv), ("dq", call.dq, c.hq)):
+        exact = want[name][0]
+        off[name] = float((c.shaped(got.t.cpu().double(), heads, exact.shape[2]) - exact).norm() / exact.norm())
+    assert off["dv"] <= 1e-6 and off["dk"] <= 1.3e-6, off
