@@ -676,8 +676,9 @@ typedef struct basp_attention_info {
  *   BASP_ERR_INVALID       layout NULL, or an argument out of range
  *   BASP_ERR_INDIVISIBLE   Hq no multiple of Hkv
  *   BASP_ERR_UNSUPPORTED   dtype BASP_INT32, d above 128, S of 2^29 or more,
- *                          (Hq / Hkv) * queries of 2^30 or more, or more
- *                          than 2^24 - 1 work-groups in a launch
+ *                          (Hq / Hkv) * queries of 2^30 or more, tokens (the
+ *                          Hl_q heads of one) of more than 2^24 bytes, or
+ *                          more than 2^24 - 1 work-groups in a launch
  */
 basp_attention_plan *basp_attention_plan_create(const basp_plan *layout, int64_t queries, int64_t window, int64_t sinks);
 void basp_attention_plan_destroy(basp_attention_plan *plan); /* NULL is allowed */

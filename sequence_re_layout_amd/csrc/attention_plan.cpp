@@ -35,7 +35,7 @@ extern "C" basp_attention_plan *basp_attention_plan_create(const basp_plan *layo
         return refuse(BASP_ERR_UNSUPPORTED);
     const int64_t ratio = layout->Hl_q / layout->Hl_kv, shards = int64_t{layout->N} * layout->Bl;
     const int64_t pairs = shards * layout->Hl_kv, token = int64_t{layout->Hl_q} * layout->d * layout->es;
-    // a tile's rows are within 31 bits of its first
+    // in token order a tile's rows are within 31 bits of its first; one limit for both orders
     if (ratio * queries >= int64_t{1} << 30 || pairs > kGroups || token > int64_t{1} << 24)
         return refuse(BASP_ERR_UNSUPPORTED);
 
