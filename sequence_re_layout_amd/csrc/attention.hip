@@ -281,7 +281,7 @@ struct StepWalk {
     __device__ inline int key_end() const { return tiles.first(i) + tiles.rows(i); }
     __device__ inline bool hides() const
     {
-        return tiles.rows(i) < KEYS || how_seen(A, mine.low, mine.high, tiles.first(i), tiles.rows(i)) != Seen::all;
+        return tiles.rows(i) < KEYS || !all_seen(A, mine.low, mine.high, tiles.first(i), tiles.rows(i));
     }
 };
 

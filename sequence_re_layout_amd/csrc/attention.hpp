@@ -466,15 +466,6 @@ struct Sight {
     {
     }
     __device__ inline bool operator()(int at) const { return (at <= last) & ((at > before) | (at < firsts)); }
-    // Moved on by n keys.
-    __device__ inline Sight at(int n) const
-    {
-        Sight s = *this;
-        s.last -= n;
-        s.before -= n;
-        s.firsts -= n;
-        return s;
-    }
 };
 
 // Tiles of keys that positions [low, high] see, KEYS each: first those of the
@@ -499,15 +490,11 @@ struct KeyTiles {
     }
 };
 
-// How positions [low, high] of a wave see the keys [first, first + rows).
-enum class Seen { none, some, all };
-
-__device__ inline Seen how_seen(const AttendShape &A, int low, int high, int first, int rows)
+// Whether all positions [low, high] of a wave see all keys [first, first + rows).
+__device__ inline bool all_seen(const AttendShape &A, int low, int high, int first, int rows)
 {
     const int last = first + rows - 1;
-    if (low > high || first > high || (low - last >= A.reach && first >= A.firsts))
-        return Seen::none;
-    return last <= low && (high - first < A.reach || last < A.firsts) ? Seen::all : Seen::some;
+    return low <= high && last <= low && (high - first < A.reach || last < A.firsts);
 }
 
 // The positions of columns [first, first + n) that are within the sequence: their

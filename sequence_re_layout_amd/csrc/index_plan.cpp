@@ -17,11 +17,6 @@ constexpr int64_t kVocabLimit = int64_t{1} << 30;
 constexpr int64_t kSumGroups = 1024;                // four work-groups a compute unit
 constexpr int64_t kSumLimit = int64_t{1} << 23;     // work-groups of a launch's 32-bit extent
 
-int float_size(basp_dtype t)
-{
-    return t == BASP_BF16 || t == BASP_FP16 ? 2 : t == BASP_FP32 ? 4 : 0;
-}
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
 
@@ -69,7 +64,7 @@ basp_status check_call(const CallBuf *in, int nin, const CallBuf *out, int nout)
 extern "C" basp_expert_plan *basp_expert_plan_create(int64_t T, int K, int E, int64_t D, int align, int id_bytes,
                                                      basp_dtype dtype, basp_dtype weight_dtype)
 {
-    const int es = float_size(dtype), wes = float_size(weight_dtype);
+    const int es = basp::float_bytes(dtype), wes = basp::float_bytes(weight_dtype);
     if (T < 0 || K < 1 || E < 1 || D < 1 || align < 1 || (id_bytes != 4 && id_bytes != 8) || !es || !wes) {
         record(BASP_ERR_INVALID);
         return nullptr;
@@ -140,7 +135,7 @@ extern "C" basp_embed_plan *basp_embed_plan_create(const basp_plan *layout, int6
                                                    int64_t padding, int id_bytes, basp_dtype dtype,
                                                    basp_dtype grad_dtype)
 {
-    const int es = float_size(dtype), ges = float_size(grad_dtype);
+    const int es = basp::float_bytes(dtype), ges = basp::float_bytes(grad_dtype);
     if (T < 0 || V < 1 || D < 1 || padding < -1 || padding >= V || (id_bytes != 4 && id_bytes != 8) || !es || !ges ||
         (layout && T != int64_t{layout->B} * layout->S)) {
         record(BASP_ERR_INVALID);

@@ -100,6 +100,12 @@ BASP_HD inline int padded_count(int n, int to)
     return to == 1 ? n : int((uint32_t(n) + uint32_t(to) - 1) / uint32_t(to) * uint32_t(to));
 }
 
+// Bytes of a number of a floating type, 0 for any other.
+inline int float_bytes(basp_dtype t)
+{
+    return t == BASP_BF16 || t == BASP_FP16 ? 2 : t == BASP_FP32 ? 4 : 0;
+}
+
 // Rows are read and written in vectors of vw bytes, the widest power of two
 // up to 16 that a row holds one of.  A row of `elems` elements takes
 // ceil(elems / epv) vectors; the last one ends with the row and so overlaps

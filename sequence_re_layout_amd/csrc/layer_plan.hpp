@@ -20,11 +20,6 @@ struct basp_norm_plan {
 
 namespace basp {
 
-inline int float_bytes(basp_dtype t)
-{
-    return t == BASP_BF16 || t == BASP_FP16 ? 2 : t == BASP_FP32 ? 4 : 0;
-}
-
 // Work-groups whose rows' shares of the weight's gradient are summed apart: two
 // a compute unit.
 constexpr int kNormGradGroups = 512;
