@@ -380,9 +380,11 @@ struct SumOperands {
 
 // Where some rows are hidden from some columns, their weight is 0, and a product
 // of 0 and an infinity or NaN would be NaN.  So rows with such numbers
-// (wild_rows) are added up one by one and without the zeros.  The kernels look for
-// them before all else, while few registers are in use, and leave their loop for
-// them: a branch inside it would cost a copy of all sums in every step.
+// (wild_rows) are added up one by one, each to the columns that see it: sees(r) for
+// row r of the N from row0 on.  (A row in sight counts with a weight of 0, too,
+// as it does in a tile that is seen as a whole.)  The kernels look for them before
+// all else, while few registers are in use, and leave their loop for them: a branch
+// inside it would cost a copy of all sums in every step.
 template <typename T, int C, int ROWS, int N>
 __device__ inline bool wild_rows(const char *tile, int row0)
 {
@@ -395,8 +397,8 @@ __device__ inline bool wild_rows(const char *tile, int row0)
     return __ballot(sum != 0.f);
 }
 
-template <typename T, int C, int ROWS, int N, int BLOCKS>
-__device__ inline void add_wild_rows(f32x16 (&sums)[BLOCKS], const char *tile, int row0, const f32x16 (&p)[N / 32])
+template <typename T, int C, int ROWS, int N, int BLOCKS, typename Sees>
+__device__ inline void add_wild_rows(f32x16 (&sums)[BLOCKS], const char *tile, int row0, const f32x16 (&p)[N / 32], Sees sees)
 {
     const int half = (threadIdx.x & 63) >> 5;
 #pragma clang loop unroll(disable)
@@ -408,12 +410,13 @@ __device__ inline void add_wild_rows(f32x16 (&sums)[BLOCKS], const char *tile, i
             w = at == j ? p[j / 16][j % 16] : w;
         const float across = other_half(w);
         w = of == half ? w : across;
+        const bool is = sees(r);
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float x = Tile<T, C, ROWS>::at(tile, row0 + r, 32 * b + row_of(i, half));
-                sums[b][i] = w != 0.f ? fmaf(w, x, sums[b][i]) : sums[b][i];
+                sums[b][i] = is ? fmaf(w, x, sums[b][i]) : sums[b][i];
                 if (i % 4 == 3)         // few of these in registers at a time
                     __builtin_amdgcn_sched_barrier(0);
             }
@@ -454,6 +457,12 @@ __device__ inline Sequence sequence_of(const AttendShape &A, uint32_t shard)
     // farther out, no row has a position within the sequence either
     s.start = s.start < -A.queries ? -A.queries : s.start > A.S ? A.S : s.start;
     return s;
+}
+
+// Whether a position of the sequence sees one of its keys.
+__device__ inline bool visible(const AttendShape &A, int position, int key)
+{
+    return (key <= position) & ((position - key < A.reach) | (key < A.firsts));
 }
 
 // The keys from `first` on that a position sees, of those below `end`: offsets up

@@ -241,7 +241,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
             most *= down;
             times(sums, down);
         } else if (more) {
-            add_wild_rows<T, C, KEYS, 32>(sums, walk.keys(), walk.row0(), ds);
+            add_wild_rows<T, C, KEYS, 32>(sums, walk.keys(), walk.row0(), ds, [&](int r) {
+                return (walk.key() + r < walk.key_end()) & visible(A, col.position, walk.key() + r);
+            });
             more = walk.next();
         }
     }
@@ -547,7 +549,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
                 p[0] = of_queries.times(k, kFromLse<T> ? walk.lse(half) : f32x16{});
                 pin_reads();
                 ds[0] = of_grads.times(v, walk.delta(half));
-                operands.read(grads, row0);
+                if constexpr (kFromLse<T>)
+                    operands.read(grads, row0);
                 pin_reads();
             }
             if constexpr (kFromLse<T>) {
@@ -603,6 +606,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
                 for (int c = 0; c < HALF; ++c)
                     dk[c] = product(other[c], ds1, dk[c]);
             } else {
+                if constexpr (!kFromLse<T>)     // registers are few, and the products long
+                    operands.read(grads, row0);
                 operands.add(dv, 0, p[0]);
                 operands.add(dv, 1, p[0]);
                 operands.read(queries, row0);
@@ -614,8 +619,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
                 break;
         }
         if (more) {
-            add_wild_rows<T, C, ROWS, 32>(dv, walk.grads(), walk.row0(), p);
-            add_wild_rows<T, C, ROWS, 32>(dk, walk.queries_at(), walk.row0(), ds);
+            const auto sees = [&](int r) { return (r < walk.rows()) & visible(A, walk.position() + r, key); };
+            add_wild_rows<T, C, ROWS, 32>(dv, walk.grads(), walk.row0(), p, sees);
+            add_wild_rows<T, C, ROWS, 32>(dk, walk.queries_at(), walk.row0(), ds, sees);
             more = walk.next();
         }
     }
