@@ -150,7 +150,7 @@ __device__ inline void attend_tiles(const AttendShape &A, const Vec8<T> (&q)[C /
             for (int j = 0; j < ROWS / 16; ++j)
                 weigh(s[j / 2], j % 2, base);
             add_wild_rows<T, C, ROWS, ROWS>(run.o, walk.values(), 0, s, [&](int r) {
-                return (walk.key() + r < walk.key_end()) & visible(A, position, walk.key() + r);
+                return walk.key() + r < walk.key_end() && visible(A, position, walk.key() + r);
             });
             more = walk.next();
         }

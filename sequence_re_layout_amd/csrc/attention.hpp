@@ -47,8 +47,8 @@ template <> struct Of<__bf16> {
 template <> struct Of<_Float16> {
     typedef _Float16 x8 __attribute__((ext_vector_type(8)));
 };
-template <> struct Of<float> {
-    typedef float x8 __attribute__((ext_vector_type(8)));
+template <> struct Of<float> {          // read at addresses of whole 16 bytes
+    typedef float x8 __attribute__((ext_vector_type(8), aligned(16)));
 };
 template <typename T> using Vec8 = typename Of<T>::x8;
 
@@ -462,7 +462,7 @@ __device__ inline Sequence sequence_of(const AttendShape &A, uint32_t shard)
 // Whether a position of the sequence sees one of its keys.
 __device__ inline bool visible(const AttendShape &A, int position, int key)
 {
-    return (key <= position) & ((position - key < A.reach) | (key < A.firsts));
+    return key <= position && (position - key < A.reach || key < A.firsts);
 }
 
 // The keys from `first` on that a position sees, of those below `end`: offsets up

@@ -242,7 +242,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
             times(sums, down);
         } else if (more) {
             add_wild_rows<T, C, KEYS, 32>(sums, walk.keys(), walk.row0(), ds, [&](int r) {
-                return (walk.key() + r < walk.key_end()) & visible(A, col.position, walk.key() + r);
+                return walk.key() + r < walk.key_end() && visible(A, col.position, walk.key() + r);
             });
             more = walk.next();
         }
@@ -619,7 +619,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
                 break;
         }
         if (more) {
-            const auto sees = [&](int r) { return (r < walk.rows()) & visible(A, walk.position() + r, key); };
+            const auto sees = [&](int r) { return r < walk.rows() && visible(A, walk.position() + r, key); };
             add_wild_rows<T, C, ROWS, 32>(dv, walk.grads(), walk.row0(), p, sees);
             add_wild_rows<T, C, ROWS, 32>(dk, walk.queries_at(), walk.row0(), ds, sees);
             more = walk.next();
