@@ -45,11 +45,14 @@ template <typename T> constexpr float kOneWeight = kShifted<T> ? 0x1p-12f : 1.f;
 // In the gradient of q that is a column's own.  The sizes of its dO and of the first
 // values give one that hardly ever has to move: most dS are below 2^9 then, and all
 // bits are kept where P is 2^-21 and more.  It comes down where a |dS| is above 2^15,
-// so that nothing overflows.  A wave leaves the largest |dS| of its 32 columns for
-// the gradients of k and v, which take the power of a chunk's queries from them, so
-// that their largest is 2^11 to 2^12: all bits are kept down to 2^-25 of it.  (To
-// find it on the way there, too, takes more registers than there are: 1350 us
-// instead of 1120 for two sequences of 8192, 128 channels and a window of 2048.)
+// so that nothing overflows.  A wave leaves the largest |dS| and |dO| of its 32
+// columns for the gradients of k and v, which take the power of a chunk's queries
+// from them, so that their largest dS is 2^11 to 2^12: all bits are kept down to 2^-25
+// of it.  dS are computed anew there, and where dP is about delta (a row of one key)
+// they are what is left of its rounding, at most 4 (d + 2) 2^-24 times d products of
+// dO and V: the power keeps these in range, too.  (To find it on the way there
+// takes more registers than there are: 1350 us instead of 1120 for two sequences of
+// 8192, 128 channels and a window of 2048.)
 //
 // The power that takes numbers of exponent `of` to `to`, 2^60 at most.
 __device__ inline float power_for(int to, int of) { return __builtin_amdgcn_ldexpf(1.f, to - of < 60 ? to - of : 60); }
@@ -60,6 +63,18 @@ __device__ inline float largest(const f32x16 &x, float most)
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         most = fmaxf(most, fabsf(x[i]));
+    return most;
+}
+
+template <typename T, int N>
+__device__ inline float largest(const Vec8<T> (&x)[N])
+{
+    float most = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            most = fmaxf(most, fabsf(static_cast<float>(x[n][i])));
     return most;
 }
 
@@ -95,7 +110,7 @@ struct AttendGradDesc {
     const float *lse;
     char *dq, *dk, *dv;
     float *rows, *partials;         // rows: [2][lse_elems], -lse / scale (or log2(e) * -lse) and -delta
-    float *most;                    // in fp16: [pairs][units], the largest |dS| of 32 columns
+    float *most;                    // in fp16: [pairs][units][2], the largest |dS| and |dO| of 32 columns
     int64_t lse_elems;
     FastDiv by_blocks, by_items, by_sink_chunks, by_chunks, by_sink_cuts, by_cuts;
     int32_t heads;                  // of a group, that a work-group of the gradient of keys and values takes
@@ -194,17 +209,15 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
     wait_tiles();                   // for the columns, too, and on every way into the loop
     bool more = walk.next();
     float power = 1.f, most = 0.f;
+    const int64_t unit = int64_t{pair} * D.units + first / 32 + wave;
+    const bool leaves = lane == 0 && first / 32 + wave < uint32_t(D.units);
     if constexpr (kShifted<T>) {
-        const Vec8<T> some = *reinterpret_cast<const Vec8<T> *>(walk.values() + lane * 16);
-        float of_g = 0.f, of_v = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            of_v = fmaxf(of_v, fabsf(float(some[i])));
-#pragma unroll
-            for (int c = 0; c < C / 16; ++c)
-                of_g = fmaxf(of_g, fabsf(float(g[c][i])));
-        }
+        const Vec8<T> some[1] = {*reinterpret_cast<const Vec8<T> *>(walk.values() + lane * 16)};
+        float of_g = largest<T>(g), of_v = largest<T>(some);
         of_g = fmaxf(of_g, other_half(of_g));
+        const float of_all = largest_of_wave(of_g);
+        if (leaves)
+            D.most[unit * 2 + 1] = of_all;
         power = power_for(7, exponent_of(of_g) + exponent_of(more ? largest_of_wave(of_v) : 0.f));
         delta *= power;
     }
@@ -249,9 +262,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
     }
     if constexpr (kShifted<T>) {
         const float here = largest_of_wave(most / power);
-        const uint32_t unit = first / 32 + wave;
-        if (lane == 0 && unit < uint32_t(D.units))
-            D.most[int64_t{pair} * D.units + unit] = here;
+        if (leaves)
+            D.most[unit * 2] = here;
         times(sums, 1.f / power);
     }
     if (!col.exists)
@@ -481,11 +493,24 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
     walk.begin();
     float power = 1.f;
     if constexpr (kShifted<T>) {
+        float of_v;
+        if constexpr (VALUES_IN_LDS) {
+            Vec8<T> mine[C / 16];
+            load_column<T, C, DIRECT>(A, D.v + at_key, exists, mine);
+            of_v = largest<T>(mine);
+        } else {
+            of_v = largest<T>(v);
+        }
         const uint32_t units_end = end > begin ? (uint32_t(end) * A.ratio + 31) / 32 : 0;
-        float most = 0.f;
-        for (uint32_t u = uint32_t(begin) * A.ratio / 32 + lane; u < units_end; u += 64)
-            most = fmaxf(most, D.most[int64_t{pair} * D.units + u]);
-        power = power_for(11, int(scalar(uint32_t(exponent_of(largest_of_wave(most))))));
+        float most = 0.f, of_g = 0.f;
+        for (uint32_t u = uint32_t(begin) * A.ratio / 32 + lane; u < units_end; u += 64) {
+            const float *const from = D.most + (int64_t{pair} * D.units + u) * 2;
+            most = fmaxf(most, from[0]);
+            of_g = fmaxf(of_g, from[1]);
+        }
+        const int largest_ds = exponent_of(largest_of_wave(most));
+        const int rounding = exponent_of(largest_of_wave(of_g)) + exponent_of(largest_of_wave(of_v)) - 10;
+        power = power_for(11, int(scalar(uint32_t(largest_ds > rounding ? largest_ds : rounding))));
     }
     const float factor = kOneWeight<T> * power;     // from weights as they are taken to those of dS
     wait_tiles();                   // for the keys, too, and on every way into the loop

@@ -133,7 +133,7 @@ extern "C" basp_attention_plan *basp_attention_plan_create(const basp_plan *layo
     if (items > kGroups / pairs || tile_blocks > kGroups / pairs)
         return refuse(BASP_ERR_UNSUPPORTED);
     r.grad_units = r.dtype == BASP_FP16 ? int32_t(ceil_div(cols, 32)) : 0;
-    r.partials_at = ceil_div(r.lse_elems * 8 + pairs * r.grad_units * 4, 256) * 256;
+    r.partials_at = ceil_div(r.lse_elems * 8 + pairs * r.grad_units * 8, 256) * 256;
     const int64_t unfinished = (r.sink_chunks > 1 ? sink_blocks * r.sink_chunks : 0) +
                                (r.chunks > 1 ? (key_blocks - sink_blocks) * r.chunks : 0);
     r.grad_workspace_bytes = r.partials_at +

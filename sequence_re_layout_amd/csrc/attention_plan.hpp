@@ -31,7 +31,7 @@ struct basp_attention_plan {
     // a work-group takes, and such chunks of all parts
     int32_t key_blocks, sink_blocks, head_parts, sink_chunk, sink_chunks, chunk, chunks;
     int32_t grad_blocks;            // blocks of columns of a key head
-    int32_t grad_units;             // waves of them, each of which leaves a number in fp16
+    int32_t grad_units;             // waves of them, each of which leaves two numbers in fp16
     int64_t partials_at;            // in the gradient's workspace, after two numbers a row and those
     int64_t workspace_bytes, grad_workspace_bytes;
 };

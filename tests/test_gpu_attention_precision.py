@@ -341,3 +341,32 @@ def test_infinities_and_nan_of_rows_without_weight(what, dtype, d):
         exact = want[name][0]
         got = c.shaped(got.t.cpu().double(), heads, c.S)
         assert bool((torch.isfinite(got) == torch.isfinite(exact)).all()), name
+
+
+ONE_KEY = {
+    "window_1": dict(S=70, d=64, Hq=2, Hkv=1, window=1),
+    "window_1_128": dict(S=300, d=128, window=1),
+    "one_token": dict(S=1, d=64),
+    "one_token_odd": dict(B=3, S=1, d=33, Hq=3, Hkv=1),
+    "first_key_only": dict(S=200, d=64, window=1, sinks=1),
+    "sharp": dict(S=500, d=64, Hq=2, Hkv=1, sharp=300.0),
+    "sharp_128": dict(S=500, d=128, Hq=2, Hkv=1, window=70, sharp=300.0),
+}
+
+
+@pytest.mark.parametrize("size", [1.0, 1e-3, 3e3])
+@pytest.mark.parametrize("name", ONE_KEY)
+def test_rows_of_one_weight_in_fp16(name, size):
+    """Rows whose weight is all on one key: dS is 0 but for the rounding of dP and
+    delta, which is another one in the two kernels."""
+    of = dict(ONE_KEY[name])
+    sharp = of.pop("sharp", 1.0)
+    if sharp > 1.0:
+        size = min(size, 1.0)       # dk is beyond fp16 else
+    c = lc.Attention(dtype="fp16", **of)
+    q, k, v, do = c.inputs(3, sharp)
+    do = (do * size).half().double()
+    call = Call(c, q, k, v, do)
+    call.forward()
+    call.backward()
+    call.check(c.exact(q, k, v, do, [0] * c.B, [c.S] * c.B, call.scale))
