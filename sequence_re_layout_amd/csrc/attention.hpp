@@ -711,14 +711,22 @@ __device__ inline void wave_order()
 // large one (a sink) count for as much as the large one.
 template <typename T> constexpr bool kShifted = std::is_same<T, _Float16>::value;
 
-// What is taken from the exponents (to the base of 2) of a column with maximum m.
-// Where weights are shifted, it is no less than the exponent of m, 7 (8, where 7 is
-// between two fp32 numbers) aside: the largest weight stays below 2^16 at any score.
+// The exponent (to the base of 2) of a column's maximum m; where weights are shifted,
+// it is rounded up.
+template <typename T>
+__device__ inline float top_exponent(float m, const AttendShape &A)
+{
+    const float top = m == -INFINITY ? 0.f : m * A.scale_log2;
+    return kShifted<T> ? fmaf(fabsf(top), 0x1p-23f, top) : top;
+}
+
+// What is taken from the exponents of the column, so that the largest weight is 1, or
+// where they are shifted 2^7 (2^8, where 7 is between two fp32 numbers) or less: it
+// stays below 2^16 at any score.
 template <typename T>
 __device__ inline float weight_base(float m, const AttendShape &A)
 {
-    const float base = m == -INFINITY ? 0.f : m * A.scale_log2;
-    return kShifted<T> ? fmaf(fabsf(base), 0x1p-23f, base) - 7.f : base;
+    return kShifted<T> ? top_exponent<T>(m, A) - 7.f : top_exponent<T>(m, A);
 }
 
 // lse from a maximum in the scores' units and the sum relative to it (to 0 where
@@ -727,7 +735,7 @@ __device__ inline float weight_base(float m, const AttendShape &A)
 template <typename T>
 __device__ inline float log_sum(float m, float l, const AttendShape &A)
 {
-    return (weight_base<T>(m, A) + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    return (top_exponent<T>(m, A) + __builtin_amdgcn_logf(kShifted<T> ? l * 0x1p-7f : l)) * 0.6931471805599453f;
 }
 
 // Four channels of a result's rows as stored.

@@ -370,3 +370,18 @@ def test_rows_of_one_weight_in_fp16(name, size):
     call.forward()
     call.backward()
     call.check(c.exact(q, k, v, do, [0] * c.B, [c.S] * c.B, call.scale))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("of", [dict(S=64), dict(S=2048, queries=2), dict(S=1500, Hq=4, Hkv=4)])
+def test_lse_of_equal_scores(dtype, of):
+    """log(n) to its last bits: the logarithm to the base of 2 is off by a step of its
+    size, the product with log(2) and that constant by half a step each."""
+    c = lc.Attention(d=64, dtype=dtype, **of)
+    q, k, v, do = c.inputs(0)
+    call = Call(c, torch.zeros_like(q), k, v, do)
+    call.forward()
+    torch.cuda.synchronize()
+    want = torch.log((c.S - c.queries + 1 + torch.arange(c.queries)).double())
+    got = call.lse.t.view(c.hq, c.queries).cpu().double()
+    assert bool(((got - want).abs() <= 4 * lc.U * want).all()), float(((got - want).abs() / want.clamp(1e-9)).max())
