@@ -637,7 +637,8 @@ basp_status basp_embed_to_seq_grad(const basp_embed_plan *plan, const void *ids,
  * and none at all if p lies outside [0, lengths[b]).  Over the keys it sees
  *     o = sum_j P_j v_j,  P = softmax(scale <q, k_j>),  lse = log sum_j exp(scale <q, k_j>).
  * A row that sees nothing gets zeros and lse = -infinity, and has no part in any
- * gradient.  Query head h reads the key and value head h / (Hq / Hkv).
+ * gradient (a row that sees a score of NaN has NaN in both).  Query head h reads
+ * the key and value head h / (Hq / Hkv).
  *   training   queries = S, starts NULL (0); padded batches by lengths
  *   serving    queries = the new tokens, starts[b] = lengths[b] - queries, their
  *              keys and values already in the cache
@@ -708,7 +709,9 @@ basp_status basp_attention_grad(const basp_attention_plan *plan, const void *q, 
 /*
  * Layer norm of T rows of D channels:
  *   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(variance + eps)
- * with the row's mean and variance (of D, not D - 1).
+ * with the row's mean and variance (of D, not D - 1).  Both are fp32: a row whose
+ * squared deviations sum to more than fp32 holds (numbers beyond 10^19 / sqrt(D))
+ * has rstd = 0.
  */
 typedef struct basp_norm_plan basp_norm_plan;
 

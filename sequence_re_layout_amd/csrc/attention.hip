@@ -291,7 +291,7 @@ struct StepWalk {
 // tiles of 32 keys in turn, each wave through LDS of its own, and join their
 // sums.  For a few queries against long sequences: bound by reading the keys, so
 // that waves fetch for themselves and wait for no one: 4 sequences of 65536 of a
-// cache of 128 channels in fp16, 142 to 151 us, 5.1 to 5.4 TB/s; 16 sequences of
+// cache of 128 channels in fp16, 130 to 157 us, 4.9 to 6 TB/s; 16 sequences of
 // 4096, 1024 in sight, 64 channels in bf16, 13 us, of which reading takes 5 and
 // the rest is the chain of lengths, queries, first tile and exchange.
 template <typename T, int C, bool DIRECT>
