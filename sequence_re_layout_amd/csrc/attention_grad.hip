@@ -43,16 +43,16 @@ template <typename T> constexpr float kOneWeight = kShifted<T> ? 0x1p-12f : 1.f;
 // dS may have any size next to dout: P is small where a row sees many keys.  In
 // fp16 it is rounded times a power of two, which the sums are freed of at the end.
 // In the gradient of q that is a column's own.  The sizes of its dO and of the first
-// values give one that hardly ever has to move: most dS are below 2^9 then, and all
-// bits are kept where P is 2^-21 and more.  It comes down where a |dS| is above 2^15,
-// so that nothing overflows.  A wave leaves the largest |dS| and |dO| of its 32
-// columns for the gradients of k and v, which take the power of a chunk's queries
-// from them, so that their largest dS is 2^11 to 2^12: all bits are kept down to 2^-25
-// of it.  dS are computed anew there, and where dP is about delta (a row of one key)
-// they are what is left of its rounding, at most 4 (d + 2) 2^-24 times d products of
-// dO and V: the power keeps these in range, too.  (To find it on the way there
-// takes more registers than there are: 1350 us instead of 1120 for two sequences of
-// 8192, 128 channels and a window of 2048.)
+// values give one, no less than 1, that hardly ever has to move: all bits are kept
+// where P is 2^-22 and more.  It comes down where a |dS| is above 2^15, so that
+// nothing overflows.  A wave leaves the largest |dS| and |dO| of its 32 columns for
+// the gradients of k and v, which take the power of a chunk's queries from them, so
+// that their largest dS is 2^14 to 2^15: all bits are kept down to 2^-28 of it.  dS
+// are computed anew there, and where dP is about delta (a row of one key) they are
+// what is left of its rounding, at most 4 (d + 2) 2^-24 times d products of dO and V:
+// the power keeps these in range, too.  (To find it on the way there takes more
+// registers than there are: 1350 us instead of 1120 for two sequences of 8192, 128
+// channels and a window of 2048.)
 //
 // The power that takes numbers of exponent `of` to `to`, 2^60 at most.
 __device__ inline float power_for(int to, int of) { return __builtin_amdgcn_ldexpf(1.f, to - of < 60 ? to - of : 60); }
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
         const float of_all = largest_of_wave(of_g);
         if (leaves)
             D.most[unit * 2 + 1] = of_all;
-        power = power_for(7, exponent_of(of_g) + exponent_of(more ? largest_of_wave(of_v) : 0.f));
+        power = fmaxf(1.f, power_for(8, exponent_of(of_g) + exponent_of(more ? largest_of_wave(of_v) : 0.f)));
         delta *= power;
     }
     while (more) {
@@ -509,8 +509,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 || C <= 64 ? 2 : 1) void a
             of_g = fmaxf(of_g, from[1]);
         }
         const int largest_ds = exponent_of(largest_of_wave(most));
-        const int rounding = exponent_of(largest_of_wave(of_g)) + exponent_of(largest_of_wave(of_v)) - 10;
-        power = power_for(11, int(scalar(uint32_t(largest_ds > rounding ? largest_ds : rounding))));
+        const int rounding = exponent_of(largest_of_wave(of_g)) + exponent_of(largest_of_wave(of_v)) - 7;
+        power = power_for(14, int(scalar(uint32_t(largest_ds > rounding ? largest_ds : rounding))));
     }
     const float factor = kOneWeight<T> * power;     // from weights as they are taken to those of dS
     wait_tiles();                   // for the keys, too, and on every way into the loop

@@ -385,3 +385,17 @@ def test_lse_of_equal_scores(dtype, of):
     want = torch.log((c.S - c.queries + 1 + torch.arange(c.queries)).double())
     got = call.lse.t.view(c.hq, c.queries).cpu().double()
     assert bool(((got - want).abs() <= 4 * lc.U * want).all()), float(((got - want).abs() / want.clamp(1e-9)).max())
+
+
+@pytest.mark.parametrize("of,sharp,values,size", [(dict(d=64), 12.0, 64.0, 16.0), (dict(d=64), 12.0, 128.0, 8.0), (dict(d=96), 8.0, 64.0, 16.0),
+                                                  (dict(d=128, Hq=2), 8.0, 128.0, 16.0)])
+def test_small_ds_beside_large_ones(of, sharp, values, size):
+    """dS of thousands, which need no power of two: small ones beside them are off by
+    no more than fp16's rounding of them as they are."""
+    c = lc.Attention(B=2, S=257, window=17, dtype="fp16", **of)
+    q, k, v, do = c.inputs(182, sharp)
+    v, do = v * values, do * size
+    call = Call(c, q, k, v, do)
+    call.forward()
+    call.backward()
+    call.check(c.exact(q, k, v, do, [0, 0], [c.S] * 2, call.scale))
