@@ -399,3 +399,21 @@ def test_small_ds_beside_large_ones(of, sharp, values, size):
     call.forward()
     call.backward()
     call.check(c.exact(q, k, v, do, [0, 0], [c.S] * 2, call.scale))
+
+
+@pytest.mark.parametrize("of,lengths", [(dict(S=700, d=64, Hq=4, window=100, sinks=130), None), (dict(S=300, d=128, Hq=8, window=60), None),
+                                        (dict(B=5, S=100, d=64, Hq=6, window=30, sinks=2), [100, 1, 0, 57, 99]),
+                                        (dict(S=500, d=40, Hq=3, queries=70), None), (dict(S=129, d=33, order="token"), [77])])
+def test_same_bits_whatever_the_workspace_holds(of, lengths):
+    c = lc.Attention(dtype="fp16", **{"Hkv": 1, **of})
+    q, k, v, do = c.inputs(9)
+    runs = []
+    for fill in (0, 255, 0x7e, 0xfe, 1):
+        call = Call(c, q, k, v, do, None, lengths)
+        call.ws.fill_(fill)
+        call.gws.fill_(fill)
+        call.forward()
+        call.backward()
+        torch.cuda.synchronize()
+        runs.append([g.t.clone() for g in call.outputs()])
+    assert all(torch.equal(x, y) for run in runs[1:] for x, y in zip(runs[0], run))
